@@ -2,7 +2,7 @@
 
 Every function here checks the torch tensors it is given (dtype, device,
 contiguity, shape), passes raw pointers and sizes to the C ABI declared in
-``include/boost_block.h`` and raises ``BoostError`` on a non-OK status. No
+``include/boost_block.h`` and ``include/boost_ops.h`` and raises ``BoostError`` on a non-OK status. No
 arithmetic of the block happens in Python; there is no CPU fallback: if the
 library is missing, ``lib()`` raises.
 """
@@ -35,6 +35,7 @@ EXPORTS = (
     "boost_profile_read_kernels", "boost_block_fwd_swiglu", "boost_block_fwd_btp",
     "boost_block_up", "boost_debug_count_writes", "boost_debug_count_log",
     "boost_profile_only", "boost_block_fwd_residual", "boost_block_bwd_residual",
+    "boost_rope", "boost_dropout",
 )
 
 
@@ -50,6 +51,18 @@ class Desc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int64), ("r", ctypes.c_int64),
                 ("k", ctypes.c_int64), ("n", ctypes.c_int64), ("S", ctypes.c_int32),
                 ("eps", ctypes.c_float), ("act", ctypes.c_int32), ("has_norm", ctypes.c_int32)]
+
+
+ROPE_MAX_DIM = 512
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64)] + \
+        [(f, ctypes.c_int32) for f in ("hq", "hk", "dim", "rot", "axes", "interleaved", "inverse",
+                                       "pos64")] + \
+        [(f, ctypes.c_int64) for f in ("q_ts", "q_hs", "k_ts", "k_hs", "qo_ts", "qo_hs", "ko_ts",
+                                       "ko_hs")] + \
+        [("axis", ctypes.c_uint8 * (ROPE_MAX_DIM // 2))]
 
 
 def lib_path() -> str:
@@ -86,6 +99,9 @@ def lib():
     L.boost_block_layout.argtypes = [dp, ctypes.POINTER(i64), ctypes.POINTER(i64),
                                      ctypes.POINTER(i64)]
     L.boost_block_check.argtypes = [vp, vp]
+    L.boost_rope.argtypes = [ctypes.POINTER(RopeDesc), vp, vp, vp, vp, vp, vp, vp]
+    L.boost_dropout.argtypes = [i64, vp, vp, vp, ctypes.c_double, ctypes.c_uint64,
+                                ctypes.c_uint64, vp, vp]
     L.boost_status_string.argtypes = [ctypes.c_int]
     L.boost_status_string.restype = ctypes.c_char_p
     L.boost_swiglu_fwd.argtypes = [i64, i64, vp, vp, vp, vp]
@@ -426,6 +442,121 @@ def add(a, b, out=None, stream=None):
         out = torch.empty_like(a)
     _check(lib().boost_add(a.numel(), _ptr(a), _ptr(b), _ptr(out), _stream(stream)), "boost_add")
     return out
+
+
+def _here(tensors, dtype=None):
+    """Check tensors of one call: on the current device (the stream and the workspace are
+    its), and of one type where given."""
+    device = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_cuda or t.device.index != device:
+            raise ValueError(f"{name} must be on the current CUDA device {device}, not {t.device}")
+
+
+def _heads(t, name, T=None, dim=None):
+    """Token and head strides of a [T, heads, dim] tensor whose values are adjacent."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [T, heads, dim] with adjacent values")
+    if (T is not None and t.shape[0] != T) or (dim is not None and t.shape[2] != dim):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected T={T}, dim={dim}")
+    # the stride of a single token or head says nothing: a plain one in its place
+    return (t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2],
+            t.stride(1) if t.shape[1] > 1 else t.shape[2])
+
+
+def rope(q, k, positions, inv_freq, *, sections=None, pair_axis=None, interleaved=False,
+         inverse=False, q_out=None, k_out=None, stream=None):
+    """Rotary positions of q [T, hq, dim] and k [T, hk, dim] (k may be None): returns
+    (q_out, k_out). ``inverse`` takes the gradients of the rotated q and k back.
+
+    positions: [T] or [axes, T], int32 or int64. inv_freq: float64 [rot / 2], radians per
+    position; the first rot values of each head turn. ``sections``: how many pairs turn with
+    each axis, in order (default: all with the first); ``pair_axis``: the axis of each pair
+    instead. q, k and the outputs take any token and head strides (multiples of 8), so slices
+    of a packed projection and [heads, T, dim] tensors seen as [T, heads, dim] are fine, and
+    q_out may be q (in place). Positions and frequencies are contiguous."""
+    bf = torch.bfloat16
+    if q.dim() != 3:
+        raise ValueError("q must be [T, heads, dim]")
+    T, hq, dim = q.shape
+    q_out = torch.empty(q.shape, dtype=bf, device=q.device) if q_out is None else q_out
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+    elif k_out is None:
+        k_out = torch.empty(k.shape, dtype=bf, device=k.device)
+    _here({"q": q, "k": k, "q_out": q_out, "k_out": k_out}, bf)
+    _here({"positions": positions, "inv_freq": inv_freq})
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise TypeError("inv_freq must be a float64 vector")
+    if not positions.is_contiguous() or not inv_freq.is_contiguous():
+        raise ValueError("positions and inv_freq must be contiguous")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.dim() not in (1, 2) or positions.shape[-1] != T:
+        raise ValueError(f"positions has shape {tuple(positions.shape)}, expected [T] or [axes, T]")
+    pairs = inv_freq.numel()
+    if 2 * pairs > ROPE_MAX_DIM:
+        raise BoostError(2, "boost_rope")
+    D = RopeDesc(T=T, hq=hq, hk=0 if k is None else k.shape[1], dim=dim, rot=2 * pairs, axes=axes,
+                 interleaved=bool(interleaved), inverse=bool(inverse),
+                 pos64=positions.dtype == torch.int64)
+    D.q_ts, D.q_hs = _heads(q, "q")
+    D.qo_ts, D.qo_hs = _heads(q_out, "q_out", T, dim)
+    if q_out.shape != q.shape:
+        raise ValueError(f"q_out has shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
+    if k is not None:
+        D.k_ts, D.k_hs = _heads(k, "k", T, dim)
+        D.ko_ts, D.ko_hs = _heads(k_out, "k_out", T, dim)
+        if k_out.shape != k.shape:
+            raise ValueError(f"k_out has shape {tuple(k_out.shape)}, expected {tuple(k.shape)}")
+    if pair_axis is not None:
+        if sections is not None:
+            raise ValueError("sections and pair_axis exclude each other")
+        if len(pair_axis) != pairs or not all(0 <= a < axes for a in pair_axis):
+            raise ValueError(f"pair_axis must give one of {axes} axes for each of {pairs} pairs")
+        D.axis[:pairs] = list(pair_axis)
+    elif sections is not None:
+        if len(sections) != axes or min(sections) < 0 or sum(sections) != pairs:
+            raise ValueError(f"sections must share {pairs} pairs among {axes} axes")
+        D.axis[:pairs] = [a for a, n in enumerate(sections) for _ in range(n)]
+    _check(lib().boost_rope(ctypes.byref(D), _ptr(q), _ptr(k), _ptr(positions), _ptr(inv_freq),
+                            _ptr(q_out), _ptr(k_out), _stream(stream)), "boost_rope")
+    return q_out, k_out
+
+
+def dropout_add(x, p, seed, offset=0, *, residual=None, out=None, counter=None, stream=None):
+    """residual + dropout(x): the element at flat index e is kept by a pure function of (e,
+    seed, offset), so no mask is stored (``boost_dropout``). ``counter``: an int64 tensor of
+    one value, added to the offset when the kernel runs, for replayed graphs."""
+    bf = torch.bfloat16
+    if out is None:
+        out = torch.empty(x.shape, dtype=bf, device=x.device)
+    _here({"x": x, "residual": residual, "out": out, "counter": counter})
+    _need(x, "x", bf)
+    _need(out, "out", bf, x.shape)
+    if residual is not None:
+        _need(residual, "residual", bf, x.shape)
+    if counter is not None:
+        _need(counter, "counter", torch.int64)
+        if counter.numel() != 1:
+            raise ValueError("counter must hold one value")
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError("seed and offset must be unsigned 64-bit values")
+    _check(lib().boost_dropout(x.numel(), _ptr(x), _ptr(residual), _ptr(out), p, seed, offset,
+                               _ptr(counter), _stream(stream)), "boost_dropout")
+    return out
+
+
+def dropout_bwd(dout, p, seed, offset=0, *, dx=None, counter=None, stream=None):
+    """Gradient of x of ``dropout_add`` with the same p, seed and offset (the residual's
+    gradient is dout itself)."""
+    return dropout_add(dout, p, seed, offset, out=dx, counter=counter, stream=stream)
 
 
 def check(ws: Workspace, stream=None):

@@ -28,6 +28,8 @@ enum KernelId : int {
   K_BTP_PARTIAL,
   K_BTP_REDUCE,
   K_STATS_FOLD,
+  K_ROPE,
+  K_DROPOUT,
   K_COUNT
 };
 

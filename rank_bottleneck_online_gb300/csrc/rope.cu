@@ -1,0 +1,312 @@
+// rope.cu -- rotary positions of q and k with one or more position axes, and their inverse.
+//
+// Per token and pair one angle serves every head, so a block first forms the cosines and
+// sines of its tokens in shared memory (one (token, pair) a thread) and then streams the
+// heads through 16-byte vectors. The pass is bound by HBM: 4 bytes of traffic a value and
+// 3 fp32 operations.
+//
+// The angle: phi = p w with p a 64-bit integer and w an fp64 frequency. In turns,
+// p w / (2 pi) mod 1 is wanted. F = floor(2^64 w / (2 pi)) mod 2^64 holds the frequency as a
+// 64-bit fixed-point fraction of a turn, and p F mod 2^64, the integer product's own wrap,
+// is the fraction of a turn to 2^-63 |p|, whatever the size of p. Its upper 32 bits go to
+// sincospif. No fp64 arithmetic is used (its rate is a 60th of fp32's here).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "boost_ops.h"
+#include "internal.h"
+#include "profile.h"
+#include "simple.cuh"
+
+namespace boost_gb300 {
+
+namespace {
+
+constexpr int kMaxAngles = 2048;   // (token, pair) angles of one block: 16 KB of shared memory
+
+struct RopeParams {
+  const __nv_bfloat16 *q, *k;
+  __nv_bfloat16 *qo, *ko;
+  const void* positions;
+  const double* inv_freq;
+  boost_rope_desc d;
+  int tok;                         // tokens of one block
+};
+
+// 2^64 w / (2 pi) mod 2^64, from the bits of w (finite).
+__device__ __forceinline__ uint64_t turns_fixed(double w) {
+  constexpr uint64_t kInvTwoPi = 0x28be60db9391054aull;   // 2^64 / (2 pi)
+  const uint64_t b = __double_as_longlong(w);
+  const int e = static_cast<int>((b >> 52) & 0x7ff);
+  if (e == 0) return 0;            // zero and subnormals: no angle for any 64-bit position
+  const uint64_t m = (b & 0xfffffffffffffull) | (1ull << 52);
+  const uint64_t hi = __umul64hi(m, kInvTwoPi), lo = m * kInvTwoPi;
+  const int sh = 52 - (e - 1023);  // w = m 2^-sh
+  uint64_t f;
+  if (sh <= 0) f = sh > -64 ? lo << -sh : 0;
+  else if (sh < 64) f = (hi << (64 - sh)) | (lo >> sh);
+  else f = sh < 128 ? hi >> (sh - 64) : 0;
+  return (b >> 63) ? 0 - f : f;
+}
+
+// Where the pairs lie: kHalf8 and kHalf4 pair i with i + rot / 2 (vectors of 8 or 4 values
+// of each half), kAdjacent pairs 2 i with 2 i + 1 (a vector of 8 holds 4 pairs).
+enum Pairing { kHalf8, kHalf4, kAdjacent };
+
+// The part of one head that a thread turns at a time: a vector of each half, or one vector
+// of adjacent pairs, as words of two bf16 values.
+template <Pairing P>
+struct Unit {
+  static constexpr int kPairs = P == kHalf8 ? 8 : 4;
+  uint32_t w[kPairs];
+
+  __device__ __forceinline__ void load(const __nv_bfloat16* h, int u, int half) {
+    if constexpr (P == kHalf8) {
+      const uint4 a = *reinterpret_cast<const uint4*>(h + 8 * u);
+      const uint4 b = *reinterpret_cast<const uint4*>(h + half + 8 * u);
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    } else if constexpr (P == kHalf4) {
+      const uint2 a = *reinterpret_cast<const uint2*>(h + 4 * u);
+      const uint2 b = *reinterpret_cast<const uint2*>(h + half + 4 * u);
+      w[0] = a.x; w[1] = a.y; w[2] = b.x; w[3] = b.y;
+    } else {
+      const uint4 a = *reinterpret_cast<const uint4*>(h + 8 * u);
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    }
+  }
+
+  __device__ __forceinline__ void turn(const float* c, const float* s) {
+    if constexpr (P == kAdjacent) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = bf16_lo(w[i]), b = bf16_hi(w[i]);
+        w[i] = pack_bf16x2(a * c[i] - b * s[i], b * c[i] + a * s[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPairs / 2; ++i) {
+        const uint32_t x = w[i], y = w[kPairs / 2 + i];
+        const float a0 = bf16_lo(x), a1 = bf16_hi(x), b0 = bf16_lo(y), b1 = bf16_hi(y);
+        w[i] = pack_bf16x2(a0 * c[2 * i] - b0 * s[2 * i], a1 * c[2 * i + 1] - b1 * s[2 * i + 1]);
+        w[kPairs / 2 + i] =
+            pack_bf16x2(b0 * c[2 * i] + a0 * s[2 * i], b1 * c[2 * i + 1] + a1 * s[2 * i + 1]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void store(__nv_bfloat16* h, int u, int half) const {
+    if constexpr (P == kHalf8) {
+      *reinterpret_cast<uint4*>(h + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(h + half + 8 * u) = make_uint4(w[4], w[5], w[6], w[7]);
+    } else if constexpr (P == kHalf4) {
+      *reinterpret_cast<uint2*>(h + 4 * u) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(h + half + 4 * u) = make_uint2(w[2], w[3]);
+    } else {
+      *reinterpret_cast<uint4*>(h + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+};
+
+// Head `h` of token `t`: query heads first.
+__device__ __forceinline__ const __nv_bfloat16* head_in(const RopeParams& p, int64_t t, int h) {
+  return h < p.d.hq ? p.q + t * p.d.q_ts + h * p.d.q_hs
+                    : p.k + t * p.d.k_ts + (h - p.d.hq) * p.d.k_hs;
+}
+__device__ __forceinline__ __nv_bfloat16* head_out(const RopeParams& p, int64_t t, int h) {
+  return h < p.d.hq ? p.qo + t * p.d.qo_ts + h * p.d.qo_hs
+                    : p.ko + t * p.d.ko_ts + (h - p.d.hq) * p.d.ko_hs;
+}
+
+template <Pairing P>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+  pdl_enter();
+  __shared__ __align__(16) float cs[kMaxAngles], sn[kMaxAngles];
+  const int pairs = p.d.rot / 2;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.tok;
+  const int tokens = static_cast<int>(min(static_cast<int64_t>(p.tok), p.d.T - t0));
+  for (int a = threadIdx.x; a < tokens * pairs; a += kThreads) {
+    const int t = a / pairs, i = a - t * pairs;
+    const int64_t at = p.d.axis[i] * p.d.T + t0 + t;
+    const int64_t pos = p.d.pos64 ? static_cast<const int64_t*>(p.positions)[at]
+                                  : static_cast<const int32_t*>(p.positions)[at];
+    const double w = p.inv_freq[i];
+    const uint64_t phase = turns_fixed(w) * static_cast<uint64_t>(pos);
+    // half turns in [-1, 1): the phase's upper 32 bits as a signed fraction
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &s, &c);
+    if (!isfinite(w)) s = c = nanf("");
+    cs[a] = c;
+    sn[a] = p.d.inverse ? -s : s;
+  }
+  __syncthreads();
+
+  const int heads = p.d.hq + p.d.hk;
+  const int units = pairs / Unit<P>::kPairs;            // of one head
+  const int items = tokens * heads * units;
+  constexpr int kBatch = P == kHalf8 ? 2 : 4;           // units in flight a thread
+  for (int first = threadIdx.x; first < items; first += kBatch * kThreads) {
+    Unit<P> v[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int item = first + b * kThreads;
+      if (item < items) {
+        const int th = item / units, t = th / heads;
+        v[b].load(head_in(p, t0 + t, th - t * heads), item - th * units, pairs);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int item = first + b * kThreads;
+      if (item < items) {
+        const int th = item / units, t = th / heads, u = item - th * units;
+        const int at = t * pairs + u * Unit<P>::kPairs;
+        float c[Unit<P>::kPairs], s[Unit<P>::kPairs];
+#pragma unroll
+        for (int i = 0; i < Unit<P>::kPairs; i += 4) {
+          *reinterpret_cast<float4*>(c + i) = *reinterpret_cast<const float4*>(cs + at + i);
+          *reinterpret_cast<float4*>(s + i) = *reinterpret_cast<const float4*>(sn + at + i);
+        }
+        v[b].turn(c, s);
+        v[b].store(head_out(p, t0 + t, th - t * heads), u, pairs);
+      }
+    }
+  }
+
+  // values that do not turn
+  const int rest = (p.d.dim - p.d.rot) / 8;
+  for (int item = threadIdx.x; item < tokens * heads * rest; item += kThreads) {
+    const int th = item / rest, t = th / heads, h = th - t * heads;
+    const int at = p.d.rot + 8 * (item - th * rest);
+    const __nv_bfloat16* src = head_in(p, t0 + t, h);
+    __nv_bfloat16* dst = head_out(p, t0 + t, h);
+    if (src != dst)
+      *reinterpret_cast<uint4*>(dst + at) = *reinterpret_cast<const uint4*>(src + at);
+  }
+}
+
+cudaError_t launch_rope(const RopeParams& p_in, cudaStream_t stream) {
+  RopeParams p = p_in;
+  const int pairs = p.d.rot / 2;
+  const bool adjacent = p.d.interleaved != 0, wide = !adjacent && pairs % 8 == 0;
+  // Tokens of one block: enough that each thread has a batch of units (so that the sine
+  // phase of one block hides behind the loads of the others), and no more.
+  const int64_t units = static_cast<int64_t>(p.d.hq + p.d.hk) * pairs / (wide ? 8 : 4);
+  int64_t tok = std::max<int64_t>(1, kThreads * (wide ? 2 : 4) / units);
+  tok = std::min<int64_t>({tok, kMaxAngles / pairs, std::max<int64_t>(1, p.d.T / 304)});
+  p.tok = static_cast<int>(tok);
+  const int64_t grid = (p.d.T + tok - 1) / tok;
+  if (adjacent) return launch_k(rope_kernel<kAdjacent>, grid, stream, p);
+  if (wide) return launch_k(rope_kernel<kHalf8>, grid, stream, p);
+  return launch_k(rope_kernel<kHalf4>, grid, stream, p);
+}
+
+// ------------------------------------------------------------------ host checks
+// One [T, heads, dim] operand as it lies in memory (strides in elements).
+struct Slice {
+  uintptr_t base;
+  int64_t T, heads, dim, ts, hs;
+  // bytes from the first to behind the last element
+  uint64_t extent() const {
+    return T * heads == 0 ? 0 : 2ull * ((T - 1) * ts + (heads - 1) * hs + dim);
+  }
+  bool same(const Slice& o) const {
+    return base == o.base && heads == o.heads && (T == 1 || ts == o.ts) &&
+           (heads == 1 || hs == o.hs);
+  }
+  // no two elements coincide: tokens apart by more than a token's heads, or heads by more
+  // than a head's tokens
+  bool one_to_one() const {
+    const int64_t token = (heads - 1) * hs + dim, head = (T - 1) * ts + dim;
+    return (heads == 1 || hs >= dim) && (T == 1 || ts >= dim) &&
+           (T == 1 || heads == 1 || ts >= token || hs >= head);
+  }
+};
+
+// Whether two operands share no element: disjoint ranges, or heads side by side in the rows
+// of one packed buffer (the same token stride, and spans that do not meet modulo it).
+bool disjoint(const Slice& a, const Slice& b) {
+  if (a.extent() == 0 || b.extent() == 0) return true;
+  if (a.base + a.extent() <= b.base || b.base + b.extent() <= a.base) return true;
+  if (a.T == 1 || a.ts != b.ts || a.ts == 0) return false;
+  const int64_t sa = 2 * ((a.heads - 1) * a.hs + a.dim), sb = 2 * ((b.heads - 1) * b.hs + b.dim);
+  const int64_t row = 2 * a.ts;
+  // where b's span begins within a's rows
+  const int64_t away = static_cast<int64_t>(b.base) - static_cast<int64_t>(a.base);
+  const int64_t o = (away % row + row) % row;
+  return o >= sa && o + sb <= row;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+
+}  // namespace boost_gb300
+
+using namespace boost_gb300;
+
+extern "C" boost_status boost_rope(const boost_rope_desc* desc, const void* q, const void* k,
+                                   const void* positions, const double* inv_freq, void* q_out,
+                                   void* k_out, void* stream) {
+  if (desc == nullptr) return BOOST_ERR_INVALID_ARG;
+  const boost_rope_desc& D = *desc;
+  if (D.T < 0 || D.hq < 1 || D.hk < 0 || D.dim < 1 || D.rot < 1 || D.rot > D.dim || D.axes < 1 ||
+      D.axes > BOOST_ROPE_MAX_AXES)
+    return BOOST_ERR_INVALID_ARG;
+  if ((D.interleaved | D.inverse | D.pos64) & ~1) return BOOST_ERR_INVALID_ARG;
+  if (D.dim % 8 || D.rot % 8 || D.dim > BOOST_ROPE_MAX_DIM) return BOOST_ERR_UNSUPPORTED_SHAPE;
+  // the grid and a block's heads x pairs stay within 31 bits; offsets take 64
+  if (D.T > 0x7fffffff || D.hq > 65536 || D.hk > 65536) return BOOST_ERR_UNSUPPORTED_SHAPE;
+  for (int i = 0; i < D.rot / 2; ++i)
+    if (D.axis[i] >= D.axes) return BOOST_ERR_INVALID_ARG;
+  const int64_t strides[8] = {D.q_ts, D.q_hs, D.k_ts, D.k_hs, D.qo_ts, D.qo_hs, D.ko_ts, D.ko_hs};
+  for (int i = 0; i < 8; ++i) {
+    if (D.hk == 0 && (i & 2)) continue;
+    if (strides[i] < 0) return BOOST_ERR_INVALID_ARG;
+    if (strides[i] % 8) return BOOST_ERR_UNSUPPORTED_SHAPE;
+    // (every offset below 2^50 elements, so that sums of them fit)
+    const double n = i % 2 == 0 ? static_cast<double>(D.T) : (i & 2) ? D.hk : D.hq;
+    if (n * static_cast<double>(strides[i]) > 0x1p50) return BOOST_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (D.hk == 0 && (k != nullptr || k_out != nullptr)) return BOOST_ERR_INVALID_ARG;
+  if (D.T == 0) return BOOST_OK;
+  if (q == nullptr || positions == nullptr || inv_freq == nullptr || q_out == nullptr)
+    return BOOST_ERR_INVALID_ARG;
+  if (D.hk > 0 && (k == nullptr || k_out == nullptr)) return BOOST_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) ||
+      !aligned16(positions) || !aligned16(inv_freq))
+    return BOOST_ERR_ALIGNMENT;
+  auto slice = [&](const void* ptr, int64_t heads, int64_t ts, int64_t hs) {
+    return Slice{reinterpret_cast<uintptr_t>(ptr), D.T, heads, D.dim, ts, hs};
+  };
+  const Slice sq = slice(q, D.hq, D.q_ts, D.q_hs), sk = slice(k, D.hk, D.k_ts, D.k_hs);
+  const Slice qo = slice(q_out, D.hq, D.qo_ts, D.qo_hs), ko = slice(k_out, D.hk, D.ko_ts, D.ko_hs);
+  if (!qo.one_to_one() || (D.hk > 0 && !ko.one_to_one())) return BOOST_ERR_INVALID_ARG;
+  if (!(sq.same(qo) || disjoint(sq, qo)) || !(sk.same(ko) || disjoint(sk, ko)) ||
+      !disjoint(sq, ko) || !disjoint(sk, qo) || !disjoint(qo, ko))
+    return BOOST_ERR_INVALID_ARG;
+  // positions and frequencies are read while the outputs are written: nothing shared there
+  const uint64_t pos_bytes = (D.pos64 ? 8ull : 4ull) * D.axes * D.T, freq_bytes = 4ull * D.rot;
+  auto meets = [](const Slice& o, const void* in, uint64_t bytes) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(in);
+    return o.extent() > 0 && b < o.base + o.extent() && o.base < b + bytes;
+  };
+  if (meets(qo, positions, pos_bytes) || meets(ko, positions, pos_bytes) ||
+      meets(qo, inv_freq, freq_bytes) || meets(ko, inv_freq, freq_bytes))
+    return BOOST_ERR_INVALID_ARG;
+
+  RopeParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.qo = static_cast<__nv_bfloat16*>(q_out);
+  p.ko = static_cast<__nv_bfloat16*>(k_out);
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.d = D;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const double values = static_cast<double>(D.T) * (D.hq + D.hk) * D.dim;
+  ProfScope ps(s, K_ROPE, 0.0, 4.0 * values + static_cast<double>(pos_bytes));
+  return launch_rope(p, s) == cudaSuccess ? BOOST_OK : BOOST_ERR_CUDA;
+}
