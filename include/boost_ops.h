@@ -93,6 +93,75 @@ boost_status boost_rope(const boost_rope_desc* desc, const void* q, const void* 
 boost_status boost_dropout(int64_t count, const void* x, const void* res, void* out, double p,
                            uint64_t seed, uint64_t offset, const uint64_t* counter, void* stream);
 
+/* ------------------------------------------------- 8-bit floating-point operands
+ *
+ * An operand is a matrix [rows, K] of e4m3 or e5m2 values (K contracted) with one
+ * power-of-two scale for each block of 128 along K: value = q * 2^(byte - 127).
+ *   values  [G, rows, pitch] bytes, pitch a multiple of 16, >= K
+ *   scales  [G] planes of boost_fp8_scale_bytes(rows, K) bytes: tiles of 128 rows x 4
+ *           blocks, the byte of row r, block b at
+ *           ((r / 128) * ceil(blocks / 4) + b / 4) * 512 + (r % 32) * 16
+ *             + (r / 32 % 4) * 4 + b % 4,        blocks = ceil(K / 128)
+ *           (the layout the tensor core reads). A byte of 255 stands for NaN.
+ */
+typedef enum { BOOST_E4M3 = 0, BOOST_E5M2 = 1 } boost_fp8;
+
+/* Bytes of one plane of scales (0 when rows or K is 0). */
+size_t boost_fp8_scale_bytes(int64_t rows, int64_t K);
+
+/*
+ * Quantise G matrices [rows, cols] of bf16 as they lie (q: K = cols), transposed
+ * (qt: [cols, rows], K = rows), or both from one reading of x: the forward product
+ * contracts the columns of x, the weight gradient its rows.
+ *
+ * The scale of a block is the smallest power of two s >= 2^-127 with
+ * max |finite x| <= s * fmax (fmax = 448 for e4m3, 57344 for e5m2), 1 for a block of
+ * zeros; values are x / s rounded to nearest, ties to even. NaN stays NaN; an infinity
+ * becomes NaN in e4m3, which has none, and stays in e5m2.
+ *   block_rows  1: each row (of q; each column for qt) has its own scales; 128: a block is
+ *               128 x 128, so q and qt hold the same values
+ *   ldx, gstride  row and matrix strides of x in elements, multiples of 8
+ *   cols        a multiple of 8
+ *   gamma       [rows] or NULL: x is replaced by bf16(gamma[row] * x), the fold of a
+ *               norm's weight into a down-projection weight; block_rows 128 or qt only
+ *   q, sf       out, or both NULL. pitch = cols rounded up to 16, zeros behind the columns
+ *   qt, sft     out, or both NULL. pitch = rows rounded up to 16, zeros behind the rows
+ * Scale bytes of rows and blocks outside the operand are 127.
+ */
+typedef struct {
+    int64_t G, rows, cols, ldx, gstride;
+    int32_t fmt, block_rows;
+} boost_fp8_quant_desc;
+
+boost_status boost_fp8_quantize(const boost_fp8_quant_desc* desc, const void* x,
+                                const void* gamma, void* q, void* sf, void* qt, void* sft,
+                                void* stream);
+
+/*
+ * out[g] = act(row_scale (.) (A[g] @ B[g]^T)), g < G, A [M, K], B [N, K], out [M, N] bf16,
+ * products and sums in fp32 on the tensor cores.
+ *   G, M, N, K   K >= 0 (K == 0: out = act(0) = 0)
+ *   a_pitch, b_pitch   bytes between rows of the operands, multiples of 16, >= K
+ *   a_fmt, b_fmt  boost_fp8
+ *   act          boost_act, applied after the row scale
+ *   row_scale    [M] fp32 or NULL: the deferred 1/rms of a normed block
+ *   out          [G, M, N] bf16; N a multiple of 8
+ *   ws           workspace of boost_fp8_matmul_workspace_bytes(desc) bytes or more,
+ *                256-byte aligned, error word cleared by boost_block_ws_init
+ * A gradient is the same product on operands quantised the other way: for y = x W^T,
+ * dx = dy W contracts the rows of W (qt of W), dW = dy^T x the tokens (qt of dy and x).
+ */
+typedef struct {
+    int64_t G, M, N, K, a_pitch, b_pitch;
+    int32_t a_fmt, b_fmt, act;
+} boost_fp8_matmul_desc;
+
+size_t boost_fp8_matmul_workspace_bytes(const boost_fp8_matmul_desc* desc);
+
+boost_status boost_fp8_matmul(const boost_fp8_matmul_desc* desc, const void* a, const void* a_sf,
+                              const void* b, const void* b_sf, const float* row_scale, void* out,
+                              void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -35,7 +35,8 @@ EXPORTS = (
     "boost_profile_read_kernels", "boost_block_fwd_swiglu", "boost_block_fwd_btp",
     "boost_block_up", "boost_debug_count_writes", "boost_debug_count_log",
     "boost_profile_only", "boost_block_fwd_residual", "boost_block_bwd_residual",
-    "boost_rope", "boost_dropout",
+    "boost_rope", "boost_dropout", "boost_fp8_scale_bytes", "boost_fp8_quantize",
+    "boost_fp8_matmul_workspace_bytes", "boost_fp8_matmul",
 )
 
 
@@ -54,6 +55,8 @@ class Desc(ctypes.Structure):
 
 
 ROPE_MAX_DIM = 512
+FP8_FORMATS = {"e4m3": (0, torch.float8_e4m3fn), "e5m2": (1, torch.float8_e5m2)}
+FP8_CODE = {dtype: code for code, dtype in FP8_FORMATS.values()}
 
 
 class RopeDesc(ctypes.Structure):
@@ -63,6 +66,16 @@ class RopeDesc(ctypes.Structure):
         [(f, ctypes.c_int64) for f in ("q_ts", "q_hs", "k_ts", "k_hs", "qo_ts", "qo_hs", "ko_ts",
                                        "ko_hs")] + \
         [("axis", ctypes.c_uint8 * (ROPE_MAX_DIM // 2))]
+
+
+class Fp8QuantDesc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int64) for f in ("G", "rows", "cols", "ldx", "gstride")] + \
+        [("fmt", ctypes.c_int32), ("block_rows", ctypes.c_int32)]
+
+
+class Fp8MatmulDesc(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int64) for f in ("G", "M", "N", "K", "a_pitch", "b_pitch")] + \
+        [(f, ctypes.c_int32) for f in ("a_fmt", "b_fmt", "act")]
 
 
 def lib_path() -> str:
@@ -102,6 +115,12 @@ def lib():
     L.boost_rope.argtypes = [ctypes.POINTER(RopeDesc), vp, vp, vp, vp, vp, vp, vp]
     L.boost_dropout.argtypes = [i64, vp, vp, vp, ctypes.c_double, ctypes.c_uint64,
                                 ctypes.c_uint64, vp, vp]
+    L.boost_fp8_scale_bytes.argtypes = [i64, i64]
+    L.boost_fp8_scale_bytes.restype = sz
+    L.boost_fp8_quantize.argtypes = [ctypes.POINTER(Fp8QuantDesc)] + [vp] * 7
+    L.boost_fp8_matmul_workspace_bytes.argtypes = [ctypes.POINTER(Fp8MatmulDesc)]
+    L.boost_fp8_matmul_workspace_bytes.restype = sz
+    L.boost_fp8_matmul.argtypes = [ctypes.POINTER(Fp8MatmulDesc)] + [vp] * 7 + [sz, vp]
     L.boost_status_string.argtypes = [ctypes.c_int]
     L.boost_status_string.restype = ctypes.c_char_p
     L.boost_swiglu_fwd.argtypes = [i64, i64, vp, vp, vp, vp]
@@ -121,7 +140,8 @@ def lib():
     L.boost_profile_read_kernels.argtypes = [ctypes.c_int, ctypes.POINTER(i64)]
     for name in EXPORTS:
         if name not in ("boost_block_workspace_bytes", "boost_status_string",
-                        "boost_debug_count_log"):
+                        "boost_debug_count_log", "boost_fp8_scale_bytes",
+                        "boost_fp8_matmul_workspace_bytes"):
             getattr(L, name).restype = ctypes.c_int
     _LIB = L
     return L
@@ -557,6 +577,97 @@ def dropout_bwd(dout, p, seed, offset=0, *, dx=None, counter=None, stream=None):
     """Gradient of x of ``dropout_add`` with the same p, seed and offset (the residual's
     gradient is dout itself)."""
     return dropout_add(dout, p, seed, offset, out=dx, counter=counter, stream=stream)
+
+
+def fp8_scale_bytes(rows, K) -> int:
+    """Bytes of the scales of one [rows, K] operand."""
+    return int(lib().boost_fp8_scale_bytes(int(rows), int(K)))
+
+
+def fp8_quantize(x, *, fmt="e4m3", block_rows=1, way="rows", gamma=None, rows_out=None,
+                 cols_out=None, stream=None):
+    """8-bit operands of x [rows, cols] or [G, rows, cols] (any row and matrix strides that
+    are multiples of 8): ((q, scales) or None, (qt, scales) or None).
+
+    way "rows": q [.., rows, pitch] contracts the columns; "columns": qt [.., cols, pitch]
+    contracts the rows; "both": one reading of x gives both. pitch is the contracted length
+    rounded up to 16. ``block_rows`` 128 shares a scale among 128 x 128 values, so that q and
+    qt hold the same values. ``gamma`` [rows]: x is replaced by bf16(gamma[row] x).
+    ``rows_out``, ``cols_out``: (q, scales) tensors to write into."""
+    if fmt not in FP8_FORMATS or way not in ("rows", "columns", "both"):
+        raise ValueError("fmt is 'e4m3' or 'e5m2', way 'rows', 'columns' or 'both'")
+    code, dtype = FP8_FORMATS[fmt]
+    if x.dim() not in (2, 3) or (x.shape[-1] > 1 and x.stride(-1) != 1):
+        raise ValueError("x must be [rows, cols] or [G, rows, cols] with adjacent columns")
+    lead = tuple(x.shape[:-2])
+    G = lead[0] if lead else 1
+    rows, cols = x.shape[-2:]
+    _here({"x": x, "gamma": gamma}, torch.bfloat16)
+    if gamma is not None:
+        _need(gamma, "gamma", torch.bfloat16, (rows,))
+
+    def operand(given, name, r, K, wanted):
+        if not wanted:
+            if given is not None:
+                raise ValueError(f"{name} given, but way is {way!r}")
+            return None
+        shape, planes = lead + (r, -(-K // 16) * 16), lead + (fp8_scale_bytes(r, K),)
+        if given is None:
+            return (torch.empty(shape, dtype=dtype, device=x.device),
+                    torch.empty(planes, dtype=torch.uint8, device=x.device))
+        _here({name: given[0], f"{name} scales": given[1]})
+        _need(given[0], name, dtype, shape)
+        _need(given[1], f"{name} scales", torch.uint8, planes)
+        return given
+
+    by_rows = operand(rows_out, "rows_out", rows, cols, way != "columns")
+    by_cols = operand(cols_out, "cols_out", cols, rows, way != "rows")
+    # the stride of a single row or matrix says nothing: a plain one in its place
+    D = Fp8QuantDesc(G, rows, cols, x.stride(-2) if rows > 1 else cols,
+                     x.stride(0) if G > 1 else 0, code, block_rows)
+    q, sf = by_rows or (None, None)
+    qt, sft = by_cols or (None, None)
+    _check(lib().boost_fp8_quantize(ctypes.byref(D), _ptr(x), _ptr(gamma), _ptr(q), _ptr(sf),
+                                    _ptr(qt), _ptr(sft), _stream(stream)), "boost_fp8_quantize")
+    return by_rows, by_cols
+
+
+def fp8_matmul_workspace_bytes(M, N, K, G=1) -> int:
+    pitch = -(-K // 16) * 16
+    D = Fp8MatmulDesc(G, M, N, K, pitch, pitch, 0, 0, 0)
+    return int(lib().boost_fp8_matmul_workspace_bytes(ctypes.byref(D)))
+
+
+def fp8_matmul(a, a_scales, b, b_scales, K, ws: Workspace, *, row_scale=None, act="identity",
+               out=None, stream=None):
+    """act(row_scale * (A @ B^T)) [M, N] in bf16 of 8-bit operands A [M, pitch], B [N, pitch]
+    with their scales (``fp8_quantize``), K values contracted; [G, ...] operands give the G
+    products [G, M, N]. row_scale: float32 [M]."""
+    if a.dim() not in (2, 3) or b.dim() != a.dim() or a.shape[:-2] != b.shape[:-2]:
+        raise ValueError("operands must be [M, pitch] and [N, pitch], or [G, ...] of them")
+    for name, t in (("a", a), ("b", b)):
+        if t.dtype not in FP8_CODE:
+            raise TypeError(f"{name} must be float8_e4m3fn or float8_e5m2, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    lead = tuple(a.shape[:-2])
+    G = lead[0] if lead else 1
+    M, N = a.shape[-2], b.shape[-2]
+    if out is None:
+        out = torch.empty(lead + (M, N), dtype=torch.bfloat16, device=a.device)
+    _here({"a": a, "a_scales": a_scales, "b": b, "b_scales": b_scales, "row_scale": row_scale,
+           "out": out, "ws": ws.buf})
+    _need(a_scales, "a_scales", torch.uint8, lead + (fp8_scale_bytes(M, K),))
+    _need(b_scales, "b_scales", torch.uint8, lead + (fp8_scale_bytes(N, K),))
+    _need(out, "out", torch.bfloat16, lead + (M, N))
+    if row_scale is not None:
+        _need(row_scale, "row_scale", torch.float32, (M,))
+    D = Fp8MatmulDesc(G, M, N, K, a.shape[-1], b.shape[-1], FP8_CODE[a.dtype], FP8_CODE[b.dtype],
+                      ACT[act])
+    _check(lib().boost_fp8_matmul(ctypes.byref(D), _ptr(a), _ptr(a_scales), _ptr(b),
+                                  _ptr(b_scales), _ptr(row_scale), _ptr(out), ws.ptr, ws.nbytes,
+                                  _stream(stream)), "boost_fp8_matmul")
+    return out
 
 
 def check(ws: Workspace, stream=None):

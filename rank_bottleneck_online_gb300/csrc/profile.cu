@@ -23,7 +23,7 @@ const char* const kNames[K_COUNT] = {
     "splitk_sum",    "splitk_finalize_dA", "dgamma_reduce", "swiglu_fwd",
     "swiglu_bwd",    "add",            "wait_probe",    "gemm_dx_swiglu",
     "gemm_up_swiglu", "gemm_down_partials", "btp_exchange_reduce", "rmsnorm_stats_fold",
-    "rope", "dropout"};
+    "rope", "dropout", "fp8_quantize", "gemm_fp8"};
 
 struct Pending {
   int id;

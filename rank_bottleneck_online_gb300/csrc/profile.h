@@ -30,6 +30,8 @@ enum KernelId : int {
   K_STATS_FOLD,
   K_ROPE,
   K_DROPOUT,
+  K_FP8_QUANT,
+  K_FP8_GEMM,
   K_COUNT
 };
 

@@ -140,3 +140,55 @@ def drop_call(L, count=64, x=0x10000, res=0x20000, out=0x30000, p=0.1, counter=0
 ])
 def test_dropout_refusals(L, kw, want):
     assert drop_call(L, **kw) == want
+
+
+# ------------------------------------------------------------------- 8-bit refusals
+def quant_call(L, G=1, rows=16, cols=64, ldx=64, gstride=0, fmt=0, block_rows=1, x=0x10000, gamma=0,
+               q=0x20000, sf=0x30000, qt=0x40000, sft=0x50000):
+    D = B.Fp8QuantDesc(G, rows, cols, ldx, gstride, fmt, block_rows)
+    return L.boost_fp8_quantize(ctypes.byref(D), ptr(x), ptr(gamma), ptr(q), ptr(sf), ptr(qt),
+                                ptr(sft), None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(G=0), INVALID), (dict(rows=-1), INVALID), (dict(cols=0), INVALID), (dict(fmt=2), INVALID),
+    (dict(block_rows=64), INVALID), (dict(ldx=-8), INVALID), (dict(cols=60), SHAPE),
+    (dict(ldx=68), SHAPE), (dict(gstride=4), SHAPE), (dict(G=70000), SHAPE),
+    (dict(rows=1 << 32), SHAPE), (dict(sf=0), INVALID), (dict(qt=0), INVALID),
+    (dict(q=0, sf=0, qt=0, sft=0), INVALID), (dict(x=0), INVALID), (dict(x=0x10008), ALIGN),
+    (dict(q=0x20008), ALIGN), (dict(sft=0x50004), ALIGN), (dict(q=0x10000), INVALID),
+    (dict(sf=0x20010), INVALID), (dict(qt=0x30000), INVALID),
+    (dict(gamma=0x60000, qt=0, sft=0), INVALID),       # a fold needs the tiled layouts
+    (dict(rows=0), 0),
+])
+def test_fp8_quantize_refusals(L, kw, want):
+    assert quant_call(L, **kw) == want
+
+
+def test_fp8_scale_bytes(L):
+    assert B.fp8_scale_bytes(1, 1) == 512
+    assert B.fp8_scale_bytes(128, 512) == 512
+    assert B.fp8_scale_bytes(129, 513) == 2048
+    assert B.fp8_scale_bytes(0, 4) == B.fp8_scale_bytes(4, 0) == 0
+
+
+def matmul_call(L, G=1, M=16, N=64, K=64, a_pitch=64, b_pitch=64, fa=0, fb=0, act=0, a=0x10000,
+                asf=0x20000, b=0x30000, bsf=0x40000, rs=0, out=0x50000, ws=0x1000000, ws_bytes=None):
+    D = B.Fp8MatmulDesc(G, M, N, K, a_pitch, b_pitch, fa, fb, act)
+    need = L.boost_fp8_matmul_workspace_bytes(ctypes.byref(D))
+    return L.boost_fp8_matmul(ctypes.byref(D), ptr(a), ptr(asf), ptr(b), ptr(bsf), ptr(rs), ptr(out),
+                              ptr(ws), need if ws_bytes is None else ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(G=0), INVALID), (dict(M=-1), INVALID), (dict(N=0), INVALID), (dict(K=-1), INVALID),
+    (dict(fa=2), INVALID), (dict(fb=-1), INVALID), (dict(act=3), INVALID),
+    (dict(a_pitch=48), INVALID), (dict(b_pitch=72), SHAPE), (dict(N=60), SHAPE),
+    (dict(G=70000), SHAPE), (dict(M=1 << 31), SHAPE), (dict(N=1 << 21), SHAPE),
+    (dict(a=0), INVALID), (dict(bsf=0), INVALID), (dict(out=0), INVALID),
+    (dict(a=0x10008), ALIGN), (dict(rs=0x60004), ALIGN), (dict(out=0x50002), ALIGN),
+    (dict(ws=0), WORKSPACE), (dict(ws=0x1000010), WORKSPACE), (dict(ws_bytes=128), WORKSPACE),
+    (dict(out=0x10000), INVALID), (dict(ws=0x50000), INVALID), (dict(M=0), 0),
+])
+def test_fp8_matmul_refusals(L, kw, want):
+    assert matmul_call(L, **kw) == want
