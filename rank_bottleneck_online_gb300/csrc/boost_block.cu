@@ -43,28 +43,7 @@ int gemm_resident(int bn, int mode, int cg, int mcm, int mcn, int num_sms) {
     return gemm_resident_fwd(bn, mode, cg, mcm, mcn, num_sms);
   return gemm_resident_bwd(bn, mode, cg, mcm, mcn, num_sms);
 }
-}  // namespace boost_gb300
 
-using namespace boost_gb300;
-
-namespace {
-
-constexpr size_t kAlign = 256;
-constexpr int64_t kMaxDim = (1ll << 31) - 1;
-
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Two buffers of `bytes` each that overlap without being the same buffer.
-bool partial_overlap(const void* a, const void* b, uint64_t bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x != y && x < y + bytes && y < x + bytes;
-}
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// --------------------------------------------------------------- devices
 int current_num_sms() {
   // per-device cache; host threads may fill it concurrently (same value)
   static std::atomic<int> cache[64];
@@ -95,12 +74,6 @@ uint64_t wait_limit_ns() {
   return v;
 }
 
-// ----------------------------------------------------------- tensor maps
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeFn get_encode() {
   static EncodeFn fn = nullptr;
   static std::once_flag once;
@@ -116,6 +89,28 @@ EncodeFn get_encode() {
   return fn;
 }
 
+}  // namespace boost_gb300
+
+using namespace boost_gb300;
+
+namespace {
+
+constexpr size_t kAlign = 256;
+constexpr int64_t kMaxDim = (1ll << 31) - 1;
+
+size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Two buffers of `bytes` each that overlap without being the same buffer.
+bool partial_overlap(const void* a, const void* b, uint64_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x != y && x < y + bytes && y < x + bytes;
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ----------------------------------------------------------- tensor maps
 // 3-D bf16 view: dims (d0 contiguous, d1, d2), byte strides of d1 and d2, box b0 x b1 x b2,
 // 128-byte swizzle (operand loads) or 64-byte swizzle (32-wide epilogue store boxes),
 // zero fill out of bounds.

@@ -1,11 +1,31 @@
-// fp8_gemm.cu -- out = act(row_scale (.) (A B^T)) for 8-bit operands with a power-of-two
-// scale for each block of 128 along K.
+// fp8_gemm.cu -- out[g] = act(row_scale (.) (A[g] B[g]^T)) for 8-bit operands with a
+// power-of-two scale for each block of 128 along K.
 //
-// One thread an output element: the products of a block of 128 are summed in fp32 and
-// joined with the block's two scales, 2^(ea + eb - 254), which is exact.
+// The tensor core applies the scales itself: tcgen05.mma kind::mxf8f6f4 multiplies K = 32
+// values a step by one E8M0 scale of each row of A and of B, which it reads from TMEM. A
+// block of 128 is four steps with the same byte of the scale words, and a scale tile (128
+// rows x 4 blocks, 512 bytes, the layout the operands are stored in) serves sixteen: it
+// travels with the operands of its first block (TMA, then tcgen05.cp to TMEM, which runs in
+// order with the MMAs). So the scales cost no arithmetic, and the sums stay in fp32 in TMEM
+// over the whole of K. (Scales of any value would have to be applied by the CUDA cores: each
+// block's 128 x 256 partial product read from TMEM and joined by an FMA each, a half of the
+// tensor cores' time at this tile.)
+//
+// The shape of the kernel is the bf16 engine's: a persistent grid, one CTA an SM, warp 0
+// streams operand tiles (128 bytes of K) with TMA, warp 1 issues the MMAs, warps 2..9 read
+// the accumulator and store it. A CTA pair (CG = 2) shares a 256 x BN tile; MCM x MCN pairs
+// form a cluster that shares operand rows by multicast.
+//
+// TMEM: 512 columns hold two accumulators of 256 less the scales. The second begins at 224
+// and shares 32 columns with the first; the epilogue reads those first and lets the next
+// tile's MMAs start, so the two tiles still overlap but for that read.
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstring>
 
 #include "fp8.cuh"
 #include "internal.h"
@@ -15,49 +35,439 @@ namespace boost_gb300 {
 
 namespace {
 
-__device__ __forceinline__ float from8(uint8_t v, int fmt) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(v, fmt == BOOST_E4M3 ? __NV_E4M3 : __NV_E5M2);
-  return __half2float(*reinterpret_cast<const __half*>(&h));
+constexpr int kKBytes = 128;           // K of one stage: a swizzle row, and a scale block
+
+struct Fp8Params {
+  CUtensorMap tmA, tmB;                // (K, rows, G) bytes, boxes 128 x 64
+  CUtensorMap tmSA, tmSB;              // scale tiles (128 words, tiles of K, row tiles of all G)
+  CUtensorMap tmO;                     // out (N, M, G), boxes 32 x 32
+  int32_t M, N, G, num_kb;
+  int32_t m_tiles, n_tiles;            // super-tiles
+  int32_t a_row_tiles, b_row_tiles;    // scale tiles along the rows of one matrix
+  int32_t a_fmt, b_fmt, act;
+  const float* row_scale;
+  __nv_bfloat16* out;
+  DeviceError* err;
+  uint64_t wait_limit_ns;
+};
+
+template <int BN, int CG, int MCM, int MCN>
+struct Fp8Cfg {
+  static constexpr int kEpiW = 8;
+  static constexpr int kThreads = 32 * (2 + kEpiW);
+  static constexpr int kBRows = BN / CG;               // B rows staged by one CTA
+  static constexpr int kABytes = kBM * kKBytes;
+  static constexpr int kBBytes = kBRows * kKBytes;
+  static constexpr int kSfTilesB = (BN + 127) / 128;
+  static constexpr int kSfBytes = kScaleTile * (1 + kSfTilesB);
+  static constexpr int kStgBytes = kEpiW * 2048;
+  static constexpr int kStages0 = (232448 - 2048 - kStgBytes) / (kABytes + kBBytes + kSfBytes);
+  static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
+  static constexpr int kAcc1 = BN == 256 ? 224 : BN;   // column of the second accumulator
+  static constexpr bool kOverlap = kAcc1 < BN;
+  static constexpr int kSfCols = 4 * (1 + kSfTilesB);
+  static constexpr int kSfCol = 512 - 32;              // two buffers of kSfCols columns
+  static constexpr int kBarBytes = 8 * (2 * kStages + 2 + 2 + 1) + 16;
+  static constexpr int kSfOffset = kStages * (kABytes + kBBytes);
+  static constexpr int kBarOffset = kSfOffset + kStages * kSfBytes;
+  static constexpr int kStgOffset = (kBarOffset + kBarBytes + 1023) / 1024 * 1024;
+  static constexpr int kSmemBytes = 1024 + kStgOffset + kStgBytes;
+  static constexpr int kPairs = MCM * MCN;
+  static constexpr int kCluster = CG * kPairs;
+  static constexpr int kTileM = kBM * CG * MCM, kTileN = BN * MCN;
+  static_assert(BN % 128 == 0 && BN <= 256, "whole scale tiles");
+  static_assert(kAcc1 + BN <= kSfCol && 2 * kSfCols <= 32, "TMEM");
+  static_assert(kPairs == 1 || (CG == 2 && BN == 256 && MCM <= 2 && MCN <= 2), "multicast shapes");
+  static_assert(kStages >= 4 && kSmemBytes <= 232448, "shared memory");
+};
+
+struct Tile {
+  int32_t g, m0, n0;
+};
+
+// Tiles in order: matrix, then groups of 8 rows of super-tiles with m fastest, so that a wave
+// shares columns of B and the group's rows of A in L2.
+template <class Cfg>
+__device__ __forceinline__ Tile tile_at(const Fp8Params& p, int32_t tile) {
+  constexpr int kGroup = 8;
+  const int32_t per = p.m_tiles * p.n_tiles;
+  const int32_t g = tile / per, rem = tile - g * per;
+  const int32_t full = kGroup * p.n_tiles, band = rem / full;
+  const int32_t rows = min(kGroup, p.m_tiles - band * kGroup);
+  const int32_t at = rem - band * full;
+  return {g, (band * kGroup + at % rows) * Cfg::kTileM, at / rows * Cfg::kTileN};
 }
 
-__device__ __forceinline__ float scale_of(uint8_t byte) {
-  if (byte == 255) return __uint_as_float(0x7fc00000u);
-  return byte == 0 ? 0x1p-127f : __uint_as_float(static_cast<uint32_t>(byte) << 23);
-}
+template <int BN, int CG, int MCM, int MCN>
+__global__ void __launch_bounds__(Fp8Cfg<BN, CG, MCM, MCN>::kThreads, 1)
+    fp8_gemm_kernel(const __grid_constant__ Fp8Params p) {
+  using Cfg = Fp8Cfg<BN, CG, MCM, MCN>;
+  constexpr int CL = Cfg::kCluster;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + Cfg::kStages * Cfg::kABytes;
+  uint8_t* sS = smem + Cfg::kSfOffset;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOffset);
+  uint64_t* empty_bar = full_bar + Cfg::kStages;
+  uint64_t* tfull_bar = empty_bar + Cfg::kStages;      // an accumulator is complete
+  uint64_t* tfree_bar = tfull_bar + 2;                 // the next tile may overwrite it
+  uint64_t* done_bar = tfree_bar + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
 
-__global__ void __launch_bounds__(kThreads) fp8_gemm_kernel(const Fp8GemmParams p) {
-  pdl_enter();
-  const int64_t m = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
-  const int64_t n = static_cast<int64_t>(blockIdx.y) * 16 + (threadIdx.x & 15);
-  const int64_t g = blockIdx.z;
-  if (m >= p.d.M || n >= p.d.N) return;
-  const uint8_t* a = p.a + (g * p.d.M + m) * p.d.a_pitch;
-  const uint8_t* b = p.b + (g * p.d.N + n) * p.d.b_pitch;
-  const uint8_t* sa = p.a_sf + g * scale_plane(p.d.M, p.d.K);
-  const uint8_t* sb = p.b_sf + g * scale_plane(p.d.N, p.d.K);
-  const int64_t kt = scale_tiles_k(p.d.K);
-  float acc = 0.0f;
-  for (int64_t k0 = 0; k0 < p.d.K; k0 += kScaleBlock) {
-    float part = 0.0f;
-    const int64_t end = min(k0 + kScaleBlock, p.d.K);
-    for (int64_t k = k0; k < end; ++k)
-      part = fmaf(from8(a[k], p.d.a_fmt), from8(b[k], p.d.b_fmt), part);
-    acc += part * scale_of(sa[scale_at(m, k0 / kScaleBlock, kt)]) *
-           scale_of(sb[scale_at(n, k0 / kScaleBlock, kt)]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = CL > 1 ? cluster_ctarank() : 0;
+  const uint32_t rank = crank % CG;                    // CTA within its pair
+  const uint32_t pp = crank / CG;                      // pair within the cluster
+  const uint32_t pm = pp % MCM, pn = pp / MCM;
+  const uint32_t leader_rank = pp * CG;
+  const bool leader = rank == 0;
+  const int32_t num_tiles = p.G * p.m_tiles * p.n_tiles;
+  const int32_t first_tile = static_cast<int32_t>(blockIdx.x) / CL;
+  const int32_t tile_stride = static_cast<int32_t>(gridDim.x) / CL;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], Cfg::kPairs);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull_bar[a], 1);
+      mbar_init(&tfree_bar[a], Cfg::kEpiW * CG);
+    }
+    mbar_init(done_bar, 1);
+    fence_barrier_init();
   }
-  if (p.row_scale != nullptr) acc *= p.row_scale[m];
-  if (p.d.act == BOOST_ACT_SILU) acc = act_fwd(acc, 1);
-  static_cast<__nv_bfloat16*>(p.out)[(g * p.d.M + m) * p.d.N + n] = __float2bfloat16_rn(acc);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.tmA);
+    tma_prefetch_desc(&p.tmB);
+    tma_prefetch_desc(&p.tmSA);
+    tma_prefetch_desc(&p.tmSB);
+    tma_prefetch_desc(&p.tmO);
+  }
+  if (warp == 1) {
+    if constexpr (CG == 2) {
+      tmem_alloc_pair(tmem_holder, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_holder, 512);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  if constexpr (CL > 1) cluster_sync(); else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  // Everything above touches only shared memory, TMEM and the kernel parameters.
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      constexpr OperandView kView{1, 0, 2, 0};         // (K, rows, G): K-major
+      int stage = 0;
+      uint32_t phase = 0, armed_mask = 0, parity_mask = 0;
+      bool ok = true;
+      for (int32_t tile = first_tile; tile < num_tiles && ok; tile += tile_stride) {
+        const Tile t = tile_at<Cfg>(p, tile);
+        const int32_t m_own = t.m0 + static_cast<int32_t>(pm * (kBM * CG) + rank * kBM);
+        const int32_t n_pair = t.n0 + static_cast<int32_t>(pn) * BN;
+        const int32_t n_own = n_pair + static_cast<int32_t>(rank) * Cfg::kBRows;
+        for (int32_t kb = 0; kb < p.num_kb; ++kb) {
+          if (!bounded_wait(&empty_bar[stage], phase ^ 1u, p.err, 21, p.wait_limit_ns)) {
+            ok = false;
+            break;
+          }
+          const bool scales = (kb & 3) == 0;
+          uint32_t bar = 0;
+          if constexpr (CG == 2) bar = mapa_shared(smem_u32(&full_bar[stage]), leader_rank);
+          if (leader)
+            mbar_arrive_expect_tx(&full_bar[stage],
+                                  CG * (Cfg::kABytes + Cfg::kBBytes + (scales ? Cfg::kSfBytes : 0)));
+          armed_mask |= 1u << stage;
+          parity_mask = (parity_mask & ~(1u << stage)) | (phase << stage);
+          uint8_t* dA = sA + stage * Cfg::kABytes;
+          uint8_t* dB = sB + stage * Cfg::kBBytes;
+          uint8_t* dS = sS + stage * Cfg::kSfBytes;
+          if constexpr (MCN == 2) {
+            uint16_t mask = 0;
+            for (uint32_t j = 0; j < MCN; ++j) mask |= 1u << ((j * MCM + pm) * CG + rank);
+            load_operand_mc(&p.tmA, kView, dA + pn * 8192, bar, mask,
+                            m_own + static_cast<int32_t>(pn) * 64, kb * kKBytes, t.g);
+          } else {
+            load_operand<CG>(&p.tmA, kView, dA, &full_bar[stage], bar, m_own, kb * kKBytes, t.g, kBM);
+          }
+          if constexpr (MCM == 2) {
+            uint16_t mask = 0;
+            for (uint32_t i = 0; i < MCM; ++i) mask |= 1u << ((pn * MCM + i) * CG + rank);
+            load_operand_mc(&p.tmB, kView, dB + pm * 8192, bar, mask,
+                            n_own + static_cast<int32_t>(pm) * 64, kb * kKBytes, t.g);
+          } else {
+            load_operand<CG>(&p.tmB, kView, dB, &full_bar[stage], bar, n_own, kb * kKBytes, t.g,
+                             Cfg::kBRows);
+          }
+          if (scales) {
+            // this CTA's rows of A, all the pair's columns of B
+            const int32_t ra = t.g * p.a_row_tiles + m_own / 128;
+            const int32_t rb = t.g * p.b_row_tiles + n_pair / 128;
+            if constexpr (CG == 2) {
+              tma_load_3d_pair(dS, &p.tmSA, bar, 0, kb >> 2, ra);
+              tma_load_3d_pair(dS + kScaleTile, &p.tmSB, bar, 0, kb >> 2, rb);
+            } else {
+              tma_load_3d(dS, &p.tmSA, &full_bar[stage], 0, kb >> 2, ra);
+              tma_load_3d(dS + kScaleTile, &p.tmSB, &full_bar[stage], 0, kb >> 2, rb);
+            }
+          }
+          if (++stage == Cfg::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // the copies started here have landed before the CTA exits (both CTAs' complete on the
+      // even CTA's barriers)
+      if (leader) {
+        for (int s = 0; s < Cfg::kStages; ++s) {
+          if (armed_mask & (1u << s)) {
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(&full_bar[s], (parity_mask >> s) & 1u)) {
+              if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+                record_error(p.err, kErrTimeout, 27);
+                break;
+              }
+            }
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- MMA issuer
+    if (lane == 0 && leader) {
+      int stage = 0;
+      uint32_t phase = 0, sf = 0;                      // sf: which scale buffer
+      const uint32_t idesc = idesc_mxf8_f32(kBM * CG, BN, p.a_fmt, p.b_fmt);
+      const uint64_t hi = desc_hi_sw128(16u, 1024u);
+      const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB), s0 = smem_u32(sS);
+      bool ok = true;
+      int32_t it = 0;                                  // tiles of this CTA so far
+      for (int32_t tile = first_tile; tile < num_tiles && ok; tile += tile_stride, ++it) {
+        const int acc = it & 1;
+        // Free: the accumulator's own tile before last has been read (parity of its use), or,
+        // where the two share columns, those of the last tile, which comes after that.
+        const int wait_acc = Cfg::kOverlap ? acc ^ 1 : acc;
+        const uint32_t uses = static_cast<uint32_t>(Cfg::kOverlap ? (it + 1) >> 1 : it >> 1);
+        if (!bounded_wait(&tfree_bar[wait_acc], (uses & 1u) ^ 1u, p.err, 22, p.wait_limit_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * Cfg::kAcc1;
+        uint32_t sa = 0, sb = 0;
+        for (int32_t kb = 0; kb < p.num_kb; ++kb) {
+          if (!bounded_wait(&full_bar[stage], phase, p.err, 23, p.wait_limit_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if ((kb & 3) == 0) {
+            sa = tmem_base + Cfg::kSfCol + sf * 16;
+            sb = sa + 4;
+            sf ^= 1u;
+            const uint32_t at = s0 + stage * Cfg::kSfBytes;
+            tc_cp_scales<CG>(sa, smem_desc_scales(at));
+#pragma unroll
+            for (int i = 0; i < Cfg::kSfTilesB; ++i)
+              tc_cp_scales<CG>(sb + 4 * i, smem_desc_scales(at + kScaleTile * (1 + i)));
+          }
+          const uint64_t ad = hi | (((a0 + stage * Cfg::kABytes) >> 4) & 0x3FFFu);
+          const uint64_t bd = hi | (((b0 + stage * Cfg::kBBytes) >> 4) & 0x3FFFu);
+          const uint32_t id = idesc | idesc_scale_id(kb & 3);
+#pragma unroll
+          for (int kk = 0; kk < kKBytes / 32; ++kk)
+            tc_mma_mxf8<CG>(d_tmem, ad + 2 * kk, bd + 2 * kk, id, sa, sb, (kk | kb) != 0);
+          if constexpr (CG == 2)
+            tc_commit_pair_mc(&empty_bar[stage], static_cast<uint16_t>((1u << CL) - 1u));
+          else
+            tc_commit(&empty_bar[stage]);
+          if (++stage == Cfg::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if constexpr (CG == 2)
+          tc_commit_pair_mc(&tfull_bar[acc], static_cast<uint16_t>(0x3u << leader_rank));
+        else
+          tc_commit(&tfull_bar[acc]);
+      }
+      // every MMA issued here is complete before TMEM is released
+      if constexpr (CG == 2) tc_commit_pair(done_bar); else tc_commit(done_bar);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(done_bar, 0)) {
+        if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+          record_error(p.err, kErrTimeout, 28);
+          break;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- epilogue
+    // Two warps a lane quarter: warp `half` takes 32-column chunks half, half + 2, ... of the
+    // first accumulator in falling order and of the second in rising order, so that the
+    // shared columns (the last chunk and the first) are read at once.
+    const int q = warp & 3, half = (warp - 2) / 4;
+    StoreRing<1, true> ring{smem + Cfg::kStgOffset + (warp - 2) * 2048, 0};
+    int32_t it = 0;
+    for (int32_t tile = first_tile; tile < num_tiles; tile += tile_stride, ++it) {
+      const int acc = it & 1;
+      const Tile t = tile_at<Cfg>(p, tile);
+      const int32_t row0 = t.m0 + static_cast<int32_t>(pm * (kBM * CG) + rank * kBM) + q * 32;
+      const int32_t n_pair = t.n0 + static_cast<int32_t>(pn) * BN;
+      const int32_t row = row0 + lane;
+      const float scale = p.row_scale != nullptr && row < p.M ? p.row_scale[row] : 1.0f;
+      const uint32_t t_row =
+          tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * Cfg::kAcc1;
+      if (!bounded_wait(&tfull_bar[acc], static_cast<uint32_t>(it >> 1) & 1u, p.err, 24,
+                        p.wait_limit_ns))
+        break;
+      tc_fence_after();
+      constexpr int kChunks = BN / 64;                 // of one warp
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int c = 2 * (acc == 0 ? kChunks - 1 - i : i) + half;
+        float v[32];
+        tmem_ld_32x32b_x32(t_row + c * 32, v);
+        tmem_ld_wait();
+        if (i == (Cfg::kOverlap ? 0 : kChunks - 1)) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (CG == 2)
+              mbar_arrive_cluster(mapa_shared(smem_u32(&tfree_bar[acc]), leader_rank));
+            else
+              mbar_arrive(&tfree_bar[acc]);
+          }
+        }
+        const int32_t col0 = n_pair + c * 32;
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          pk[j] = pack_bf16x2(act_fwd(v[2 * j] * scale, p.act), act_fwd(v[2 * j + 1] * scale, p.act));
+        if (col0 < p.N && row0 < p.M)
+          store_chunk_bf16(ring, lane, pk, &p.tmO, true, col0, row0, t.g,
+                           static_cast<__nv_bfloat16*>(nullptr), 0, 0, 0);
+      }
+    }
+    if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  if constexpr (CL > 1) cluster_sync(); else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (CG == 2) tmem_dealloc_pair(tmem_base, 512);
+    else tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// ----------------------------------------------------------------------- host
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t d0, uint64_t d1,
+              uint64_t d2, uint64_t s1, uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2,
+              CUtensorMapSwizzle swizzle) {
+  EncodeFn enc = get_encode();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {s1, s2};
+  const cuuint32_t box[3] = {b0, b1, b2}, ones[3] = {1, 1, 1};
+  return enc(m, type, 3, const_cast<void*>(base), dims, strides, box, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, int CG, int MCM, int MCN>
+cudaError_t launch_shape(const Fp8GemmParams& g, cudaStream_t stream) {
+  using Cfg = Fp8Cfg<BN, CG, MCM, MCN>;
+  constexpr int CL = Cfg::kCluster;
+  const auto kern = fp8_gemm_kernel<BN, CG, MCM, MCN>;
+  const boost_fp8_matmul_desc& d = g.d;
+  Fp8Params p;
+  std::memset(&p, 0, sizeof(p));
+  const uint64_t M = d.M, N = d.N, K = d.K, G = d.G;
+  const uint64_t kt = scale_tiles_k(d.K), ra = (M + 127) / 128, rb = (N + 127) / 128;
+  if (!make_map(&p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, K, M, G, d.a_pitch, M * d.a_pitch,
+                kKBytes, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&p.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b, K, N, G, d.b_pitch, N * d.b_pitch,
+                kKBytes, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&p.tmSA, CU_TENSOR_MAP_DATA_TYPE_INT32, g.a_sf, 128, kt, ra * G, kScaleTile,
+                kt * kScaleTile, 128, 1, 1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !make_map(&p.tmSB, CU_TENSOR_MAP_DATA_TYPE_INT32, g.b_sf, 128, kt, rb * G, kScaleTile,
+                kt * kScaleTile, 128, 1, Cfg::kSfTilesB, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !make_map(&p.tmO, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.out, N, M, G, 2 * N, 2 * M * N, 32, 32,
+                1, CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
+  p.M = static_cast<int32_t>(M);
+  p.N = static_cast<int32_t>(N);
+  p.G = static_cast<int32_t>(G);
+  p.num_kb = static_cast<int32_t>((K + kKBytes - 1) / kKBytes);
+  p.m_tiles = static_cast<int32_t>((M + Cfg::kTileM - 1) / Cfg::kTileM);
+  p.n_tiles = static_cast<int32_t>((N + Cfg::kTileN - 1) / Cfg::kTileN);
+  p.a_row_tiles = static_cast<int32_t>(ra);
+  p.b_row_tiles = static_cast<int32_t>(rb);
+  p.a_fmt = d.a_fmt;
+  p.b_fmt = d.b_fmt;
+  p.act = d.act;
+  p.row_scale = g.row_scale;
+  p.out = static_cast<__nv_bfloat16*>(g.out);
+  p.err = static_cast<DeviceError*>(g.ws);
+  p.wait_limit_ns = wait_limit_ns();
+
+  // per-device state, filled once (host threads may do so concurrently with the same values)
+  static std::atomic<int> resident[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CL;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int groups = dev < 64 ? resident[dev].load(std::memory_order_acquire) : 0;
+  if (groups == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    groups = current_num_sms() / CL;
+    if (CL > 1) {
+      int n = 0;
+      cfg.gridDim = dim3(static_cast<unsigned>(groups * CL), 1, 1);
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0)
+        groups = std::min(groups, n);
+      else
+        cudaGetLastError();
+    }
+    if (dev < 64) resident[dev].store(groups, std::memory_order_release);
+  }
+  const int64_t tiles = static_cast<int64_t>(p.G) * p.m_tiles * p.n_tiles;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, groups) * CL), 1, 1);
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace
 
 size_t fp8_gemm_workspace(const boost_fp8_matmul_desc&) { return 256; }
 
-cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((p.d.M + 15) / 16), static_cast<unsigned>((p.d.N + 15) / 16),
-                  static_cast<unsigned>(p.d.G));
-  return launch_grid(fp8_gemm_kernel, grid, stream, p);
+cudaError_t launch_fp8_gemm(const Fp8GemmParams& g, cudaStream_t stream) {
+  if (g.d.M <= 128) return launch_shape<128, 1, 1, 1>(g, stream);
+  return launch_shape<256, 2, 1, 1>(g, stream);
 }
 
 }  // namespace boost_gb300

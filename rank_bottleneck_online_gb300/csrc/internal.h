@@ -24,6 +24,17 @@ int gemm_resident(int bn, int mode, int cg, int mcm, int mcn, int num_sms);
 // touches global memory) unless the environment sets BOOST_PDL=0.
 bool pdl_enabled();
 
+// SMs of the current device (cached).
+int current_num_sms();
+// Limit of every device-side wait (BOOST_WAIT_LIMIT_MS, 2 s by default).
+uint64_t wait_limit_ns();
+// The driver's cuTensorMapEncodeTiled, or NULL without a driver.
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn get_encode();
+
 // ------------------------------------------------------ CUDA-core kernels
 cudaError_t launch_rmsnorm_stats(const void* x, int64_t T, int64_t d, int S, float eps,
                                  float* ssq, float* rstd, cudaStream_t stream);

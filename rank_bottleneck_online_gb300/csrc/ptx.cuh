@@ -413,3 +413,65 @@ __device__ __forceinline__ void tma_load_3d_pair_mc(void* dst, const void* tmap,
 }
 
 }  // namespace boost_gb300
+
+namespace boost_gb300 {
+
+// ------------------------------------- 8-bit operands with hardware block scales
+// Instruction descriptor for kind::mxf8f6f4 (8-bit A/B, fp32 D, E8M0 scales) without the
+// scale ids. Formats: 0 e4m3, 1 e5m2; both operands K-major.
+__host__ __device__ constexpr uint32_t idesc_mxf8_f32(uint32_t M, uint32_t N, uint32_t a_fmt,
+                                                      uint32_t b_fmt) {
+  return (a_fmt << 7)          // A format
+         | (b_fmt << 10)       // B format
+         | ((N >> 3) << 17)    // N / 8
+         | (1u << 23)          // scale format: E8M0
+         | ((M >> 4) << 24);   // M / 16
+}
+
+// The byte of each 32-bit scale word in TMEM that this instruction uses, for A and B alike.
+__device__ __forceinline__ uint32_t idesc_scale_id(uint32_t id) { return (id << 4) | (id << 29); }
+
+// Descriptor of a scale tile in shared memory for tcgen05.cp: 32 rows of 16 bytes without a
+// swizzle, groups of 8 rows 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128u >> 4) << 32) |
+         (1ull << 46);
+}
+
+// Copy 32 rows x 16 bytes from shared memory to 4 TMEM columns of each of the four lane
+// quarters (of both CTAs of a pair, from each CTA's own shared memory). Runs in order with
+// the MMAs that this thread issues after it.
+template <int CG>
+__device__ __forceinline__ void tc_cp_scales(uint32_t tmem, uint64_t desc) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
+}
+
+// D (+)= (scale_a A) (scale_b B)^T, K = 32, one scale of each row of A and B, from TMEM.
+template <int CG>
+__device__ __forceinline__ void tc_mma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem,
+                                            uint32_t accumulate) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+}  // namespace boost_gb300
