@@ -13,8 +13,7 @@
 //
 // The shape of the kernel is the bf16 engine's: a persistent grid, one CTA an SM, warp 0
 // streams operand tiles (128 bytes of K) with TMA, warp 1 issues the MMAs, warps 2..9 read
-// the accumulator and store it. A CTA pair (CG = 2) shares a 256 x BN tile; MCM x MCN pairs
-// form a cluster that shares operand rows by multicast.
+// the accumulator and store it. A CTA pair (CG = 2) shares a 256 x BN tile.
 //
 // TMEM: 512 columns hold two accumulators of 256 less the scales. The second begins at 224
 // and shares 32 columns with the first; the epilogue reads those first and lets the next
@@ -25,6 +24,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cstdlib>
 #include <cstring>
 
 #include "fp8.cuh"
@@ -38,11 +38,11 @@ namespace {
 constexpr int kKBytes = 128;           // K of one stage: a swizzle row, and a scale block
 
 struct Fp8Params {
-  CUtensorMap tmA, tmB;                // (K, rows, G) bytes, boxes 128 x 64
+  CUtensorMap tmA, tmB;                // (K, rows, G) bytes, boxes 128 x a CTA's rows
   CUtensorMap tmSA, tmSB;              // scale tiles (128 words, tiles of K, row tiles of all G)
   CUtensorMap tmO;                     // out (N, M, G), boxes 32 x 32
   int32_t M, N, G, num_kb;
-  int32_t m_tiles, n_tiles;            // super-tiles
+  int32_t m_tiles, n_tiles;            // of 128 CG x BN
   int32_t a_row_tiles, b_row_tiles;    // scale tiles along the rows of one matrix
   int32_t a_fmt, b_fmt, act;
   const float* row_scale;
@@ -51,7 +51,7 @@ struct Fp8Params {
   uint64_t wait_limit_ns;
 };
 
-template <int BN, int CG, int MCM, int MCN>
+template <int BN, int CG>
 struct Fp8Cfg {
   static constexpr int kEpiW = 8;
   static constexpr int kThreads = 32 * (2 + kEpiW);
@@ -72,12 +72,9 @@ struct Fp8Cfg {
   static constexpr int kBarOffset = kSfOffset + kStages * kSfBytes;
   static constexpr int kStgOffset = (kBarOffset + kBarBytes + 1023) / 1024 * 1024;
   static constexpr int kSmemBytes = 1024 + kStgOffset + kStgBytes;
-  static constexpr int kPairs = MCM * MCN;
-  static constexpr int kCluster = CG * kPairs;
-  static constexpr int kTileM = kBM * CG * MCM, kTileN = BN * MCN;
-  static_assert(BN % 128 == 0 && BN <= 256, "whole scale tiles");
+  static constexpr int kTileM = kBM * CG;
+  static_assert(BN % 64 == 0 && BN <= 256, "a tile begins on a pair of scale columns");
   static_assert(kAcc1 + BN <= kSfCol && 2 * kSfCols <= 32, "TMEM");
-  static_assert(kPairs == 1 || (CG == 2 && BN == 256 && MCM <= 2 && MCN <= 2), "multicast shapes");
   static_assert(kStages >= 4 && kSmemBytes <= 232448, "shared memory");
 };
 
@@ -85,9 +82,9 @@ struct Tile {
   int32_t g, m0, n0;
 };
 
-// Tiles in order: matrix, then groups of 8 rows of super-tiles with m fastest, so that a wave
+// Tiles in order: matrix, then groups of 8 rows of tiles with m fastest, so that a wave
 // shares columns of B and the group's rows of A in L2.
-template <class Cfg>
+template <int BN, int CG>
 __device__ __forceinline__ Tile tile_at(const Fp8Params& p, int32_t tile) {
   constexpr int kGroup = 8;
   const int32_t per = p.m_tiles * p.n_tiles;
@@ -95,14 +92,19 @@ __device__ __forceinline__ Tile tile_at(const Fp8Params& p, int32_t tile) {
   const int32_t full = kGroup * p.n_tiles, band = rem / full;
   const int32_t rows = min(kGroup, p.m_tiles - band * kGroup);
   const int32_t at = rem - band * full;
-  return {g, (band * kGroup + at % rows) * Cfg::kTileM, at / rows * Cfg::kTileN};
+  return {g, (band * kGroup + at % rows) * (kBM * CG), at / rows * BN};
 }
 
-template <int BN, int CG, int MCM, int MCN>
-__global__ void __launch_bounds__(Fp8Cfg<BN, CG, MCM, MCN>::kThreads, 1)
+// A wait of the whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, DeviceError* err,
+                                          uint32_t where, uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, bounded_wait(bar, parity, err, where, limit_ns));
+}
+
+template <int BN, int CG>
+__global__ void __launch_bounds__(Fp8Cfg<BN, CG>::kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ Fp8Params p) {
-  using Cfg = Fp8Cfg<BN, CG, MCM, MCN>;
-  constexpr int CL = Cfg::kCluster;
+  using Cfg = Fp8Cfg<BN, CG>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -117,20 +119,16 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, MCM, MCN>::kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t crank = CL > 1 ? cluster_ctarank() : 0;
-  const uint32_t rank = crank % CG;                    // CTA within its pair
-  const uint32_t pp = crank / CG;                      // pair within the cluster
-  const uint32_t pm = pp % MCM, pn = pp / MCM;
-  const uint32_t leader_rank = pp * CG;
+  const uint32_t rank = CG > 1 ? cluster_ctarank() : 0;   // CTA within its pair
   const bool leader = rank == 0;
   const int32_t num_tiles = p.G * p.m_tiles * p.n_tiles;
-  const int32_t first_tile = static_cast<int32_t>(blockIdx.x) / CL;
-  const int32_t tile_stride = static_cast<int32_t>(gridDim.x) / CL;
+  const int32_t first_tile = static_cast<int32_t>(blockIdx.x) / CG;
+  const int32_t tile_stride = static_cast<int32_t>(gridDim.x) / CG;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::kStages; ++s) {
       mbar_init(&full_bar[s], 1);
-      mbar_init(&empty_bar[s], Cfg::kPairs);
+      mbar_init(&empty_bar[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull_bar[a], 1);
@@ -156,7 +154,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, MCM, MCN>::kThreads, 1)
     }
   }
   tc_fence_before();
-  if constexpr (CL > 1) cluster_sync(); else __syncthreads();
+  if constexpr (CG > 1) cluster_sync(); else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   // Everything above touches only shared memory, TMEM and the kernel parameters.
@@ -166,15 +164,13 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, MCM, MCN>::kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      constexpr OperandView kView{1, 0, 2, 0};         // (K, rows, G): K-major
       int stage = 0;
       uint32_t phase = 0, armed_mask = 0, parity_mask = 0;
       bool ok = true;
       for (int32_t tile = first_tile; tile < num_tiles && ok; tile += tile_stride) {
-        const Tile t = tile_at<Cfg>(p, tile);
-        const int32_t m_own = t.m0 + static_cast<int32_t>(pm * (kBM * CG) + rank * kBM);
-        const int32_t n_pair = t.n0 + static_cast<int32_t>(pn) * BN;
-        const int32_t n_own = n_pair + static_cast<int32_t>(rank) * Cfg::kBRows;
+        const Tile t = tile_at<BN, CG>(p, tile);
+        const int32_t m_own = t.m0 + static_cast<int32_t>(rank) * kBM;
+        const int32_t n_own = t.n0 + static_cast<int32_t>(rank) * Cfg::kBRows;
         for (int32_t kb = 0; kb < p.num_kb; ++kb) {
           if (!bounded_wait(&empty_bar[stage], phase ^ 1u, p.err, 21, p.wait_limit_ns)) {
             ok = false;
@@ -182,7 +178,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, MCM, MCN>::kThreads, 1)
           }
           const bool scales = (kb & 3) == 0;
           uint32_t bar = 0;
-          if constexpr (CG == 2) bar = mapa_shared(smem_u32(&full_bar[stage]), leader_rank);
+          if constexpr (CG == 2) bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
           if (leader)
             mbar_arrive_expect_tx(&full_bar[stage],
                                   CG * (Cfg::kABytes + Cfg::kBBytes + (scales ? Cfg::kSfBytes : 0)));
@@ -191,27 +187,17 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, MCM, MCN>::kThreads, 1)
           uint8_t* dA = sA + stage * Cfg::kABytes;
           uint8_t* dB = sB + stage * Cfg::kBBytes;
           uint8_t* dS = sS + stage * Cfg::kSfBytes;
-          if constexpr (MCN == 2) {
-            uint16_t mask = 0;
-            for (uint32_t j = 0; j < MCN; ++j) mask |= 1u << ((j * MCM + pm) * CG + rank);
-            load_operand_mc(&p.tmA, kView, dA + pn * 8192, bar, mask,
-                            m_own + static_cast<int32_t>(pn) * 64, kb * kKBytes, t.g);
+          if constexpr (CG == 2) {
+            tma_load_3d_pair(dA, &p.tmA, bar, kb * kKBytes, m_own, t.g);
+            tma_load_3d_pair(dB, &p.tmB, bar, kb * kKBytes, n_own, t.g);
           } else {
-            load_operand<CG>(&p.tmA, kView, dA, &full_bar[stage], bar, m_own, kb * kKBytes, t.g, kBM);
-          }
-          if constexpr (MCM == 2) {
-            uint16_t mask = 0;
-            for (uint32_t i = 0; i < MCM; ++i) mask |= 1u << ((pn * MCM + i) * CG + rank);
-            load_operand_mc(&p.tmB, kView, dB + pm * 8192, bar, mask,
-                            n_own + static_cast<int32_t>(pm) * 64, kb * kKBytes, t.g);
-          } else {
-            load_operand<CG>(&p.tmB, kView, dB, &full_bar[stage], bar, n_own, kb * kKBytes, t.g,
-                             Cfg::kBRows);
+            tma_load_3d(dA, &p.tmA, &full_bar[stage], kb * kKBytes, m_own, t.g);
+            tma_load_3d(dB, &p.tmB, &full_bar[stage], kb * kKBytes, n_own, t.g);
           }
           if (scales) {
-            // this CTA's rows of A, all the pair's columns of B
+            // this CTA's rows of A, all the tile's columns of B
             const int32_t ra = t.g * p.a_row_tiles + m_own / 128;
-            const int32_t rb = t.g * p.b_row_tiles + n_pair / 128;
+            const int32_t rb = t.g * p.b_row_tiles + t.n0 / 128;
             if constexpr (CG == 2) {
               tma_load_3d_pair(dS, &p.tmSA, bar, 0, kb >> 2, ra);
               tma_load_3d_pair(dS + kScaleTile, &p.tmSB, bar, 0, kb >> 2, rb);
@@ -244,7 +230,10 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, MCM, MCN>::kThreads, 1)
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
-    if (lane == 0 && leader) {
+    // The whole warp runs the loop and one elected lane issues: with the loop itself on one
+    // lane, the descriptors live in ordinary registers and each MMA took about 250 cycles to
+    // issue, twice its execution (8192^3: 335 us, so 292 us).
+    if (leader) {
       int stage = 0;
       uint32_t phase = 0, sf = 0;                      // sf: which scale buffer
       const uint32_t idesc = idesc_mxf8_f32(kBM * CG, BN, p.a_fmt, p.b_fmt);
@@ -258,51 +247,64 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, MCM, MCN>::kThreads, 1)
         // where the two share columns, those of the last tile, which comes after that.
         const int wait_acc = Cfg::kOverlap ? acc ^ 1 : acc;
         const uint32_t uses = static_cast<uint32_t>(Cfg::kOverlap ? (it + 1) >> 1 : it >> 1);
-        if (!bounded_wait(&tfree_bar[wait_acc], (uses & 1u) ^ 1u, p.err, 22, p.wait_limit_ns)) {
+        if (!warp_wait(&tfree_bar[wait_acc], (uses & 1u) ^ 1u, p.err, 22, p.wait_limit_ns)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        const Tile t = tile_at<BN, CG>(p, tile);
         const uint32_t d_tmem = tmem_base + acc * Cfg::kAcc1;
-        uint32_t sa = 0, sb = 0;
+        const uint32_t sb_at = 4 + ((t.n0 & 127) >> 5);  // the first row within its scale tile
+        uint32_t sa = 0;
         for (int32_t kb = 0; kb < p.num_kb; ++kb) {
-          if (!bounded_wait(&full_bar[stage], phase, p.err, 23, p.wait_limit_ns)) {
+          if (!warp_wait(&full_bar[stage], phase, p.err, 23, p.wait_limit_ns)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          if ((kb & 3) == 0) {
+          const bool scales = (kb & 3) == 0;
+          if (scales) {
             sa = tmem_base + Cfg::kSfCol + sf * 16;
-            sb = sa + 4;
             sf ^= 1u;
-            const uint32_t at = s0 + stage * Cfg::kSfBytes;
-            tc_cp_scales<CG>(sa, smem_desc_scales(at));
-#pragma unroll
-            for (int i = 0; i < Cfg::kSfTilesB; ++i)
-              tc_cp_scales<CG>(sb + 4 * i, smem_desc_scales(at + kScaleTile * (1 + i)));
           }
           const uint64_t ad = hi | (((a0 + stage * Cfg::kABytes) >> 4) & 0x3FFFu);
           const uint64_t bd = hi | (((b0 + stage * Cfg::kBBytes) >> 4) & 0x3FFFu);
+          const uint64_t sd = smem_desc_scales(s0 + stage * Cfg::kSfBytes);
           const uint32_t id = idesc | idesc_scale_id(kb & 3);
+          if (elect_one()) {
+            if (scales) {
 #pragma unroll
-          for (int kk = 0; kk < kKBytes / 32; ++kk)
-            tc_mma_mxf8<CG>(d_tmem, ad + 2 * kk, bd + 2 * kk, id, sa, sb, (kk | kb) != 0);
-          if constexpr (CG == 2)
-            tc_commit_pair_mc(&empty_bar[stage], static_cast<uint16_t>((1u << CL) - 1u));
-          else
-            tc_commit(&empty_bar[stage]);
+              for (int i = 0; i <= Cfg::kSfTilesB; ++i)
+                tc_cp_scales<CG>(sa + 4 * i, sd + i * (kScaleTile >> 4));
+            }
+#pragma unroll
+            for (int kk = 0; kk < kKBytes / 32; ++kk)
+              tc_mma_mxf8<CG>(d_tmem, ad + 2 * kk, bd + 2 * kk, id, sa, sa + sb_at,
+                              kk > 0 ? 1u : (kb > 0 ? 1u : 0u));
+            if constexpr (CG == 2)
+              tc_commit_pair_mc(&empty_bar[stage], static_cast<uint16_t>(3));
+            else
+              tc_commit(&empty_bar[stage]);
+          }
+          __syncwarp();
           if (++stage == Cfg::kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if constexpr (CG == 2)
-          tc_commit_pair_mc(&tfull_bar[acc], static_cast<uint16_t>(0x3u << leader_rank));
-        else
-          tc_commit(&tfull_bar[acc]);
+        if (elect_one()) {
+          if constexpr (CG == 2)
+            tc_commit_pair_mc(&tfull_bar[acc], static_cast<uint16_t>(3));
+          else
+            tc_commit(&tfull_bar[acc]);
+        }
+        __syncwarp();
       }
       // every MMA issued here is complete before TMEM is released
-      if constexpr (CG == 2) tc_commit_pair(done_bar); else tc_commit(done_bar);
+      if (elect_one()) {
+        if constexpr (CG == 2) tc_commit_pair(done_bar); else tc_commit(done_bar);
+      }
+      __syncwarp();
       const uint64_t t0 = globaltimer_ns();
       while (!mbar_try_wait(done_bar, 0)) {
         if (globaltimer_ns() - t0 > p.wait_limit_ns) {
@@ -310,6 +312,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, MCM, MCN>::kThreads, 1)
           break;
         }
       }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------- epilogue
@@ -321,9 +324,8 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, MCM, MCN>::kThreads, 1)
     int32_t it = 0;
     for (int32_t tile = first_tile; tile < num_tiles; tile += tile_stride, ++it) {
       const int acc = it & 1;
-      const Tile t = tile_at<Cfg>(p, tile);
-      const int32_t row0 = t.m0 + static_cast<int32_t>(pm * (kBM * CG) + rank * kBM) + q * 32;
-      const int32_t n_pair = t.n0 + static_cast<int32_t>(pn) * BN;
+      const Tile t = tile_at<BN, CG>(p, tile);
+      const int32_t row0 = t.m0 + static_cast<int32_t>(rank) * kBM + q * 32;
       const int32_t row = row0 + lane;
       const float scale = p.row_scale != nullptr && row < p.M ? p.row_scale[row] : 1.0f;
       const uint32_t t_row =
@@ -344,12 +346,12 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, MCM, MCN>::kThreads, 1)
           __syncwarp();
           if (lane == 0) {
             if constexpr (CG == 2)
-              mbar_arrive_cluster(mapa_shared(smem_u32(&tfree_bar[acc]), leader_rank));
+              mbar_arrive_cluster(mapa_shared(smem_u32(&tfree_bar[acc]), 0));
             else
               mbar_arrive(&tfree_bar[acc]);
           }
         }
-        const int32_t col0 = n_pair + c * 32;
+        const int32_t col0 = t.n0 + c * 32;
         uint32_t pk[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
@@ -364,7 +366,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG, MCM, MCN>::kThreads, 1)
   }
 
   tc_fence_before();
-  if constexpr (CL > 1) cluster_sync(); else __syncthreads();
+  if constexpr (CG > 1) cluster_sync(); else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     if constexpr (CG == 2) tmem_dealloc_pair(tmem_base, 512);
@@ -385,20 +387,19 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, int CG, int MCM, int MCN>
+template <int BN, int CG>
 cudaError_t launch_shape(const Fp8GemmParams& g, cudaStream_t stream) {
-  using Cfg = Fp8Cfg<BN, CG, MCM, MCN>;
-  constexpr int CL = Cfg::kCluster;
-  const auto kern = fp8_gemm_kernel<BN, CG, MCM, MCN>;
+  using Cfg = Fp8Cfg<BN, CG>;
+  const auto kern = fp8_gemm_kernel<BN, CG>;
   const boost_fp8_matmul_desc& d = g.d;
   Fp8Params p;
   std::memset(&p, 0, sizeof(p));
   const uint64_t M = d.M, N = d.N, K = d.K, G = d.G;
   const uint64_t kt = scale_tiles_k(d.K), ra = (M + 127) / 128, rb = (N + 127) / 128;
   if (!make_map(&p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.a, K, M, G, d.a_pitch, M * d.a_pitch,
-                kKBytes, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+                kKBytes, kBM, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&p.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.b, K, N, G, d.b_pitch, N * d.b_pitch,
-                kKBytes, 64, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+                kKBytes, Cfg::kBRows, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&p.tmSA, CU_TENSOR_MAP_DATA_TYPE_INT32, g.a_sf, 128, kt, ra * G, kScaleTile,
                 kt * kScaleTile, 128, 1, 1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !make_map(&p.tmSB, CU_TENSOR_MAP_DATA_TYPE_INT32, g.b_sf, 128, kt, rb * G, kScaleTile,
@@ -411,7 +412,7 @@ cudaError_t launch_shape(const Fp8GemmParams& g, cudaStream_t stream) {
   p.G = static_cast<int32_t>(G);
   p.num_kb = static_cast<int32_t>((K + kKBytes - 1) / kKBytes);
   p.m_tiles = static_cast<int32_t>((M + Cfg::kTileM - 1) / Cfg::kTileM);
-  p.n_tiles = static_cast<int32_t>((N + Cfg::kTileN - 1) / Cfg::kTileN);
+  p.n_tiles = static_cast<int32_t>((N + BN - 1) / BN);
   p.a_row_tiles = static_cast<int32_t>(ra);
   p.b_row_tiles = static_cast<int32_t>(rb);
   p.a_fmt = d.a_fmt;
@@ -433,7 +434,7 @@ cudaError_t launch_shape(const Fp8GemmParams& g, cudaStream_t stream) {
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CL;
+  attr[0].val.clusterDim.x = CG;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -444,10 +445,10 @@ cudaError_t launch_shape(const Fp8GemmParams& g, cudaStream_t stream) {
   if (groups == 0) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
     if (e != cudaSuccess) return e;
-    groups = current_num_sms() / CL;
-    if (CL > 1) {
+    groups = current_num_sms() / CG;
+    if (CG > 1) {
       int n = 0;
-      cfg.gridDim = dim3(static_cast<unsigned>(groups * CL), 1, 1);
+      cfg.gridDim = dim3(static_cast<unsigned>(groups * CG), 1, 1);
       if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0)
         groups = std::min(groups, n);
       else
@@ -456,7 +457,7 @@ cudaError_t launch_shape(const Fp8GemmParams& g, cudaStream_t stream) {
     if (dev < 64) resident[dev].store(groups, std::memory_order_release);
   }
   const int64_t tiles = static_cast<int64_t>(p.G) * p.m_tiles * p.n_tiles;
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, groups) * CL), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, groups) * CG), 1, 1);
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
@@ -466,8 +467,11 @@ cudaError_t launch_shape(const Fp8GemmParams& g, cudaStream_t stream) {
 size_t fp8_gemm_workspace(const boost_fp8_matmul_desc&) { return 256; }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmParams& g, cudaStream_t stream) {
-  if (g.d.M <= 128) return launch_shape<128, 1, 1, 1>(g, stream);
-  return launch_shape<256, 2, 1, 1>(g, stream);
+  static const int shape = getenv("FP8_SHAPE") ? atoi(getenv("FP8_SHAPE")) : 0;
+  if (g.d.M <= 128) return launch_shape<128, 1>(g, stream);
+  if (shape == 1) return launch_shape<192, 2>(g, stream);
+  if (shape == 2) return launch_shape<128, 2>(g, stream);
+  return launch_shape<256, 2>(g, stream);
 }
 
 }  // namespace boost_gb300

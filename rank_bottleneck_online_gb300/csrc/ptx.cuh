@@ -416,6 +416,18 @@ __device__ __forceinline__ void tma_load_3d_pair_mc(void* dst, const void* tmap,
 
 namespace boost_gb300 {
 
+// One lane of a converged warp (elect.sync). Code that only this lane runs inside a loop that
+// the whole warp runs keeps its operands in uniform registers, which tcgen05 takes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0u;
+}
+
 // ------------------------------------- 8-bit operands with hardware block scales
 // Instruction descriptor for kind::mxf8f6f4 (8-bit A/B, fp32 D, E8M0 scales) without the
 // scale ids. Formats: 0 e4m3, 1 e5m2; both operands K-major.
