@@ -10,6 +10,7 @@ library is missing, ``lib()`` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -464,28 +465,68 @@ def add(a, b, out=None, stream=None):
     return out
 
 
-def _here(tensors, dtype=None):
-    """Check tensors of one call: on the current device (the stream and the workspace are
-    its), and of one type where given."""
-    device = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if dtype is not None and t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if not t.is_cuda or t.device.index != device:
-            raise ValueError(f"{name} must be on the current CUDA device {device}, not {t.device}")
+# ---------------------------------------------------- operators around the block
+#
+# Small calls are bound by this code, so it checks a tensor in one pass and leaves the
+# words to _refuse; pointers and the stream go to ctypes as plain integers.
+
+def _refuse(t, name, dtype, shape, device):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current CUDA device {device}, not {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _heads(t, name, T=None, dim=None):
-    """Token and head strides of a [T, heads, dim] tensor whose values are adjacent."""
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name} must be [T, heads, dim] with adjacent values")
-    if (T is not None and t.shape[0] != T) or (dim is not None and t.shape[2] != dim):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected T={T}, dim={dim}")
+def _take(t, name, dtype, shape, device):
+    """Address of a contiguous tensor of this type and shape on the current device (the
+    stream and the workspace are its)."""
+    if (t is None or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous()
+            or t.shape != shape):
+        _refuse(t, name, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def _heads(t, name, T, dim, device):
+    """(address, token stride, head stride, heads) of a bf16 [T, heads, dim] tensor whose
+    values are adjacent."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, dim]")
+    t0, heads, d0 = t.shape
+    if t.dtype is not torch.bfloat16 or t.get_device() != device or t0 != T or d0 != dim:
+        _refuse(t.contiguous(), name, torch.bfloat16, (T, heads, dim), device)
+    ts, hs, vs = t.stride()
+    if vs != 1 and dim > 1:
+        raise ValueError(f"{name} must have adjacent values, not a stride of {vs}")
     # the stride of a single token or head says nothing: a plain one in its place
-    return (t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2],
-            t.stride(1) if t.shape[1] > 1 else t.shape[2])
+    return (t.data_ptr(), ts if T > 1 else heads * dim, hs if heads > 1 else dim, heads)
+
+
+@functools.lru_cache(maxsize=512)
+def _rope_desc(T, hq, hk, dim, pairs, axes, interleaved, inverse, pos64, strides, sections,
+               pair_axis):
+    if 2 * pairs > ROPE_MAX_DIM:
+        raise BoostError(2, "boost_rope")
+    D = RopeDesc(T, hq, hk, dim, 2 * pairs, axes, interleaved, inverse, pos64, *strides)
+    if pair_axis is not None:
+        if sections is not None:
+            raise ValueError("sections and pair_axis exclude each other")
+        if len(pair_axis) != pairs or not all(0 <= a < axes for a in pair_axis):
+            raise ValueError(f"pair_axis must give one of {axes} axes for each of {pairs} pairs")
+        D.axis[:pairs] = pair_axis
+    elif sections is not None:
+        if len(sections) != axes or min(sections) < 0 or sum(sections) != pairs:
+            raise ValueError(f"sections must share {pairs} pairs among {axes} axes")
+        D.axis[:pairs] = [a for a, n in enumerate(sections) for _ in range(n)]
+    return D
 
 
 def rope(q, k, positions, inv_freq, *, sections=None, pair_axis=None, interleaved=False,
@@ -499,54 +540,39 @@ def rope(q, k, positions, inv_freq, *, sections=None, pair_axis=None, interleave
     instead. q, k and the outputs take any token and head strides (multiples of 8), so slices
     of a packed projection and [heads, T, dim] tensors seen as [T, heads, dim] are fine, and
     q_out may be q (in place). Positions and frequencies are contiguous."""
-    bf = torch.bfloat16
     if q.dim() != 3:
         raise ValueError("q must be [T, heads, dim]")
-    T, hq, dim = q.shape
-    q_out = torch.empty(q.shape, dtype=bf, device=q.device) if q_out is None else q_out
-    if k is None:
-        if k_out is not None:
-            raise ValueError("k_out without k")
-    elif k_out is None:
-        k_out = torch.empty(k.shape, dtype=bf, device=k.device)
-    _here({"q": q, "k": k, "q_out": q_out, "k_out": k_out}, bf)
-    _here({"positions": positions, "inv_freq": inv_freq})
-    if positions.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
-        raise TypeError("inv_freq must be a float64 vector")
-    if not positions.is_contiguous() or not inv_freq.is_contiguous():
-        raise ValueError("positions and inv_freq must be contiguous")
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if positions.dim() not in (1, 2) or positions.shape[-1] != T:
-        raise ValueError(f"positions has shape {tuple(positions.shape)}, expected [T] or [axes, T]")
-    pairs = inv_freq.numel()
-    if 2 * pairs > ROPE_MAX_DIM:
-        raise BoostError(2, "boost_rope")
-    D = RopeDesc(T=T, hq=hq, hk=0 if k is None else k.shape[1], dim=dim, rot=2 * pairs, axes=axes,
-                 interleaved=bool(interleaved), inverse=bool(inverse),
-                 pos64=positions.dtype == torch.int64)
-    D.q_ts, D.q_hs = _heads(q, "q")
-    D.qo_ts, D.qo_hs = _heads(q_out, "q_out", T, dim)
-    if q_out.shape != q.shape:
-        raise ValueError(f"q_out has shape {tuple(q_out.shape)}, expected {tuple(q.shape)}")
+    device = torch.cuda.current_device()
+    T, _, dim = q.shape
+    qp, q_ts, q_hs, hq = _heads(q, "q", T, dim, device)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    qop, qo_ts, qo_hs, ho = _heads(q_out, "q_out", T, dim, device)
+    kp = kop = None
+    k_ts = k_hs = ko_ts = ko_hs = hk = hko = 0
     if k is not None:
-        D.k_ts, D.k_hs = _heads(k, "k", T, dim)
-        D.ko_ts, D.ko_hs = _heads(k_out, "k_out", T, dim)
-        if k_out.shape != k.shape:
-            raise ValueError(f"k_out has shape {tuple(k_out.shape)}, expected {tuple(k.shape)}")
-    if pair_axis is not None:
-        if sections is not None:
-            raise ValueError("sections and pair_axis exclude each other")
-        if len(pair_axis) != pairs or not all(0 <= a < axes for a in pair_axis):
-            raise ValueError(f"pair_axis must give one of {axes} axes for each of {pairs} pairs")
-        D.axis[:pairs] = list(pair_axis)
-    elif sections is not None:
-        if len(sections) != axes or min(sections) < 0 or sum(sections) != pairs:
-            raise ValueError(f"sections must share {pairs} pairs among {axes} axes")
-        D.axis[:pairs] = [a for a, n in enumerate(sections) for _ in range(n)]
-    _check(lib().boost_rope(ctypes.byref(D), _ptr(q), _ptr(k), _ptr(positions), _ptr(inv_freq),
-                            _ptr(q_out), _ptr(k_out), _stream(stream)), "boost_rope")
+        kp, k_ts, k_hs, hk = _heads(k, "k", T, dim, device)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+        kop, ko_ts, ko_hs, hko = _heads(k_out, "k_out", T, dim, device)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if ho != hq or hko != hk:
+        raise ValueError("an output has another number of heads than its input")
+    pos64 = positions.dtype is torch.int64
+    if not pos64 and positions.dtype is not torch.int32:
+        raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    pp = _take(positions, "positions", positions.dtype,
+               (T,) if positions.dim() == 1 else (axes, T), device)
+    pairs = inv_freq.numel()
+    wp = _take(inv_freq, "inv_freq", torch.float64, (pairs,), device)
+    D = _rope_desc(T, hq, hk, dim, pairs, axes, bool(interleaved), bool(inverse), pos64,
+                   (q_ts, q_hs, k_ts, k_hs, qo_ts, qo_hs, ko_ts, ko_hs),
+                   None if sections is None else tuple(sections),
+                   None if pair_axis is None else tuple(pair_axis))
+    _check(lib().boost_rope(D, qp, kp, pp, wp, qop, kop, _raw_stream(stream, device)),
+           "boost_rope")
     return q_out, k_out
 
 
@@ -554,22 +580,21 @@ def dropout_add(x, p, seed, offset=0, *, residual=None, out=None, counter=None, 
     """residual + dropout(x): the element at flat index e is kept by a pure function of (e,
     seed, offset), so no mask is stored (``boost_dropout``). ``counter``: an int64 tensor of
     one value, added to the offset when the kernel runs, for replayed graphs."""
-    bf = torch.bfloat16
+    bf, shape, device = torch.bfloat16, x.shape, torch.cuda.current_device()
+    xp = _take(x, "x", bf, shape, device)
     if out is None:
-        out = torch.empty(x.shape, dtype=bf, device=x.device)
-    _here({"x": x, "residual": residual, "out": out, "counter": counter})
-    _need(x, "x", bf)
-    _need(out, "out", bf, x.shape)
-    if residual is not None:
-        _need(residual, "residual", bf, x.shape)
+        out = torch.empty(shape, dtype=bf, device=x.device)
+    op = _take(out, "out", bf, shape, device)
+    rp = None if residual is None else _take(residual, "residual", bf, shape, device)
+    cp = None
     if counter is not None:
-        _need(counter, "counter", torch.int64)
         if counter.numel() != 1:
             raise ValueError("counter must hold one value")
+        cp = _take(counter, "counter", torch.int64, counter.shape, device)
     if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
         raise ValueError("seed and offset must be unsigned 64-bit values")
-    _check(lib().boost_dropout(x.numel(), _ptr(x), _ptr(residual), _ptr(out), p, seed, offset,
-                               _ptr(counter), _stream(stream)), "boost_dropout")
+    _check(lib().boost_dropout(x.numel(), xp, rp, op, p, seed, offset, cp,
+                               _raw_stream(stream, device)), "boost_dropout")
     return out
 
 
@@ -580,8 +605,19 @@ def dropout_bwd(dout, p, seed, offset=0, *, dx=None, counter=None, stream=None):
 
 
 def fp8_scale_bytes(rows, K) -> int:
-    """Bytes of the scales of one [rows, K] operand."""
-    return int(lib().boost_fp8_scale_bytes(int(rows), int(K)))
+    """Bytes of the scales of one [rows, K] operand (``boost_fp8_scale_bytes``)."""
+    return -(-rows // 128) * -(-K // 512) * 512
+
+
+def _operand_out(given, name, lead, rows, K, dtype, x, device):
+    """The (values, scales) tensors of a quantised operand and their addresses."""
+    shape, planes = lead + (rows, -(-K // 16) * 16), lead + (fp8_scale_bytes(rows, K),)
+    if given is None:
+        q = torch.empty(shape, dtype=dtype, device=x.device)
+        sf = torch.empty(planes, dtype=torch.uint8, device=x.device)
+        return (q, sf), q.data_ptr(), sf.data_ptr()
+    return (given, _take(given[0], name, dtype, shape, device),
+            _take(given[1], f"{name} scales", torch.uint8, planes, device))
 
 
 def fp8_quantize(x, *, fmt="e4m3", block_rows=1, way="rows", gamma=None, rows_out=None,
@@ -597,45 +633,36 @@ def fp8_quantize(x, *, fmt="e4m3", block_rows=1, way="rows", gamma=None, rows_ou
     if fmt not in FP8_FORMATS or way not in ("rows", "columns", "both"):
         raise ValueError("fmt is 'e4m3' or 'e5m2', way 'rows', 'columns' or 'both'")
     code, dtype = FP8_FORMATS[fmt]
-    if x.dim() not in (2, 3) or (x.shape[-1] > 1 and x.stride(-1) != 1):
+    device = torch.cuda.current_device()
+    if x.dtype is not torch.bfloat16 or x.get_device() != device:
+        _refuse(x, "x", torch.bfloat16, x.shape, device)
+    dims, strides = x.shape, x.stride()
+    if len(dims) not in (2, 3) or (dims[-1] > 1 and strides[-1] != 1):
         raise ValueError("x must be [rows, cols] or [G, rows, cols] with adjacent columns")
-    lead = tuple(x.shape[:-2])
-    G = lead[0] if lead else 1
-    rows, cols = x.shape[-2:]
-    _here({"x": x, "gamma": gamma}, torch.bfloat16)
-    if gamma is not None:
-        _need(gamma, "gamma", torch.bfloat16, (rows,))
-
-    def operand(given, name, r, K, wanted):
-        if not wanted:
-            if given is not None:
-                raise ValueError(f"{name} given, but way is {way!r}")
-            return None
-        shape, planes = lead + (r, -(-K // 16) * 16), lead + (fp8_scale_bytes(r, K),)
-        if given is None:
-            return (torch.empty(shape, dtype=dtype, device=x.device),
-                    torch.empty(planes, dtype=torch.uint8, device=x.device))
-        _here({name: given[0], f"{name} scales": given[1]})
-        _need(given[0], name, dtype, shape)
-        _need(given[1], f"{name} scales", torch.uint8, planes)
-        return given
-
-    by_rows = operand(rows_out, "rows_out", rows, cols, way != "columns")
-    by_cols = operand(cols_out, "cols_out", cols, rows, way != "rows")
+    lead = tuple(dims[:-2])
+    G, (rows, cols) = (lead[0] if lead else 1), dims[-2:]
+    gp = None if gamma is None else _take(gamma, "gamma", torch.bfloat16, (rows,), device)
+    by_rows = by_cols = q = sf = qt = sft = None
+    if way != "columns":
+        by_rows, q, sf = _operand_out(rows_out, "rows_out", lead, rows, cols, dtype, x, device)
+    elif rows_out is not None:
+        raise ValueError("rows_out given, but way is 'columns'")
+    if way != "rows":
+        by_cols, qt, sft = _operand_out(cols_out, "cols_out", lead, cols, rows, dtype, x, device)
+    elif cols_out is not None:
+        raise ValueError("cols_out given, but way is 'rows'")
     # the stride of a single row or matrix says nothing: a plain one in its place
-    D = Fp8QuantDesc(G, rows, cols, x.stride(-2) if rows > 1 else cols,
-                     x.stride(0) if G > 1 else 0, code, block_rows)
-    q, sf = by_rows or (None, None)
-    qt, sft = by_cols or (None, None)
-    _check(lib().boost_fp8_quantize(ctypes.byref(D), _ptr(x), _ptr(gamma), _ptr(q), _ptr(sf),
-                                    _ptr(qt), _ptr(sft), _stream(stream)), "boost_fp8_quantize")
+    D = Fp8QuantDesc(G, rows, cols, strides[-2] if rows > 1 else cols,
+                     strides[0] if G > 1 else 0, code, block_rows)
+    _check(lib().boost_fp8_quantize(D, x.data_ptr(), gp, q, sf, qt, sft,
+                                    _raw_stream(stream, device)), "boost_fp8_quantize")
     return by_rows, by_cols
 
 
 def fp8_matmul_workspace_bytes(M, N, K, G=1) -> int:
     pitch = -(-K // 16) * 16
-    D = Fp8MatmulDesc(G, M, N, K, pitch, pitch, 0, 0, 0)
-    return int(lib().boost_fp8_matmul_workspace_bytes(ctypes.byref(D)))
+    return int(lib().boost_fp8_matmul_workspace_bytes(
+        Fp8MatmulDesc(G, M, N, K, pitch, pitch, 0, 0, 0)))
 
 
 def fp8_matmul(a, a_scales, b, b_scales, K, ws: Workspace, *, row_scale=None, act="identity",
@@ -643,30 +670,27 @@ def fp8_matmul(a, a_scales, b, b_scales, K, ws: Workspace, *, row_scale=None, ac
     """act(row_scale * (A @ B^T)) [M, N] in bf16 of 8-bit operands A [M, pitch], B [N, pitch]
     with their scales (``fp8_quantize``), K values contracted; [G, ...] operands give the G
     products [G, M, N]. row_scale: float32 [M]."""
-    if a.dim() not in (2, 3) or b.dim() != a.dim() or a.shape[:-2] != b.shape[:-2]:
+    device = torch.cuda.current_device()
+    da, db = a.shape, b.shape
+    lead = tuple(da[:-2])
+    if len(da) not in (2, 3) or len(db) != len(da) or tuple(db[:-2]) != lead:
         raise ValueError("operands must be [M, pitch] and [N, pitch], or [G, ...] of them")
-    for name, t in (("a", a), ("b", b)):
-        if t.dtype not in FP8_CODE:
-            raise TypeError(f"{name} must be float8_e4m3fn or float8_e5m2, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    lead = tuple(a.shape[:-2])
-    G = lead[0] if lead else 1
-    M, N = a.shape[-2], b.shape[-2]
+    if a.dtype not in FP8_CODE or b.dtype not in FP8_CODE:
+        raise TypeError(f"operands must be float8_e4m3fn or float8_e5m2, got {a.dtype}, {b.dtype}")
+    G, M, N = (lead[0] if lead else 1), da[-2], db[-2]
     if out is None:
         out = torch.empty(lead + (M, N), dtype=torch.bfloat16, device=a.device)
-    _here({"a": a, "a_scales": a_scales, "b": b, "b_scales": b_scales, "row_scale": row_scale,
-           "out": out, "ws": ws.buf})
-    _need(a_scales, "a_scales", torch.uint8, lead + (fp8_scale_bytes(M, K),))
-    _need(b_scales, "b_scales", torch.uint8, lead + (fp8_scale_bytes(N, K),))
-    _need(out, "out", torch.bfloat16, lead + (M, N))
-    if row_scale is not None:
-        _need(row_scale, "row_scale", torch.float32, (M,))
-    D = Fp8MatmulDesc(G, M, N, K, a.shape[-1], b.shape[-1], FP8_CODE[a.dtype], FP8_CODE[b.dtype],
-                      ACT[act])
-    _check(lib().boost_fp8_matmul(ctypes.byref(D), _ptr(a), _ptr(a_scales), _ptr(b),
-                                  _ptr(b_scales), _ptr(row_scale), _ptr(out), ws.ptr, ws.nbytes,
-                                  _stream(stream)), "boost_fp8_matmul")
+    D = Fp8MatmulDesc(G, M, N, K, da[-1], db[-1], FP8_CODE[a.dtype], FP8_CODE[b.dtype], ACT[act])
+    wb = ws.buf
+    _check(lib().boost_fp8_matmul(
+        D, _take(a, "a", a.dtype, da, device),
+        _take(a_scales, "a_scales", torch.uint8, lead + (fp8_scale_bytes(M, K),), device),
+        _take(b, "b", b.dtype, db, device),
+        _take(b_scales, "b_scales", torch.uint8, lead + (fp8_scale_bytes(N, K),), device),
+        None if row_scale is None else _take(row_scale, "row_scale", torch.float32, (M,), device),
+        _take(out, "out", torch.bfloat16, lead + (M, N), device),
+        _take(wb, "ws", torch.uint8, wb.shape, device), ws.nbytes, _raw_stream(stream, device)),
+        "boost_fp8_matmul")
     return out
 
 

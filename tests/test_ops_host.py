@@ -166,6 +166,8 @@ def test_fp8_quantize_refusals(L, kw, want):
 
 
 def test_fp8_scale_bytes(L):
+    for rows, K in ((1, 1), (128, 512), (129, 513), (0, 4), (4, 0), (300, 11008)):
+        assert B.fp8_scale_bytes(rows, K) == L.boost_fp8_scale_bytes(rows, K)
     assert B.fp8_scale_bytes(1, 1) == 512
     assert B.fp8_scale_bytes(128, 512) == 512
     assert B.fp8_scale_bytes(129, 513) == 2048
