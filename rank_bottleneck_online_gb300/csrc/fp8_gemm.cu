@@ -15,6 +15,9 @@
 // streams operand tiles (128 bytes of K) with TMA, warp 1 issues the MMAs, warps 2..9 read
 // the accumulator and store it. A CTA pair (CG = 2) shares a 256 x BN tile.
 //
+// A few tiles with a long K: the CTAs of a cluster share a tile's K (CG = 1), and each joins a
+// part of its rows from all their parts in shared memory, in a fixed order.
+//
 // TMEM: 512 columns hold two accumulators of 256 less the scales. The second begins at 224
 // and shares 32 columns with the first; the epilogue reads those first and lets the next
 // tile's MMAs start, so the two tiles still overlap but for that read.
@@ -24,7 +27,7 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cstdlib>
+#include <cmath>
 #include <cstring>
 
 #include "fp8.cuh"
@@ -44,6 +47,7 @@ struct Fp8Params {
   int32_t M, N, G, num_kb;
   int32_t m_tiles, n_tiles;            // of 128 CG x BN
   int32_t a_row_tiles, b_row_tiles;    // scale tiles along the rows of one matrix
+  int32_t split, kb_split;             // CTAs that share a tile's K (CG = 1), blocks of each
   int32_t a_fmt, b_fmt, act;
   const float* row_scale;
   __nv_bfloat16* out;
@@ -72,10 +76,12 @@ struct Fp8Cfg {
   static constexpr int kBarOffset = kSfOffset + kStages * kSfBytes;
   static constexpr int kStgOffset = (kBarOffset + kBarBytes + 1023) / 1024 * 1024;
   static constexpr int kSmemBytes = 1024 + kStgOffset + kStgBytes;
+  static constexpr int kPartPitch = BN * 4 + 16;       // bytes a row of a shared tile's part
   static constexpr int kTileM = kBM * CG;
   static_assert(BN % 64 == 0 && BN <= 256, "a tile begins on a pair of scale columns");
   static_assert(kAcc1 + BN <= kSfCol && 2 * kSfCols <= 32, "TMEM");
   static_assert(kStages >= 4 && kSmemBytes <= 232448, "shared memory");
+  static_assert(kBM * kPartPitch <= kSfOffset, "the part fits the operand ring");
 };
 
 struct Tile {
@@ -119,11 +125,16 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG>::kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG > 1 ? cluster_ctarank() : 0;   // CTA within its pair
+  const uint32_t crank = cluster_ctarank();
+  const uint32_t rank = CG > 1 ? crank : 0;            // CTA within its pair
   const bool leader = rank == 0;
   const int32_t num_tiles = p.G * p.m_tiles * p.n_tiles;
-  const int32_t first_tile = static_cast<int32_t>(blockIdx.x) / CG;
-  const int32_t tile_stride = static_cast<int32_t>(gridDim.x) / CG;
+  // With a shared K a cluster of `split` CTAs has one tile, and this CTA blocks [kb0, kb1).
+  const int32_t ctas = CG > 1 ? CG : p.split;
+  const int32_t first_tile = static_cast<int32_t>(blockIdx.x) / ctas;
+  const int32_t tile_stride = static_cast<int32_t>(gridDim.x) / ctas;
+  const int32_t kb0 = CG > 1 ? 0 : static_cast<int32_t>(crank) * p.kb_split;
+  const int32_t kb1 = min(p.num_kb, kb0 + p.kb_split);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::kStages; ++s) {
@@ -163,71 +174,72 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, armed_mask = 0, parity_mask = 0;
-      bool ok = true;
-      for (int32_t tile = first_tile; tile < num_tiles && ok; tile += tile_stride) {
-        const Tile t = tile_at<BN, CG>(p, tile);
-        const int32_t m_own = t.m0 + static_cast<int32_t>(rank) * kBM;
-        const int32_t n_own = t.n0 + static_cast<int32_t>(rank) * Cfg::kBRows;
-        for (int32_t kb = 0; kb < p.num_kb; ++kb) {
-          if (!bounded_wait(&empty_bar[stage], phase ^ 1u, p.err, 21, p.wait_limit_ns)) {
-            ok = false;
-            break;
-          }
-          const bool scales = (kb & 3) == 0;
-          uint32_t bar = 0;
-          if constexpr (CG == 2) bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
-          if (leader)
-            mbar_arrive_expect_tx(&full_bar[stage],
-                                  CG * (Cfg::kABytes + Cfg::kBBytes + (scales ? Cfg::kSfBytes : 0)));
-          armed_mask |= 1u << stage;
-          parity_mask = (parity_mask & ~(1u << stage)) | (phase << stage);
+    // (as the MMA issuer: the whole warp runs the loop, an elected lane issues)
+    int stage = 0;
+    uint32_t phase = 0, armed_mask = 0, parity_mask = 0;
+    bool ok = true;
+    for (int32_t tile = first_tile; tile < num_tiles && ok; tile += tile_stride) {
+      const Tile t = tile_at<BN, CG>(p, tile);
+      const int32_t m_own = t.m0 + static_cast<int32_t>(rank) * kBM;
+      const int32_t n_own = t.n0 + static_cast<int32_t>(rank) * Cfg::kBRows;
+      // scale tiles: of this CTA's rows of A and all the tile's columns of B
+      const int32_t ra = t.g * p.a_row_tiles + m_own / 128;
+      const int32_t rb = t.g * p.b_row_tiles + t.n0 / 128;
+      for (int32_t kb = kb0; kb < kb1; ++kb) {
+        if (!warp_wait(&empty_bar[stage], phase ^ 1u, p.err, 21, p.wait_limit_ns)) {
+          ok = false;
+          break;
+        }
+        const bool scales = (kb & 3) == 0 || kb == kb0;
+        armed_mask |= 1u << stage;
+        parity_mask = (parity_mask & ~(1u << stage)) | (phase << stage);
+        if (elect_one()) {
           uint8_t* dA = sA + stage * Cfg::kABytes;
           uint8_t* dB = sB + stage * Cfg::kBBytes;
           uint8_t* dS = sS + stage * Cfg::kSfBytes;
+          if (leader)
+            mbar_arrive_expect_tx(&full_bar[stage],
+                                  CG * (Cfg::kABytes + Cfg::kBBytes + (scales ? Cfg::kSfBytes : 0)));
           if constexpr (CG == 2) {
+            const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
             tma_load_3d_pair(dA, &p.tmA, bar, kb * kKBytes, m_own, t.g);
             tma_load_3d_pair(dB, &p.tmB, bar, kb * kKBytes, n_own, t.g);
+            if (scales) {
+              tma_load_3d_pair(dS, &p.tmSA, bar, 0, kb >> 2, ra);
+              tma_load_3d_pair(dS + kScaleTile, &p.tmSB, bar, 0, kb >> 2, rb);
+            }
           } else {
             tma_load_3d(dA, &p.tmA, &full_bar[stage], kb * kKBytes, m_own, t.g);
             tma_load_3d(dB, &p.tmB, &full_bar[stage], kb * kKBytes, n_own, t.g);
-          }
-          if (scales) {
-            // this CTA's rows of A, all the tile's columns of B
-            const int32_t ra = t.g * p.a_row_tiles + m_own / 128;
-            const int32_t rb = t.g * p.b_row_tiles + t.n0 / 128;
-            if constexpr (CG == 2) {
-              tma_load_3d_pair(dS, &p.tmSA, bar, 0, kb >> 2, ra);
-              tma_load_3d_pair(dS + kScaleTile, &p.tmSB, bar, 0, kb >> 2, rb);
-            } else {
+            if (scales) {
               tma_load_3d(dS, &p.tmSA, &full_bar[stage], 0, kb >> 2, ra);
               tma_load_3d(dS + kScaleTile, &p.tmSB, &full_bar[stage], 0, kb >> 2, rb);
             }
           }
-          if (++stage == Cfg::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (++stage == Cfg::kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      // the copies started here have landed before the CTA exits (both CTAs' complete on the
-      // even CTA's barriers)
-      if (leader) {
-        for (int s = 0; s < Cfg::kStages; ++s) {
-          if (armed_mask & (1u << s)) {
-            const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(&full_bar[s], (parity_mask >> s) & 1u)) {
-              if (globaltimer_ns() - t0 > p.wait_limit_ns) {
-                record_error(p.err, kErrTimeout, 27);
-                break;
-              }
+    }
+    // the copies started here have landed before the CTA exits (both CTAs' complete on the
+    // even CTA's barriers)
+    if (leader) {
+      for (int s = 0; s < Cfg::kStages; ++s) {
+        if (armed_mask & (1u << s)) {
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(&full_bar[s], (parity_mask >> s) & 1u)) {
+            if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+              record_error(p.err, kErrTimeout, 27);
+              break;
             }
           }
         }
       }
     }
+    __syncwarp();
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
     // The whole warp runs the loop and one elected lane issues: with the loop itself on one
@@ -256,13 +268,13 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG>::kThreads, 1)
         const uint32_t d_tmem = tmem_base + acc * Cfg::kAcc1;
         const uint32_t sb_at = 4 + ((t.n0 & 127) >> 5);  // the first row within its scale tile
         uint32_t sa = 0;
-        for (int32_t kb = 0; kb < p.num_kb; ++kb) {
+        for (int32_t kb = kb0; kb < kb1; ++kb) {
           if (!warp_wait(&full_bar[stage], phase, p.err, 23, p.wait_limit_ns)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const bool scales = (kb & 3) == 0;
+          const bool scales = (kb & 3) == 0 || kb == kb0;
           if (scales) {
             sa = tmem_base + Cfg::kSfCol + sf * 16;
             sf ^= 1u;
@@ -280,7 +292,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG>::kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < kKBytes / 32; ++kk)
               tc_mma_mxf8<CG>(d_tmem, ad + 2 * kk, bd + 2 * kk, id, sa, sa + sb_at,
-                              kk > 0 ? 1u : (kb > 0 ? 1u : 0u));
+                              kk > 0 ? 1u : (kb > kb0 ? 1u : 0u));
             if constexpr (CG == 2)
               tc_commit_pair_mc(&empty_bar[stage], static_cast<uint16_t>(3));
             else
@@ -335,6 +347,22 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG>::kThreads, 1)
         break;
       tc_fence_after();
       constexpr int kChunks = BN / 64;                 // of one warp
+      if (CG == 1 && p.split > 1) {
+        // this CTA's part of the tile to shared memory (the ring: its operands are used up)
+        float* mine = reinterpret_cast<float*>(smem + (q * 32 + lane) * Cfg::kPartPitch);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int c = 2 * i + half;
+          float v[32];
+          tmem_ld_32x32b_x32(t_row + c * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(mine + c * 32 + j) =
+                make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+        break;                                         // (one tile a cluster)
+      }
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         const int c = 2 * (acc == 0 ? kChunks - 1 - i : i) + half;
@@ -365,8 +393,31 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG>::kThreads, 1)
     __syncwarp();
   }
 
+  if (CG == 1 && p.split > 1) {
+    // The parts are summed in the CTAs' order; each CTA takes every split-th row.
+    cluster_sync();
+    constexpr int kVec = BN / 4;
+    const Tile t = tile_at<BN, CG>(p, first_tile);
+    const int32_t rows = (min(kBM, p.M - t.m0) - static_cast<int32_t>(crank) + p.split - 1) / p.split;
+    for (int32_t i = threadIdx.x; i < rows * kVec; i += Cfg::kThreads) {
+      const int32_t r = i / kVec * p.split + static_cast<int32_t>(crank), c = i % kVec * 4;
+      if (t.n0 + c >= p.N) continue;
+      const uint32_t at = smem_u32(smem) + r * Cfg::kPartPitch + c * 4;
+      float4 v = ld_cluster_f4(mapa_shared(at, 0));
+      for (int32_t k = 1; k < p.split; ++k) {
+        const float4 w = ld_cluster_f4(mapa_shared(at, k));
+        v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+      }
+      const int32_t row = t.m0 + r;
+      const float f = p.row_scale != nullptr ? p.row_scale[row] : 1.0f;
+      *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(t.g) * p.M + row) * p.N + t.n0 + c) =
+          make_uint2(pack_bf16x2(act_fwd(v.x * f, p.act), act_fwd(v.y * f, p.act)),
+                     pack_bf16x2(act_fwd(v.z * f, p.act), act_fwd(v.w * f, p.act)));
+    }
+  }
+  // (a CTA whose shared memory others read stays until they have)
   tc_fence_before();
-  if constexpr (CG > 1) cluster_sync(); else __syncthreads();
+  if (CG > 1 || p.split > 1) cluster_sync(); else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     if constexpr (CG == 2) tmem_dealloc_pair(tmem_base, 512);
@@ -387,8 +438,9 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// `split` CTAs of a cluster share a tile's K (CG = 1).
 template <int BN, int CG>
-cudaError_t launch_shape(const Fp8GemmParams& g, cudaStream_t stream) {
+cudaError_t launch_shape(const Fp8GemmParams& g, int split, cudaStream_t stream) {
   using Cfg = Fp8Cfg<BN, CG>;
   const auto kern = fp8_gemm_kernel<BN, CG>;
   const boost_fp8_matmul_desc& d = g.d;
@@ -415,6 +467,9 @@ cudaError_t launch_shape(const Fp8GemmParams& g, cudaStream_t stream) {
   p.n_tiles = static_cast<int32_t>((N + BN - 1) / BN);
   p.a_row_tiles = static_cast<int32_t>(ra);
   p.b_row_tiles = static_cast<int32_t>(rb);
+  // every CTA of a cluster has a block at least
+  p.kb_split = (p.num_kb + split - 1) / split;
+  p.split = (p.num_kb + p.kb_split - 1) / p.kb_split;
   p.a_fmt = d.a_fmt;
   p.b_fmt = d.b_fmt;
   p.act = d.act;
@@ -458,6 +513,10 @@ cudaError_t launch_shape(const Fp8GemmParams& g, cudaStream_t stream) {
   }
   const int64_t tiles = static_cast<int64_t>(p.G) * p.m_tiles * p.n_tiles;
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, groups) * CG), 1, 1);
+  if (CG == 1 && p.split > 1) {
+    attr[0].val.clusterDim.x = p.split;
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split), 1, 1);
+  }
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
@@ -466,12 +525,42 @@ cudaError_t launch_shape(const Fp8GemmParams& g, cudaStream_t stream) {
 
 size_t fp8_gemm_workspace(const boost_fp8_matmul_desc&) { return 256; }
 
+// Launch shape by a model of its time in microseconds, fitted to 44 sizes (M from 1 to 1024,
+// N x K from 1536 x 2048 to 11008 x 1024; most are within 15%):
+//   CTA pairs, 256 x 256:  7 + waves (0.7 + 0.265 blocks of K)
+//   single CTAs, 128 x 128:  6 + waves (0.4 + 0.225 blocks): a CTA's operands arrive at the
+//     SM's 64 bytes a cycle from L2, so the smaller tile's block is hardly quicker and only
+//     wins by using more SMs (M = 512, 4096 x 4096: 14.5 against 16.6 us)
+//   the same with K shared by a cluster:  7.5 + 0.225 of its blocks + 2.2 to join 128 rows,
+//     all of that once more for every further wave of clusters (M = 1, 1024 x 11008: 25.4 us
+//     on 8 CTAs, 9.7 us on 64)
 cudaError_t launch_fp8_gemm(const Fp8GemmParams& g, cudaStream_t stream) {
-  static const int shape = getenv("FP8_SHAPE") ? atoi(getenv("FP8_SHAPE")) : 0;
-  if (g.d.M <= 128) return launch_shape<128, 1>(g, stream);
-  if (shape == 1) return launch_shape<192, 2>(g, stream);
-  if (shape == 2) return launch_shape<128, 2>(g, stream);
-  return launch_shape<256, 2>(g, stream);
+  const boost_fp8_matmul_desc& d = g.d;
+  const int sms = current_num_sms();
+  const double blocks = static_cast<double>((d.K + kKBytes - 1) / kKBytes);
+  auto waves = [&](int64_t m, int64_t n, int64_t slots) {
+    const int64_t tiles = d.G * ((d.M + m - 1) / m) * ((d.N + n - 1) / n);
+    return static_cast<double>((tiles + slots - 1) / std::max<int64_t>(slots, 1));
+  };
+  double best = 7.0 + waves(256, 256, sms / 2) * (0.7 + 0.265 * blocks);
+  int split = 0;                         // 0: CTA pairs
+  const double single = 6.0 + waves(128, 128, sms) * (0.4 + 0.225 * blocks);
+  if (single < best) {
+    best = single;
+    split = 1;
+  }
+  for (int c = 2; c <= 8 && c <= blocks; ++c) {
+    // (clusters sit inside one of eight GPCs of 18 to 20 SMs; 15 of eight CTAs fit)
+    const int slots = (sms / 8 - 1) / c * 8 - (c == 8);
+    const double join = 2.2 * std::min<int64_t>(d.M, 128) / 128.0;
+    const double t = waves(128, 128, slots) * (7.5 + 0.225 * std::ceil(blocks / c) + join);
+    if (t < best) {
+      best = t;
+      split = c;
+    }
+  }
+  if (split == 0) return launch_shape<256, 2>(g, 1, stream);
+  return launch_shape<128, 1>(g, split, stream);
 }
 
 }  // namespace boost_gb300

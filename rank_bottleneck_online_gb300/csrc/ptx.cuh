@@ -331,6 +331,16 @@ __device__ __forceinline__ void cluster_sync() {
                    : "memory");
 }
 
+// 16 bytes of a CTA's shared memory, at a cluster address.
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // Arrive on a barrier of another CTA of the cluster (default .release.cta semantics:
 // no cluster-scope fence; callers order their tcgen05 reads with tcgen05 fences).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
