@@ -82,7 +82,7 @@ __device__ __forceinline__ uint32_t mend_inf(uint32_t bits16, uint32_t q8) {
 
 // 8 values (a vector's four words) times `inv` to 8 bytes.
 template <int FMT>
-__device__ __forceinline__ uint2 quant8(const uint32_t (&w)[4], float inv, bool inf) {
+__device__ __forceinline__ uint2 quant8(const uint32_t* w, float inv, bool inf) {
   uint32_t p[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) p[i] = to8<FMT>(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
@@ -95,6 +95,54 @@ __device__ __forceinline__ uint2 quant8(const uint32_t (&w)[4], float inv, bool 
   return make_uint2(p[0] | p[1] << 16, p[2] | p[3] << 16);
 }
 
+// Largest magnitudes of kRows rows over the kLanes lanes (a power of two) that hold a block, in
+// `top`: with infinities where there are some, and those then again over the finite values,
+// which is what the scale comes from. Two rows go through the shuffles in the halves of a
+// word. Returns a bit for each row whose block holds an infinity.
+template <int kRows, int kWords, int kLanes>
+__device__ __forceinline__ uint32_t block_tops(const uint32_t (&w)[kRows][kWords],
+                                               uint32_t (&top)[kRows]) {
+  uint32_t two[kRows / 2];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    uint32_t m = w[r][0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < kWords; ++i) m = max2(m, w[r][i] & 0x7fff7fffu);
+    top[r] = m;
+  }
+#pragma unroll
+  for (int r = 0; r < kRows / 2; ++r)              // the larger half of each row's word
+    two[r] = max2(__byte_perm(top[2 * r], top[2 * r + 1], 0x5410),
+                  __byte_perm(top[2 * r], top[2 * r + 1], 0x7632));
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1)
+#pragma unroll
+    for (int r = 0; r < kRows / 2; ++r)
+      two[r] = max2(two[r], __shfl_xor_sync(0xffffffffu, two[r], o));
+  uint32_t inf = 0;
+#pragma unroll
+  for (int r = 0; r < kRows / 2; ++r) {
+    // (a block of NaN alone leaves a NaN here: no finite value, as 0)
+    top[2 * r] = two[r] & 0xffffu;
+    top[2 * r + 1] = two[r] >> 16;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) inf |= (top[2 * r + h] >= kInf ? 1u : 0u) << (2 * r + h);
+  }
+  if (__any_sync(0xffffffffu, inf != 0)) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      uint32_t f = 0;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) f = max2(f, finite2(w[r][i]));
+      f = larger_half(f);
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) f = max(f, __shfl_xor_sync(0xffffffffu, f, o));
+      if (inf >> r & 1) top[r] = f;
+    }
+  }
+  return inf;
+}
+
 // ------------------------------------------------------------------- rows alone
 // A warp takes rows of 512 columns: 8 lanes a block of 128, 16 values a lane, four rows in
 // flight. A block of 8 warps covers 32 rows. grid = (scale tiles along the columns,
@@ -105,66 +153,41 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const QuantParams 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 512 + lane * 16;
   const int64_t row0 = static_cast<int64_t>(blockIdx.y) * 32 + warp * 4;
-  const int64_t blocks = (p.cols + 127) / 128;
-  const __nv_bfloat16* x = p.x + blockIdx.z * p.gstride;
-  uint32_t w[4][2][4];
+  const int rows = static_cast<int>(min(max(p.rows - row0, static_cast<int64_t>(0)),
+                                        static_cast<int64_t>(4)));
+  const __nv_bfloat16* x = p.x + blockIdx.z * p.gstride + row0 * p.ldx + col;
+  uint32_t w[4][8];
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint4 v = make_uint4(0, 0, 0, 0);
-      if (row0 + r < p.rows && col + 8 * h < p.cols)
-        v = __ldg(reinterpret_cast<const uint4*>(x + (row0 + r) * p.ldx + col + 8 * h));
-      w[r][h][0] = v.x; w[r][h][1] = v.y; w[r][h][2] = v.z; w[r][h][3] = v.w;
+      if (r < rows && col + 8 * h < p.cols)
+        v = __ldg(reinterpret_cast<const uint4*>(x + r * p.ldx + 8 * h));
+      w[r][4 * h] = v.x; w[r][4 * h + 1] = v.y; w[r][4 * h + 2] = v.z; w[r][4 * h + 3] = v.w;
     }
   }
-  // largest magnitudes over a block's 8 lanes, two rows in the halves of a word
   uint32_t top[4];
+  const uint32_t infs = block_tops<4, 8, 8>(w, top);
+  uint8_t* q = p.q + (blockIdx.z * p.rows + row0) * p.pitch + col;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * 4;      // block of lane 0
+  uint8_t* sf = p.sf + blockIdx.z * p.plane + scale_at(row0, first, p.kt);
+  const bool in_cols = first + (lane >> 3) < (p.cols + 127) / 128;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max2(m, w[r][i >> 2][i & 3] & 0x7fff7fffu);
-    top[r] = larger_half(m);
-  }
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-#pragma unroll
-    for (int r = 0; r < 4; r += 2) {
-      const uint32_t both = top[r] | top[r + 1] << 16;
-      const uint32_t m = max2(both, __shfl_xor_sync(0xffffffffu, both, o));
-      top[r] = m & 0xffffu;
-      top[r + 1] = m >> 16;
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int64_t row = row0 + r;
-    const bool inf = top[r] == kInf;
-    if (__any_sync(0xffffffffu, inf)) {          // again over the finite values
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max2(m, finite2(w[r][i >> 2][i & 3]));
-      m = larger_half(m);
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (inf) top[r] = m;
-    }
     const uint32_t byte = scale_byte<FMT>(top[r]);
-    if (row < p.rows && col < p.pitch) {
+    if (r < rows && col < p.pitch) {
       const float inv = scale_inverse(byte);
-      const uint2 a = quant8<FMT>(w[r][0], inv, inf), b = quant8<FMT>(w[r][1], inv, inf);
-      *reinterpret_cast<uint4*>(p.q + (blockIdx.z * p.rows + row) * p.pitch + col) =
-          make_uint4(a.x, a.y, b.x, b.y);
+      const bool inf = infs >> r & 1;
+      const uint2 a = quant8<FMT>(w[r], inv, inf), b = quant8<FMT>(w[r] + 4, inv, inf);
+      *reinterpret_cast<uint4*>(q + r * p.pitch) = make_uint4(a.x, a.y, b.x, b.y);
     }
     // the four blocks' bytes, 127 outside the operand
-    const bool in = row < p.rows && static_cast<int64_t>(blockIdx.x) * 4 + (lane >> 3) < blocks;
-    uint32_t word = (in ? byte : 127u) << (lane & 24);
+    uint32_t word = (in_cols && r < rows ? byte : 127u) << (lane & 24);
     word |= __shfl_xor_sync(0xffffffffu, word, 8);
     word |= __shfl_xor_sync(0xffffffffu, word, 16);
-    if (lane == 0)
-      *reinterpret_cast<uint32_t*>(p.sf + blockIdx.z * p.plane +
-                                   scale_at(row, static_cast<int64_t>(blockIdx.x) * 4, p.kt)) = word;
+    // (four rows of one quarter of a scale tile lie 16 bytes apart)
+    if (lane == 0) *reinterpret_cast<uint32_t*>(sf + 16 * r) = word;
   }
 }
 
@@ -172,10 +195,11 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const QuantParams 
 // A block holds one tile in registers: thread (rg, cg), rg = threadIdx.x / 16, has rows
 // 8 rg .. 8 rg + 7 of columns 8 cg .. 8 cg + 7, so that 16 lanes read a row's 256 bytes. The
 // transposed bytes go through shared memory: column c's 128 bytes lie at 128 c, the 8 bytes
-// of row group rg in slot rg ^ (c / 8), which keeps both sides free of bank conflicts.
-// grid = (column tiles, row tiles, matrices).
+// of row group rg in slot rg ^ (c / 8), which keeps both sides free of bank conflicts. The
+// pass is close to the issue rate (about 15 instructions a value for both layouts), so every
+// address is a base and a small stride. grid = (column tiles, row tiles, matrices).
 template <int FMT, bool SQUARE>
-__global__ void __launch_bounds__(kThreads) quant_tile_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kThreads, 4) quant_tile_kernel(const QuantParams p) {
   pdl_enter();
   __shared__ __align__(16) uint8_t bytes[128 * 128];
   __shared__ uint32_t part[2][16][64];  // a row group's column maxima, in pairs:
@@ -184,26 +208,28 @@ __global__ void __launch_bounds__(kThreads) quant_tile_kernel(const QuantParams 
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
   const int64_t row0 = static_cast<int64_t>(blockIdx.y) * 128;
   const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 128;
-  const int64_t col = col0 + cg * 8;
-  const __nv_bfloat16* x = p.x + blockIdx.z * p.gstride;
+  const int64_t row = row0 + rg * 8, col = col0 + cg * 8;          // this thread's first
+  const int rows = static_cast<int>(min(max(p.rows - row, static_cast<int64_t>(0)),
+                                        static_cast<int64_t>(8)));
+  const bool in_cols = col < p.cols;
   uint32_t w[8][4];
+  {
+    const __nv_bfloat16* x = p.x + blockIdx.z * p.gstride + row * p.ldx + col;
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    const int64_t row = row0 + rg * 8 + r;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row < p.rows && col < p.cols)
-      v = __ldg(reinterpret_cast<const uint4*>(x + row * p.ldx + col));
-    w[r][0] = v.x; w[r][1] = v.y; w[r][2] = v.z; w[r][3] = v.w;
+    for (int r = 0; r < 8; ++r) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < rows && in_cols) v = __ldg(reinterpret_cast<const uint4*>(x));
+      x += p.ldx;
+      w[r][0] = v.x; w[r][1] = v.y; w[r][2] = v.z; w[r][3] = v.w;
+    }
   }
   if (p.gamma != nullptr) {
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      const int64_t row = row0 + rg * 8 + r;
-      if (row < p.rows) {
-        const float g = __bfloat162float(p.gamma[row]);
+      if (r < rows && in_cols) {
+        const float g = __bfloat162float(p.gamma[row + r]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (col < p.cols) w[r][i] = pack_bf16x2(g * bf16_lo(w[r][i]), g * bf16_hi(w[r][i]));
+        for (int i = 0; i < 4; ++i) w[r][i] = pack_bf16x2(g * bf16_lo(w[r][i]), g * bf16_hi(w[r][i]));
       }
     }
   }
@@ -211,11 +237,11 @@ __global__ void __launch_bounds__(kThreads) quant_tile_kernel(const QuantParams 
   if (SQUARE || p.qt != nullptr) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint32_t m = 0;
+      uint32_t m = w[0][i] & 0x7fff7fffu;
 #pragma unroll
-      for (int r = 0; r < 8; ++r) m = max2(m, w[r][i] & 0x7fff7fffu);
+      for (int r = 1; r < 8; ++r) m = max2(m, w[r][i] & 0x7fff7fffu);
       uint32_t f = m;
-      if ((m & 0xffffu) == kInf || (m >> 16) == kInf) {
+      if ((m & 0xffffu) >= kInf || (m >> 16) >= kInf) {
         f = 0;
 #pragma unroll
         for (int r = 0; r < 8; ++r) f = max2(f, finite2(w[r][i]));
@@ -233,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) quant_tile_kernel(const QuantParams 
     }
     __syncthreads();
   }
-  uint32_t tile_top = 0;
+  uint32_t tile_byte = 0;
   bool tile_inf = false;
   if constexpr (SQUARE) {
     const int lane = threadIdx.x & 31;
@@ -244,88 +270,67 @@ __global__ void __launch_bounds__(kThreads) quant_tile_kernel(const QuantParams 
       m = max2(m, __shfl_xor_sync(0xffffffffu, m, o));
       f = max2(f, __shfl_xor_sync(0xffffffffu, f, o));
     }
-    tile_top = larger_half(f);
+    tile_byte = scale_byte<FMT>(larger_half(f));
     tile_inf = larger_half(m) == kInf;
   }
 
   if (p.q != nullptr) {
-    const int64_t blocks = (p.cols + 127) / 128;
-    const bool last = blockIdx.x + 1 == gridDim.x;
+    const int64_t b0 = static_cast<int64_t>(blockIdx.x), blocks = (p.cols + 127) / 128;
+    // one byte a block; the last column tile fills its scale tile
+    const int64_t b = b0 + cg;
+    const bool writes = cg == 0 || (b0 + 1 == gridDim.x && b < 4 * p.kt);
+    uint8_t* sf = p.sf + blockIdx.z * p.plane + scale_at(row, b, p.kt);
+    uint8_t* q = p.q + (blockIdx.z * p.rows + row) * p.pitch + col;
+    uint32_t top[8], infs = 0;
+    if constexpr (!SQUARE) infs = block_tops<8, 4, 16>(w, top);
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      const int64_t row = row0 + rg * 8 + r;
-      uint32_t top = tile_top;
-      bool inf = tile_inf;
-      if constexpr (!SQUARE) {
-        top = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max2(top, w[r][i] & 0x7fff7fffu);
-        top = larger_half(top);
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        inf = top == kInf;
-        if (__any_sync(0xffffffffu, inf)) {      // again over the finite values
-          uint32_t f = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f = max2(f, finite2(w[r][i]));
-          f = larger_half(f);
-#pragma unroll
-          for (int o = 1; o < 16; o <<= 1) f = max(f, __shfl_xor_sync(0xffffffffu, f, o));
-          if (inf) top = f;
-        }
-      }
-      const uint32_t byte = scale_byte<FMT>(top);
-      if (row < p.rows && col < p.pitch)
-        *reinterpret_cast<uint2*>(p.q + (blockIdx.z * p.rows + row) * p.pitch + col) =
-            quant8<FMT>(w[r], scale_inverse(byte), inf);
-      // one byte a block; the last column tile fills its scale tile
-      const int64_t b = static_cast<int64_t>(blockIdx.x) + cg;
-      if (cg == 0 || (last && b < 4 * p.kt))
-        p.sf[blockIdx.z * p.plane + scale_at(row, b, p.kt)] =
-            static_cast<uint8_t>(row < p.rows && b < blocks ? byte : 127u);
+      const uint32_t byte = SQUARE ? tile_byte : scale_byte<FMT>(top[r]);
+      if (r < rows && col < p.pitch)
+        *reinterpret_cast<uint2*>(q) =
+            quant8<FMT>(w[r], scale_inverse(byte), SQUARE ? tile_inf : (infs >> r & 1) != 0);
+      q += p.pitch;
+      // (eight rows of one quarter of a scale tile lie 16 bytes apart)
+      if (writes) sf[16 * r] = static_cast<uint8_t>(r < rows && b < blocks ? byte : 127u);
     }
   }
 
   if (p.qt != nullptr) {
-    const int64_t blocks = (p.rows + 127) / 128;
-    const bool last = blockIdx.y + 1 == gridDim.y;
+    const int64_t b0 = static_cast<int64_t>(blockIdx.y), blocks = (p.rows + 127) / 128;
+    const int64_t b = b0 + rg;
+    const bool writes = rg == 0 || (b0 + 1 == gridDim.y && b < 4 * p.kt_t);
+    uint8_t* sf = p.sft + blockIdx.z * p.plane_t + scale_at(col, b, p.kt_t);
+    uint8_t* slot = bytes + cg * 1024 + ((rg ^ cg) * 8);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const uint32_t t = SQUARE ? 0 : col_top[cg * 4 + i], a = SQUARE ? 0 : col_all[cg * 4 + i];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int c = cg * 8 + 2 * i + h;
-        uint32_t top = tile_top;
-        bool inf = tile_inf;
-        if constexpr (!SQUARE) {
-          const uint32_t t = col_top[cg * 4 + i], a = col_all[cg * 4 + i];
-          top = h ? t >> 16 : t & 0xffffu;
-          inf = (h ? a >> 16 : a & 0xffffu) == kInf;
-        }
-        const uint32_t byte = scale_byte<FMT>(top);
+        const int c = 2 * i + h;
+        const uint32_t byte = SQUARE ? tile_byte : scale_byte<FMT>(h ? t >> 16 : t & 0xffffu);
+        const bool inf = SQUARE ? tile_inf : (h ? a >> 16 : a & 0xffffu) == kInf;
         uint32_t v[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)     // rows 2 r and 2 r + 1 of this column
-          v[r] = h ? (w[2 * r][i] >> 16) | (w[2 * r + 1][i] & 0xffff0000u)
-                   : (w[2 * r][i] & 0xffffu) | (w[2 * r + 1][i] << 16);
-        *reinterpret_cast<uint2*>(bytes + c * 128 + ((rg ^ cg) * 8)) =
-            quant8<FMT>(v, scale_inverse(byte), inf);
-        // one byte a block; the last row tile fills its scale tile
-        const int64_t b = static_cast<int64_t>(blockIdx.y) + rg;
-        if (rg == 0 || (last && b < 4 * p.kt_t))
-          p.sft[blockIdx.z * p.plane_t + scale_at(col0 + c, b, p.kt_t)] =
-              static_cast<uint8_t>(col0 + c < p.cols && b < blocks ? byte : 127u);
+          v[r] = __byte_perm(w[2 * r][i], w[2 * r + 1][i], h ? 0x7632 : 0x5410);
+        *reinterpret_cast<uint2*>(slot + c * 128) = quant8<FMT>(v, scale_inverse(byte), inf);
+        if (writes) sf[16 * c] = static_cast<uint8_t>(in_cols && b < blocks ? byte : 127u);
       }
     }
     __syncthreads();
+    // 8 lanes a column, 16 bytes a lane
+    const int c0 = threadIdx.x >> 3, piece = threadIdx.x & 7;
+    const bool in_pitch = row0 + piece * 16 < p.pitch_t;
+    uint8_t* qt = p.qt + (blockIdx.z * p.cols + col0 + c0) * p.pitch_t + row0 + piece * 16;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {       // 8 lanes a column, 16 bytes a lane
-      const int c = k * 32 + (threadIdx.x >> 3), piece = threadIdx.x & 7;
+    for (int k = 0; k < 4; ++k) {
+      const int c = k * 32 + c0;
       const uint8_t* at = bytes + c * 128;
-      const uint2 a = *reinterpret_cast<const uint2*>(at + (((2 * piece) ^ (c >> 3)) * 8));
-      const uint2 b = *reinterpret_cast<const uint2*>(at + (((2 * piece + 1) ^ (c >> 3)) * 8));
-      if (col0 + c < p.cols && row0 + piece * 16 < p.pitch_t)
-        *reinterpret_cast<uint4*>(p.qt + (blockIdx.z * p.cols + col0 + c) * p.pitch_t + row0 +
-                                  piece * 16) = make_uint4(a.x, a.y, b.x, b.y);
+      const uint2 lo = *reinterpret_cast<const uint2*>(at + (((2 * piece) ^ (c >> 3)) * 8));
+      const uint2 hi = *reinterpret_cast<const uint2*>(at + (((2 * piece + 1) ^ (c >> 3)) * 8));
+      if (col0 + c < p.cols && in_pitch)
+        *reinterpret_cast<uint4*>(qt) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      qt += 32 * p.pitch_t;
     }
   }
 }

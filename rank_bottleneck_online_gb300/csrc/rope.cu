@@ -33,6 +33,8 @@ struct RopeParams {
   const double* inv_freq;
   boost_rope_desc d;
   int tok;                         // tokens of one block
+  int units;                       // units of a head
+  int head_step, tok_step;         // heads and tokens that a block turns at a time
 };
 
 // 2^64 w / (2 pi) mod 2^64, from the bits of w (finite).
@@ -143,34 +145,46 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   }
   __syncthreads();
 
+  // A thread keeps its unit of a head and walks over heads and tokens: no division in the
+  // loop (with two a unit, the pass was bound by its integer instructions).
   const int heads = p.d.hq + p.d.hk;
-  const int units = pairs / Unit<P>::kPairs;            // of one head
-  const int items = tokens * heads * units;
   constexpr int kBatch = P == kHalf8 ? 2 : 4;           // units in flight a thread
-  for (int first = threadIdx.x; first < items; first += kBatch * kThreads) {
+  const int slot = threadIdx.x / p.units, u = threadIdx.x - slot * p.units;
+  int t = slot / p.head_step, h = slot - t * p.head_step;
+  if (t >= p.tok_step) t = tokens;                      // (threads past the last whole slot)
+  const int h0 = h;
+  const int angle0 = u * Unit<P>::kPairs;
+  while (t < tokens) {
     Unit<P> v[kBatch];
+    __nv_bfloat16* to[kBatch];
+    int at[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int item = first + b * kThreads;
-      if (item < items) {
-        const int th = item / units, t = th / heads;
-        v[b].load(head_in(p, t0 + t, th - t * heads), item - th * units, pairs);
+      to[b] = nullptr;
+      if (t < tokens) {
+        if (h < heads) {
+          v[b].load(head_in(p, t0 + t, h), u, pairs);
+          to[b] = head_out(p, t0 + t, h);
+          at[b] = t * pairs + angle0;
+        }
+        h += p.head_step;
+        if (h >= heads) {
+          h = h0;
+          t += p.tok_step;
+        }
       }
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int item = first + b * kThreads;
-      if (item < items) {
-        const int th = item / units, t = th / heads, u = item - th * units;
-        const int at = t * pairs + u * Unit<P>::kPairs;
+      if (to[b] != nullptr) {
         float c[Unit<P>::kPairs], s[Unit<P>::kPairs];
 #pragma unroll
         for (int i = 0; i < Unit<P>::kPairs; i += 4) {
-          *reinterpret_cast<float4*>(c + i) = *reinterpret_cast<const float4*>(cs + at + i);
-          *reinterpret_cast<float4*>(s + i) = *reinterpret_cast<const float4*>(sn + at + i);
+          *reinterpret_cast<float4*>(c + i) = *reinterpret_cast<const float4*>(cs + at[b] + i);
+          *reinterpret_cast<float4*>(s + i) = *reinterpret_cast<const float4*>(sn + at[b] + i);
         }
         v[b].turn(c, s);
-        v[b].store(head_out(p, t0 + t, th - t * heads), u, pairs);
+        v[b].store(to[b], u, pairs);
       }
     }
   }
@@ -191,10 +205,16 @@ cudaError_t launch_rope(const RopeParams& p_in, cudaStream_t stream) {
   RopeParams p = p_in;
   const int pairs = p.d.rot / 2;
   const bool adjacent = p.d.interleaved != 0, wide = !adjacent && pairs % 8 == 0;
-  // Tokens of one block: enough that each thread has a batch of units (so that the sine
-  // phase of one block hides behind the loads of the others), and no more.
-  const int64_t units = static_cast<int64_t>(p.d.hq + p.d.hk) * pairs / (wide ? 8 : 4);
-  int64_t tok = std::max<int64_t>(1, kThreads * (wide ? 2 : 4) / units);
+  // A block has room for `slots` units' worth of heads: all heads of one or more tokens, or a
+  // part of one token's heads at a time. It takes tokens until each thread has a batch of
+  // units or two (so that the sine phase of one block hides behind the loads of others).
+  const int heads = p.d.hq + p.d.hk;
+  p.units = pairs / (wide ? 8 : 4);
+  const int slots = kThreads / p.units, batch = wide ? 2 : 4;
+  p.head_step = std::min(heads, slots);
+  p.tok_step = slots / p.head_step;
+  const int64_t passes = (heads + p.head_step - 1) / p.head_step;
+  int64_t tok = std::max<int64_t>(1, batch * p.tok_step / passes);
   tok = std::min<int64_t>({tok, kMaxAngles / pairs, std::max<int64_t>(1, p.d.T / 304)});
   p.tok = static_cast<int>(tok);
   const int64_t grid = (p.d.T + tok - 1) / tok;
