@@ -27,7 +27,7 @@ struct DropoutParams {
   const uint64_t* counter;     // or NULL
   int64_t count;
   uint64_t seed, offset;
-  uint32_t drop;               // draws below this drop the element
+  uint32_t drop;               // 65536 times the draw below which an element is dropped
   float scale;                 // 65536 / (65536 - drop)
 };
 
@@ -48,17 +48,21 @@ __device__ __forceinline__ void philox(uint32_t (&c)[4], uint32_t k0, uint32_t k
   }
 }
 
-// The 8 draws of vector g.
-__device__ __forceinline__ void draws(const DropoutParams& p, uint64_t offset, int64_t g,
-                                      uint32_t (&d)[8]) {
+// Which of vector g's 8 elements are kept, as masks of its words' halves: a draw is compared as
+// the upper half of a word, whose lower half cannot change the answer.
+__device__ __forceinline__ uint4 keep_masks(const DropoutParams& p, uint64_t offset, int64_t g) {
   uint32_t c[4] = {static_cast<uint32_t>(g), static_cast<uint32_t>(g >> 32),
                    static_cast<uint32_t>(offset), static_cast<uint32_t>(offset >> 32)};
   philox(c, static_cast<uint32_t>(p.seed), static_cast<uint32_t>(p.seed >> 32));
+  uint32_t m[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    d[2 * j] = c[j] & 0xffffu;
-    d[2 * j + 1] = c[j] >> 16;
-  }
+  for (int j = 0; j < 4; ++j)
+    m[j] = (c[j] << 16 >= p.drop ? 0xffffu : 0u) | (c[j] >= p.drop ? 0xffff0000u : 0u);
+  return make_uint4(m[0], m[1], m[2], m[3]);
+}
+
+__device__ __forceinline__ uint4 operator&(const uint4& a, const uint4& b) {
+  return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w);
 }
 
 constexpr int kBatch = 2;      // vectors in flight a thread
@@ -82,33 +86,27 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p
   for (int b = 0; b < kBatch; ++b) {
     const int64_t g = first + b * kThreads;
     if (g < vectors) {
-      uint32_t d[8];
       float f[8], s[8];
-      draws(p, offset, g, d);
-      unpack8(x[b], f);
+      unpack8(x[b] & keep_masks(p, offset, g), f);
       if (RES) unpack8(r[b], s);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = d[e] >= p.drop ? f[e] * p.scale : 0.0f;
-        f[e] = RES ? s[e] + v : v;
-      }
+      for (int e = 0; e < 8; ++e) f[e] = RES ? fmaf(f[e], p.scale, s[e]) : f[e] * p.scale;
       p.out[g] = pack8(f);
     }
   }
   // the last, partly filled vector
   const int tail = static_cast<int>(p.count & 7);
   if (blockIdx.x == 0 && threadIdx.x < tail) {
-    uint32_t d[8], mine = 0;
-    draws(p, offset, vectors, d);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j == threadIdx.x) mine = d[j];
+    const uint4 m = keep_masks(p, offset, vectors);
+    const int j = threadIdx.x >> 1;
+    const uint32_t word = j == 0 ? m.x : j == 1 ? m.y : j == 2 ? m.z : m.w;
+    const bool keep = (threadIdx.x & 1 ? word >> 16 : word & 0xffffu) != 0;
     const int64_t e = vectors * 8 + threadIdx.x;
     const float f = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.x)[e]);
-    const float v = mine >= p.drop ? f * p.scale : 0.0f;
-    const float s =
-        RES ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.res)[e]) + v : v;
-    reinterpret_cast<__nv_bfloat16*>(p.out)[e] = __float2bfloat16_rn(s);
+    const float s = RES ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.res)[e]) : 0.0f;
+    const float v = keep ? f : 0.0f;
+    reinterpret_cast<__nv_bfloat16*>(p.out)[e] =
+        __float2bfloat16_rn(RES ? fmaf(v, p.scale, s) : v * p.scale);
   }
 }
 
@@ -150,7 +148,7 @@ extern "C" boost_status boost_dropout(int64_t count, const void* x, const void* 
   d.count = count;
   d.seed = seed;
   d.offset = offset;
-  d.drop = static_cast<uint32_t>(drop);
+  d.drop = static_cast<uint32_t>(drop) << 16;
   d.scale = static_cast<float>(65536.0 / (65536.0 - drop));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t grid = (count / 8 + kBatch * kThreads - 1) / (kBatch * kThreads);

@@ -80,12 +80,28 @@ __device__ __forceinline__ uint32_t mend_inf(uint32_t bits16, uint32_t q8) {
   return ((bits16 >> 8) & 0x80u) | (FMT == BOOST_E4M3 ? 0x7fu : 0x7cu);
 }
 
+// Two products in one instruction.
+__device__ __forceinline__ float2 mul2(float a, float b, float f) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %4};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a), "f"(b), "f"(f));
+  return r;
+}
+
 // 8 values (a vector's four words) times `inv` to 8 bytes.
 template <int FMT>
 __device__ __forceinline__ uint2 quant8(const uint32_t* w, float inv, bool inf) {
   uint32_t p[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) p[i] = to8<FMT>(bf16_lo(w[i]) * inv, bf16_hi(w[i]) * inv);
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = mul2(bf16_lo(w[i]), bf16_hi(w[i]), inv);
+    p[i] = to8<FMT>(v.x, v.y);
+  }
   if (inf) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)

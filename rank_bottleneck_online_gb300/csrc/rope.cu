@@ -53,61 +53,75 @@ __device__ __forceinline__ uint64_t turns_fixed(double w) {
   return (b >> 63) ? 0 - f : f;
 }
 
-// Where the pairs lie: kHalf8 and kHalf4 pair i with i + rot / 2 (vectors of 8 or 4 values
-// of each half), kAdjacent pairs 2 i with 2 i + 1 (a vector of 8 holds 4 pairs).
-enum Pairing { kHalf8, kHalf4, kAdjacent };
+// Where the pairs lie, and how many a thread turns at a time: kHalf pairs i with i + rot / 2
+// (a vector of each half), kAdjacent pairs 2 i with 2 i + 1 (adjacent values).
+enum Pairing { kHalf, kAdjacent };
 
-// The part of one head that a thread turns at a time: a vector of each half, or one vector
-// of adjacent pairs, as words of two bf16 values.
-template <Pairing P>
+// N pairs (8, or 4 where a head's pairs are no multiple of 8) of one head as N words of two
+// bf16 values.
+template <Pairing P, int N>
 struct Unit {
-  static constexpr int kPairs = P == kHalf8 ? 8 : 4;
-  uint32_t w[kPairs];
+  uint32_t w[N];
 
-  __device__ __forceinline__ void load(const __nv_bfloat16* h, int u, int half) {
-    if constexpr (P == kHalf8) {
-      const uint4 a = *reinterpret_cast<const uint4*>(h + 8 * u);
-      const uint4 b = *reinterpret_cast<const uint4*>(h + half + 8 * u);
-      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-    } else if constexpr (P == kHalf4) {
-      const uint2 a = *reinterpret_cast<const uint2*>(h + 4 * u);
-      const uint2 b = *reinterpret_cast<const uint2*>(h + half + 4 * u);
-      w[0] = a.x; w[1] = a.y; w[2] = b.x; w[3] = b.y;
+  // word i of the unit's first (kHalf: N / 2 words of each half)
+  template <int kWords>
+  static __device__ __forceinline__ void words(const __nv_bfloat16* from, uint32_t* to) {
+    if constexpr (kWords == 2) {
+      const uint2 a = *reinterpret_cast<const uint2*>(from);
+      to[0] = a.x; to[1] = a.y;
     } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(h + 8 * u);
-      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 a = *reinterpret_cast<const uint4*>(from + 2 * i);
+        to[i] = a.x; to[i + 1] = a.y; to[i + 2] = a.z; to[i + 3] = a.w;
+      }
+    }
+  }
+  template <int kWords>
+  static __device__ __forceinline__ void put(__nv_bfloat16* to, const uint32_t* from) {
+    if constexpr (kWords == 2) {
+      *reinterpret_cast<uint2*>(to) = make_uint2(from[0], from[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4)
+        *reinterpret_cast<uint4*>(to + 2 * i) = make_uint4(from[i], from[i + 1], from[i + 2], from[i + 3]);
     }
   }
 
-  __device__ __forceinline__ void turn(const float* c, const float* s) {
+  __device__ __forceinline__ void load(const __nv_bfloat16* h, int u, int half) {
+    if constexpr (P == kHalf) {
+      words<N / 2>(h + N * u, w);
+      words<N / 2>(h + half + N * u, w + N / 2);
+    } else {
+      words<N>(h + 2 * N * u, w);
+    }
+  }
+
+  __device__ __forceinline__ void turn(const float (&c)[N], const float (&s)[N]) {
     if constexpr (P == kAdjacent) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < N; ++i) {
         const float a = bf16_lo(w[i]), b = bf16_hi(w[i]);
         w[i] = pack_bf16x2(a * c[i] - b * s[i], b * c[i] + a * s[i]);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kPairs / 2; ++i) {
-        const uint32_t x = w[i], y = w[kPairs / 2 + i];
+      for (int i = 0; i < N / 2; ++i) {
+        const uint32_t x = w[i], y = w[N / 2 + i];
         const float a0 = bf16_lo(x), a1 = bf16_hi(x), b0 = bf16_lo(y), b1 = bf16_hi(y);
         w[i] = pack_bf16x2(a0 * c[2 * i] - b0 * s[2 * i], a1 * c[2 * i + 1] - b1 * s[2 * i + 1]);
-        w[kPairs / 2 + i] =
+        w[N / 2 + i] =
             pack_bf16x2(b0 * c[2 * i] + a0 * s[2 * i], b1 * c[2 * i + 1] + a1 * s[2 * i + 1]);
       }
     }
   }
 
   __device__ __forceinline__ void store(__nv_bfloat16* h, int u, int half) const {
-    if constexpr (P == kHalf8) {
-      *reinterpret_cast<uint4*>(h + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
-      *reinterpret_cast<uint4*>(h + half + 8 * u) = make_uint4(w[4], w[5], w[6], w[7]);
-    } else if constexpr (P == kHalf4) {
-      *reinterpret_cast<uint2*>(h + 4 * u) = make_uint2(w[0], w[1]);
-      *reinterpret_cast<uint2*>(h + half + 4 * u) = make_uint2(w[2], w[3]);
+    if constexpr (P == kHalf) {
+      put<N / 2>(h + N * u, w);
+      put<N / 2>(h + half + N * u, w + N / 2);
     } else {
-      *reinterpret_cast<uint4*>(h + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
+      put<N>(h + 2 * N * u, w);
     }
   }
 };
@@ -122,7 +136,7 @@ __device__ __forceinline__ __nv_bfloat16* head_out(const RopeParams& p, int64_t 
                     : p.ko + t * p.d.ko_ts + (h - p.d.hq) * p.d.ko_hs;
 }
 
-template <Pairing P>
+template <Pairing P, int N>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
   pdl_enter();
   __shared__ __align__(16) float cs[kMaxAngles], sn[kMaxAngles];
@@ -145,46 +159,43 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   }
   __syncthreads();
 
-  // A thread keeps its unit of a head and walks over heads and tokens: no division in the
-  // loop (with two a unit, the pass was bound by its integer instructions).
+  // A thread keeps its unit of a head, and so its angles, over a token's heads: no division and
+  // few multiplications in the loop (with both, the pass was bound by integer instructions).
   const int heads = p.d.hq + p.d.hk;
-  constexpr int kBatch = P == kHalf8 ? 2 : 4;           // units in flight a thread
+  constexpr int kBatch = 2;                             // units in flight a thread
   const int slot = threadIdx.x / p.units, u = threadIdx.x - slot * p.units;
-  int t = slot / p.head_step, h = slot - t * p.head_step;
-  if (t >= p.tok_step) t = tokens;                      // (threads past the last whole slot)
-  const int h0 = h;
-  const int angle0 = u * Unit<P>::kPairs;
-  while (t < tokens) {
-    Unit<P> v[kBatch];
-    __nv_bfloat16* to[kBatch];
-    int at[kBatch];
+  const int ts = slot / p.head_step, h0 = slot - ts * p.head_step;
+  // (threads past the last whole slot have no token)
+  for (int t = ts < p.tok_step ? ts : tokens; t < tokens; t += p.tok_step) {
+    const __nv_bfloat16* qi = p.q + (t0 + t) * p.d.q_ts;
+    const __nv_bfloat16* ki = p.k + (t0 + t) * p.d.k_ts;
+    __nv_bfloat16* qo = p.qo + (t0 + t) * p.d.qo_ts;
+    __nv_bfloat16* ko = p.ko + (t0 + t) * p.d.ko_ts;
+    float c[N], s[N];
+    for (int h = h0; h < heads; h += kBatch * p.head_step) {
+      Unit<P, N> v[kBatch];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      to[b] = nullptr;
-      if (t < tokens) {
-        if (h < heads) {
-          v[b].load(head_in(p, t0 + t, h), u, pairs);
-          to[b] = head_out(p, t0 + t, h);
-          at[b] = t * pairs + angle0;
-        }
-        h += p.head_step;
-        if (h >= heads) {
-          h = h0;
-          t += p.tok_step;
+      for (int b = 0; b < kBatch; ++b) {
+        const int hb = h + b * p.head_step;
+        if (hb < heads)
+          v[b].load(hb < p.d.hq ? qi + hb * p.d.q_hs : ki + (hb - p.d.hq) * p.d.k_hs, u, pairs);
+      }
+      if (h == h0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+          *reinterpret_cast<float4*>(c + i) =
+              *reinterpret_cast<const float4*>(cs + t * pairs + u * N + i);
+          *reinterpret_cast<float4*>(s + i) =
+              *reinterpret_cast<const float4*>(sn + t * pairs + u * N + i);
         }
       }
-    }
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (to[b] != nullptr) {
-        float c[Unit<P>::kPairs], s[Unit<P>::kPairs];
-#pragma unroll
-        for (int i = 0; i < Unit<P>::kPairs; i += 4) {
-          *reinterpret_cast<float4*>(c + i) = *reinterpret_cast<const float4*>(cs + at[b] + i);
-          *reinterpret_cast<float4*>(s + i) = *reinterpret_cast<const float4*>(sn + at[b] + i);
+      for (int b = 0; b < kBatch; ++b) {
+        const int hb = h + b * p.head_step;
+        if (hb < heads) {
+          v[b].turn(c, s);
+          v[b].store(hb < p.d.hq ? qo + hb * p.d.qo_hs : ko + (hb - p.d.hq) * p.d.ko_hs, u, pairs);
         }
-        v[b].turn(c, s);
-        v[b].store(to[b], u, pairs);
       }
     }
   }
@@ -204,23 +215,23 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 cudaError_t launch_rope(const RopeParams& p_in, cudaStream_t stream) {
   RopeParams p = p_in;
   const int pairs = p.d.rot / 2;
-  const bool adjacent = p.d.interleaved != 0, wide = !adjacent && pairs % 8 == 0;
+  const int n = pairs % 8 == 0 ? 8 : 4;
   // A block has room for `slots` units' worth of heads: all heads of one or more tokens, or a
-  // part of one token's heads at a time. It takes tokens until each thread has a batch of
-  // units or two (so that the sine phase of one block hides behind the loads of others).
+  // part of one token's heads at a time. It takes tokens until each thread has two units (so
+  // that the sine phase of one block hides behind the loads of others).
   const int heads = p.d.hq + p.d.hk;
-  p.units = pairs / (wide ? 8 : 4);
-  const int slots = kThreads / p.units, batch = wide ? 2 : 4;
+  p.units = pairs / n;
+  const int slots = kThreads / p.units;
   p.head_step = std::min(heads, slots);
   p.tok_step = slots / p.head_step;
   const int64_t passes = (heads + p.head_step - 1) / p.head_step;
-  int64_t tok = std::max<int64_t>(1, batch * p.tok_step / passes);
+  int64_t tok = std::max<int64_t>(1, 2 * p.tok_step / passes);
   tok = std::min<int64_t>({tok, kMaxAngles / pairs, std::max<int64_t>(1, p.d.T / 304)});
   p.tok = static_cast<int>(tok);
   const int64_t grid = (p.d.T + tok - 1) / tok;
-  if (adjacent) return launch_k(rope_kernel<kAdjacent>, grid, stream, p);
-  if (wide) return launch_k(rope_kernel<kHalf8>, grid, stream, p);
-  return launch_k(rope_kernel<kHalf4>, grid, stream, p);
+  if (p.d.interleaved)
+    return launch_k(n == 8 ? rope_kernel<kAdjacent, 8> : rope_kernel<kAdjacent, 4>, grid, stream, p);
+  return launch_k(n == 8 ? rope_kernel<kHalf, 8> : rope_kernel<kHalf, 4>, grid, stream, p);
 }
 
 // ------------------------------------------------------------------ host checks
