@@ -55,11 +55,82 @@ class Block:
                            dx_residual=dx_residual)
 
 
+class Fp8Block(Block):
+    """A block whose forward multiplies in 8 bits: e4m3 weights quantised once, with gamma
+    folded into A, in square blocks of 128; activations quantised row by row on the way. The
+    1/rms scale and the activation stay in the down-projection's epilogue. The backward is the
+    bf16 block's on the bf16 weights, which this block keeps (straight-through)."""
+
+    def __init__(self, T, d, r, k, n, **kw):
+        super().__init__(T, d, r, k, n, **kw)
+        D = self.desc
+        f8, bf, dev = torch.float8_e4m3fn, torch.bfloat16, self.device
+
+        def operand(lead, rows, K):
+            return (torch.empty(lead + (rows, -(-K // 16) * 16), dtype=f8, device=dev),
+                    torch.empty(lead + (B.fp8_scale_bytes(rows, K),), dtype=torch.uint8, device=dev))
+
+        self.A8, self.B8 = operand((), k * r, d), operand((k,), n, r)
+        self.x8, self.a8 = operand((), T, d), operand((k,), T, r)
+        self.a = torch.empty(T, k * r, dtype=bf, device=dev)
+        self.ssq = torch.empty(D.S, T, dtype=torch.float32, device=dev) if D.has_norm else None
+        self.ws8 = B.Workspace(max(B.fp8_matmul_workspace_bytes(T, k * r, d),
+                                   B.fp8_matmul_workspace_bytes(T, n, r, k)), dev)
+        self.act = "silu" if D.act else "identity"
+        self.quantize_weights()
+
+    def quantize_weights(self, stream=None):
+        """Take the 8-bit weights from A, B and gamma again (after an update of them)."""
+        B.fp8_quantize(self.A, way="columns", block_rows=128, gamma=self.gamma, cols_out=self.A8,
+                       stream=stream)
+        B.fp8_quantize(self.B, way="columns", block_rows=128, cols_out=self.B8, stream=stream)
+
+    def forward(self, x, stream=None, residual=None):
+        D = self.desc
+        if D.has_norm:
+            B.rmsnorm_stats(D, x, self.ssq, self.rstd, stream)
+        B.fp8_quantize(x, rows_out=self.x8, stream=stream)
+        B.fp8_matmul(*self.x8, *self.A8, D.d, self.ws8, row_scale=self.rstd, act=self.act,
+                     out=self.a, stream=stream)
+        groups = self.a.view(D.T, D.k, D.r).transpose(0, 1)
+        B.fp8_quantize(groups, rows_out=self.a8, stream=stream)
+        B.fp8_matmul(*self.a8, *self.B8, D.r, self.ws8, out=self.y, stream=stream)
+        if residual is not None:
+            if D.k != 1:
+                raise ValueError("a residual needs one output group")
+            B.add(self.y[0], residual, self.y[0], stream=stream)
+        return self.y
+
+
+class Rotary:
+    """Rotary positions of q and k for heads of ``dim`` values: base^(-i / pairs) radians a
+    position for pair i of ``rot`` / 2 (or ``inv_freq``, any frequencies), shared among the
+    position axes by ``sections``."""
+
+    def __init__(self, dim, *, rot=None, base=10000.0, inv_freq=None, sections=None,
+                 interleaved=False, device="cuda"):
+        pairs = (dim if rot is None else rot) // 2
+        if inv_freq is None:
+            inv_freq = base ** (-torch.arange(pairs, dtype=torch.float64) / pairs)
+        self.dim, self.sections, self.interleaved = dim, sections, interleaved
+        self.inv_freq = inv_freq.to(device=device, dtype=torch.float64).contiguous()
+
+    def __call__(self, q, k, positions, *, inverse=False, q_out=None, k_out=None, stream=None):
+        """Turn q and k [T, heads * dim] (back, for gradients, when ``inverse``)."""
+        def split(t):
+            return None if t is None else t.view(t.shape[0], -1, self.dim)
+
+        B.rope(split(q), split(k), positions, self.inv_freq, sections=self.sections,
+               interleaved=self.interleaved, inverse=inverse, q_out=split(q_out),
+               k_out=split(k_out), stream=stream)
+        return q_out, k_out
+
+
 class MLP:
     """LLaMA MLP of two bottlenecks: gate/up (normed, k=2) -> SwiGLU -> down (k=1)."""
 
     def __init__(self, T, d, r, ffn, *, S=1, eps=1e-5, act="silu", weights=None,
-                 device="cuda", ws=None, fused_glu=True, checkpoint="input"):
+                 device="cuda", ws=None, fused_glu=True, checkpoint="input", fp8=False):
         w = weights or {}
         self.T, self.d, self.r, self.ffn = T, d, r, ffn
         # SwiGLU forward in the gate/up up-projection's epilogue, and its backward in the
@@ -75,10 +146,15 @@ class MLP:
         if checkpoint == "bottleneck" and not fused_glu:
             raise ValueError("the bottleneck cut regenerates gate, up and h with the fused kernel")
         self.checkpoint = checkpoint
-        self.gu = Block(T, d, r, 2, ffn, S=S, eps=eps, act=act, has_norm=True,
+        # fp8: both blocks' forward in 8 bits (with a separate SwiGLU pass between them)
+        if fp8 and checkpoint != "input":
+            raise ValueError("the bottleneck cut regenerates the bf16 block's activations")
+        self.fp8 = fp8
+        block = Fp8Block if fp8 else Block
+        self.gu = block(T, d, r, 2, ffn, S=S, eps=eps, act=act, has_norm=True,
                         weights={"gamma": w.get("gamma"), "A": w.get("A1"), "B": w.get("B1")},
                         device=device, ws=ws)
-        self.dn = Block(T, ffn, r, 1, d, S=1, eps=eps, act=act, has_norm=False,
+        self.dn = block(T, ffn, r, 1, d, S=1, eps=eps, act=act, has_norm=False,
                         weights={"A": w.get("A2"), "B": w.get("B2")}, device=device,
                         ws=self.gu.ws if checkpoint == "input" else None)
         if checkpoint == "input":
@@ -95,7 +171,7 @@ class MLP:
 
     def forward(self, x, stream=None, residual=None):
         """residual [T, d]: out = residual + MLP(x), added in the down block's epilogue."""
-        if self.fused_glu:
+        if self.fused_glu and not self.fp8:
             gu = self.gu
             B.block_fwd_swiglu(gu.desc, x, gu.gamma, gu.A, gu.B, gu.ws, y=gu.y, h=self.h,
                                rstd=gu.rstd, stream=stream)
@@ -141,25 +217,37 @@ class Layer:
     Both residual adds run in GEMM epilogues: x1 = x + O(v) in the O block's
     up-projection, out = x1 + MLP(x1) in the MLP's down up-projection; in the backward,
     dx1 = dout + (MLP input gradient) in the MLP's dx epilogue and dx = dx1 + (QKV input
-    gradient) in the QKV block's."""
+    gradient) in the QKV block's.
 
-    def __init__(self, T, d, r, ffn, *, S=1, eps=1e-5, act="silu", weights=None, device="cuda"):
+    rotary (a ``Rotary``): q and k are turned in place in the QKV block's output, and the
+    attention core's gradients of the turned q and k back on their way into the QKV block's
+    upstream gradient. dropout (p > 0): x1 = x + dropout(O(v)), out = x1 + dropout(MLP(x1)),
+    with the masks of (``seed``, ``mask`` of the call) and none stored. fp8: the blocks'
+    forward in 8 bits (``Fp8Block``)."""
+
+    def __init__(self, T, d, r, ffn, *, S=1, eps=1e-5, act="silu", weights=None, device="cuda",
+                 rotary=None, dropout=0.0, seed=0, fp8=False):
         p = weights or {}
         self.T, self.d = T, d
-        self.qkv = Block(T, d, r, 3, d, S=S, eps=eps, act=act, has_norm=True,
+        self.rotary, self.dropout, self.seed = rotary, dropout, seed
+        block = Fp8Block if fp8 else Block
+        self.qkv = block(T, d, r, 3, d, S=S, eps=eps, act=act, has_norm=True,
                          weights={"gamma": p.get("gamma1"), "A": p.get("A_qkv"),
                                   "B": p.get("B_qkv")}, device=device)
         ws = self.qkv.ws
-        self.o = Block(T, d, r, 1, d, S=1, eps=eps, act=act, has_norm=False,
+        self.o = block(T, d, r, 1, d, S=1, eps=eps, act=act, has_norm=False,
                        weights={"A": p.get("A_o"), "B": p.get("B_o")}, device=device, ws=ws)
         self.mlp = MLP(T, d, r, ffn, S=S, eps=eps, act=act,
                        weights={"gamma": p.get("gamma2"), "A1": p.get("A_gu"), "B1": p.get("B_gu"),
-                                "A2": p.get("A_dn"), "B2": p.get("B_dn")}, device=device, ws=ws)
+                                "A2": p.get("A_dn"), "B2": p.get("B_dn")}, device=device, ws=ws,
+                       fp8=fp8)
         ws = self.mlp.gu.ws
         for blk in (self.qkv, self.o):
             blk.ws = ws
         dev = self.qkv.device
         self.dqkv = torch.empty(3, T, d, dtype=torch.bfloat16, device=dev)
+        # gradient of a branch behind its dropout
+        self.dbranch = torch.empty(T, d, dtype=torch.bfloat16, device=dev) if dropout else None
 
     @property
     def x1(self):
@@ -181,23 +269,49 @@ class Layer:
         """Gradient at x: dx1 + the QKV block's input gradient (its dx buffer)."""
         return self.qkv.dx
 
-    def forward(self, x, stream=None):
-        qkv = self.qkv.forward(x, stream)
-        x1 = self.o.forward(qkv[2], stream, residual=x)[0]
-        return self.mlp.forward(x1, stream, residual=x1)
+    def _join(self, branch, residual, which, mask, counter, stream):
+        """residual + dropout(branch), in the branch's buffer."""
+        return B.dropout_add(branch, self.dropout, (self.seed + which) % (1 << 64), mask,
+                             residual=residual, out=branch, counter=counter, stream=stream)
 
-    def backward(self, x, dout, dq, dk, stream=None):
-        """dq, dk: the attention core's gradients of q and k. The QKV block's upstream
-        gradient is the stacked [dq, dk, dv]; dq and dk are copied into it unless they
-        are already its first two planes (`dqkv[0]`, `dqkv[1]`), and the O block writes
-        dv straight into the third."""
-        dx1 = self.mlp.backward(self.x1, dout, stream, dx_residual=dout)[0]
-        s = torch.cuda.current_stream() if stream is None else stream
-        with torch.cuda.stream(s):
-            for i, g in enumerate((dq, dk)):
-                if g.data_ptr() != self.dqkv[i].data_ptr():
-                    self.dqkv[i].copy_(g)
-        self.o.backward(self.qkv.y[2], dx1.view(1, self.T, self.d), stream, dx=self.dqkv[2])
+    def _split(self, grad, which, mask, counter, stream):
+        """Gradient of the branch whose dropout joined it to the residual."""
+        if not self.dropout:
+            return grad
+        return B.dropout_bwd(grad, self.dropout, (self.seed + which) % (1 << 64), mask,
+                             dx=self.dbranch, counter=counter, stream=stream)
+
+    def forward(self, x, stream=None, positions=None, mask=0, counter=None):
+        """positions ([T] or [axes, T]): those of the tokens, with ``rotary``. mask: which
+        dropout masks (plus ``counter``, a device value, as in ``binding.dropout_add``)."""
+        qkv = self.qkv.forward(x, stream)
+        if self.rotary is not None:
+            self.rotary(qkv[0], qkv[1], positions, q_out=qkv[0], k_out=qkv[1], stream=stream)
+        if not self.dropout:
+            x1 = self.o.forward(qkv[2], stream, residual=x)[0]
+            return self.mlp.forward(x1, stream, residual=x1)
+        x1 = self._join(self.o.forward(qkv[2], stream)[0], x, 0, mask, counter, stream)
+        return self._join(self.mlp.forward(x1, stream), x1, 1, mask, counter, stream)
+
+    def backward(self, x, dout, dq, dk, stream=None, positions=None, mask=0, counter=None):
+        """dq, dk: the attention core's gradients of q and k (the turned ones, with
+        ``rotary``). The QKV block's upstream gradient is the stacked [dq, dk, dv]; dq and
+        dk are turned back or copied into it (copied unless they are already its first two
+        planes, `dqkv[0]`, `dqkv[1]`), and the O block writes dv straight into the third.
+        positions, mask, counter: those of the forward."""
+        dm = self._split(dout, 1, mask, counter, stream)
+        dx1 = self.mlp.backward(self.x1, dm, stream, dx_residual=dout)[0]
+        if self.rotary is not None:
+            self.rotary(dq, dk, positions, inverse=True, q_out=self.dqkv[0], k_out=self.dqkv[1],
+                        stream=stream)
+        else:
+            s = torch.cuda.current_stream() if stream is None else stream
+            with torch.cuda.stream(s):
+                for i, g in enumerate((dq, dk)):
+                    if g.data_ptr() != self.dqkv[i].data_ptr():
+                        self.dqkv[i].copy_(g)
+        do = self._split(dx1, 0, mask, counter, stream)
+        self.o.backward(self.qkv.y[2], do.view(1, self.T, self.d), stream, dx=self.dqkv[2])
         return self.qkv.backward(x, self.dqkv, stream, dx_residual=dx1)[0]
 
 
