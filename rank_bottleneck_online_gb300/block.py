@@ -117,6 +117,9 @@ class Rotary:
 
     def __call__(self, q, k, positions, *, inverse=False, q_out=None, k_out=None, stream=None):
         """Turn q and k [T, heads * dim] (back, for gradients, when ``inverse``)."""
+        if positions is None:
+            raise ValueError("rotary positions need the tokens' positions")
+
         def split(t):
             return None if t is None else t.view(t.shape[0], -1, self.dim)
 

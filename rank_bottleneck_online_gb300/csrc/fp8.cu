@@ -45,10 +45,17 @@ boost_status validate(const boost_fp8_matmul_desc* D) {
   if (D->act != BOOST_ACT_IDENTITY && D->act != BOOST_ACT_SILU) return BOOST_ERR_INVALID_ARG;
   if (D->a_pitch < D->K || D->b_pitch < D->K) return BOOST_ERR_INVALID_ARG;
   if (D->a_pitch % 16 || D->b_pitch % 16 || D->N % 8) return BOOST_ERR_UNSUPPORTED_SHAPE;
-  // (a million columns, so that tile counts and grids stay within 31 bits)
   if (D->M > kMaxDim || D->N > 65535ll * 16 || D->K > kMaxDim || D->G > 65535 ||
       D->a_pitch > kMaxDim || D->b_pitch > kMaxDim)
     return BOOST_ERR_UNSUPPORTED_SHAPE;
+  // a tensor map's matrix stride is below 2^40 bytes; tiles, times 8 for a shared K, and grids
+  // stay within 31 bits
+  constexpr double kStride = 0x1p40;
+  if (static_cast<double>(D->M) * D->a_pitch >= kStride ||
+      static_cast<double>(D->N) * D->b_pitch >= kStride || 2.0 * D->M * D->N >= kStride)
+    return BOOST_ERR_UNSUPPORTED_SHAPE;
+  const double tiles = static_cast<double>((D->M + 127) / 128) * ((D->N + 127) / 128) * D->G;
+  if (tiles > 0x1p28 - 1) return BOOST_ERR_UNSUPPORTED_SHAPE;
   return BOOST_OK;
 }
 

@@ -51,12 +51,17 @@ __device__ __forceinline__ uint32_t larger_half(uint32_t w) {
   return max(w & 0xffffu, w >> 16);     // magnitudes order as integers
 }
 
-// Scale byte of a block whose largest finite magnitude has the bf16 bits m.
+// Scale byte of a block whose largest finite magnitude has the bf16 bits m: its exponent less 8
+// (15), and one more where the fraction is above 1.75, which adding 0x1f carries over.
 template <int FMT>
 __device__ __forceinline__ uint32_t scale_byte(uint32_t m) {
-  if (m == 0) return 127;
-  const int e = static_cast<int>(m >> 7) - (FMT == BOOST_E4M3 ? 8 : 15) + ((m & 0x7f) > 0x60);
+  const int e = static_cast<int>((m + 0x1fu) >> 7) - (FMT == BOOST_E4M3 ? 8 : 15);
   return e < 0 ? 0 : e;
+}
+
+// The byte that is stored: 127 (a scale of 1) for zeros, which any factor leaves as they are.
+__device__ __forceinline__ uint8_t stored_byte(uint32_t byte, uint32_t m, bool inside) {
+  return static_cast<uint8_t>(inside && m != 0 ? byte : 127u);
 }
 
 // 2^(127 - byte), the factor that takes the block's values to 8 bits (byte <= 247, so the
@@ -114,8 +119,9 @@ __device__ __forceinline__ uint2 quant8(const uint32_t* w, float inv, bool inf) 
 // Largest magnitudes of kRows rows over the kLanes lanes (a power of two) that hold a block, in
 // `top`: with infinities where there are some, and those then again over the finite values,
 // which is what the scale comes from. Two rows go through the shuffles in the halves of a
-// word. Returns a bit for each row whose block holds an infinity.
-template <int kRows, int kWords, int kLanes>
+// word. Returns a bit for each row whose block holds an infinity (or nothing but NaN). Without
+// kMayInf every value is known to be finite.
+template <int kRows, int kWords, int kLanes, bool kMayInf = true>
 __device__ __forceinline__ uint32_t block_tops(const uint32_t (&w)[kRows][kWords],
                                                uint32_t (&top)[kRows]) {
   uint32_t two[kRows / 2];
@@ -141,10 +147,12 @@ __device__ __forceinline__ uint32_t block_tops(const uint32_t (&w)[kRows][kWords
     // (a block of NaN alone leaves a NaN here: no finite value, as 0)
     top[2 * r] = two[r] & 0xffffu;
     top[2 * r + 1] = two[r] >> 16;
+    if (kMayInf) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) inf |= (top[2 * r + h] >= kInf ? 1u : 0u) << (2 * r + h);
+      for (int h = 0; h < 2; ++h) inf |= (top[2 * r + h] >= kInf ? 1u : 0u) << (2 * r + h);
+    }
   }
-  if (__any_sync(0xffffffffu, inf != 0)) {
+  if (kMayInf && __any_sync(0xffffffffu, inf != 0)) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       uint32_t f = 0;
@@ -164,7 +172,7 @@ __device__ __forceinline__ uint32_t block_tops(const uint32_t (&w)[kRows][kWords
 // flight. A block of 8 warps covers 32 rows. grid = (scale tiles along the columns,
 // 4 x row tiles of 128, matrices).
 template <int FMT>
-__global__ void __launch_bounds__(kThreads) quant_rows_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const QuantParams p) {
   pdl_enter();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 512 + lane * 16;
@@ -199,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const QuantParams 
       *reinterpret_cast<uint4*>(q + r * p.pitch) = make_uint4(a.x, a.y, b.x, b.y);
     }
     // the four blocks' bytes, 127 outside the operand
-    uint32_t word = (in_cols && r < rows ? byte : 127u) << (lane & 24);
+    uint32_t word = static_cast<uint32_t>(stored_byte(byte, top[r], in_cols && r < rows)) << (lane & 24);
     word |= __shfl_xor_sync(0xffffffffu, word, 8);
     word |= __shfl_xor_sync(0xffffffffu, word, 16);
     // (four rows of one quarter of a scale tile lie 16 bytes apart)
@@ -212,70 +220,25 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(const QuantParams 
 // 8 rg .. 8 rg + 7 of columns 8 cg .. 8 cg + 7, so that 16 lanes read a row's 256 bytes. The
 // transposed bytes go through shared memory: column c's 128 bytes lie at 128 c, the 8 bytes
 // of row group rg in slot rg ^ (c / 8), which keeps both sides free of bank conflicts. The
-// pass is close to the issue rate (about 15 instructions a value for both layouts), so every
-// address is a base and a small stride. grid = (column tiles, row tiles, matrices).
-template <int FMT, bool SQUARE>
-__global__ void __launch_bounds__(kThreads, 4) quant_tile_kernel(const QuantParams p) {
-  pdl_enter();
-  __shared__ __align__(16) uint8_t bytes[128 * 128];
-  __shared__ uint32_t part[2][16][64];  // a row group's column maxima, in pairs:
-                                        // of all magnitudes, of the finite ones
-  __shared__ uint32_t col_all[64], col_top[64];         // the tile's
+// pass is close to the issue rate, so every address is a base and a small stride, and tiles
+// that lie inside x and are finite, by far the most, skip the checks of both. (A persistent
+// form with the next tile on its way by cp.async was slower, 67 us against 57 before that
+// last step: its shared memory leaves three blocks an SM, not four.)
+// grid = (column tiles, row tiles, matrices).
+
+// What follows a tile's column maxima: both layouts' values and scales. PLAIN: the tile lies
+// inside x and holds finite values alone.
+template <int FMT, bool SQUARE, bool PLAIN>
+__device__ __forceinline__ void write_tile(const QuantParams& p, const uint32_t (&w)[8][4],
+                                           const uint32_t* col_all, const uint32_t* col_top,
+                                           uint8_t* bytes) {
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
   const int64_t row0 = static_cast<int64_t>(blockIdx.y) * 128;
   const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 128;
   const int64_t row = row0 + rg * 8, col = col0 + cg * 8;          // this thread's first
-  const int rows = static_cast<int>(min(max(p.rows - row, static_cast<int64_t>(0)),
-                                        static_cast<int64_t>(8)));
-  const bool in_cols = col < p.cols;
-  uint32_t w[8][4];
-  {
-    const __nv_bfloat16* x = p.x + blockIdx.z * p.gstride + row * p.ldx + col;
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < rows && in_cols) v = __ldg(reinterpret_cast<const uint4*>(x));
-      x += p.ldx;
-      w[r][0] = v.x; w[r][1] = v.y; w[r][2] = v.z; w[r][3] = v.w;
-    }
-  }
-  if (p.gamma != nullptr) {
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      if (r < rows && in_cols) {
-        const float g = __bfloat162float(p.gamma[row + r]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[r][i] = pack_bf16x2(g * bf16_lo(w[r][i]), g * bf16_hi(w[r][i]));
-      }
-    }
-  }
-
-  if (SQUARE || p.qt != nullptr) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t m = w[0][i] & 0x7fff7fffu;
-#pragma unroll
-      for (int r = 1; r < 8; ++r) m = max2(m, w[r][i] & 0x7fff7fffu);
-      uint32_t f = m;
-      if ((m & 0xffffu) >= kInf || (m >> 16) >= kInf) {
-        f = 0;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) f = max2(f, finite2(w[r][i]));
-      }
-      part[0][rg][cg * 4 + i] = m;
-      part[1][rg][cg * 4 + i] = f;
-    }
-    __syncthreads();
-    if (threadIdx.x < 128) {
-      const int which = threadIdx.x >> 6, c2 = threadIdx.x & 63;
-      uint32_t m = 0;
-#pragma unroll
-      for (int g = 0; g < 16; ++g) m = max2(m, part[which][g][c2]);
-      (which == 0 ? col_all : col_top)[c2] = m;
-    }
-    __syncthreads();
-  }
-  uint32_t tile_byte = 0;
+  const int rows = PLAIN ? 8 : static_cast<int>(min(max(p.rows - row, static_cast<int64_t>(0)),
+                                                    static_cast<int64_t>(8)));
+  uint32_t tile_top = 0, tile_byte = 0;
   bool tile_inf = false;
   if constexpr (SQUARE) {
     const int lane = threadIdx.x & 31;
@@ -286,57 +249,69 @@ __global__ void __launch_bounds__(kThreads, 4) quant_tile_kernel(const QuantPara
       m = max2(m, __shfl_xor_sync(0xffffffffu, m, o));
       f = max2(f, __shfl_xor_sync(0xffffffffu, f, o));
     }
-    tile_byte = scale_byte<FMT>(larger_half(f));
-    tile_inf = larger_half(m) == kInf;
+    tile_top = larger_half(f);
+    tile_byte = scale_byte<FMT>(tile_top);
+    tile_inf = !PLAIN && larger_half(m) == kInf;
   }
 
   if (p.q != nullptr) {
     const int64_t b0 = static_cast<int64_t>(blockIdx.x), blocks = (p.cols + 127) / 128;
-    // one byte a block; the last column tile fills its scale tile
-    const int64_t b = b0 + cg;
-    const bool writes = cg == 0 || (b0 + 1 == gridDim.x && b < 4 * p.kt);
-    uint8_t* sf = p.sf + blockIdx.z * p.plane + scale_at(row, b, p.kt);
     uint8_t* q = p.q + (blockIdx.z * p.rows + row) * p.pitch + col;
     uint32_t top[8], infs = 0;
-    if constexpr (!SQUARE) infs = block_tops<8, 4, 16>(w, top);
+    if constexpr (!SQUARE) infs = block_tops<8, 4, 16, !PLAIN>(w, top);
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
+      if constexpr (SQUARE) top[r] = tile_top;
       const uint32_t byte = SQUARE ? tile_byte : scale_byte<FMT>(top[r]);
-      if (r < rows && col < p.pitch)
-        *reinterpret_cast<uint2*>(q) =
-            quant8<FMT>(w[r], scale_inverse(byte), SQUARE ? tile_inf : (infs >> r & 1) != 0);
+      if (PLAIN || (r < rows && col < p.pitch))
+        *reinterpret_cast<uint2*>(q) = quant8<FMT>(
+            w[r], scale_inverse(byte), !PLAIN && (SQUARE ? tile_inf : (infs >> r & 1) != 0));
       q += p.pitch;
+    }
+    // one byte a block; the last column tile fills its scale tile
+    const int64_t b = b0 + cg;
+    if (cg == 0 || (b0 + 1 == gridDim.x && b < 4 * p.kt)) {
       // (eight rows of one quarter of a scale tile lie 16 bytes apart)
-      if (writes) sf[16 * r] = static_cast<uint8_t>(r < rows && b < blocks ? byte : 127u);
+      uint8_t* sf = p.sf + blockIdx.z * p.plane + scale_at(row, b, p.kt);
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        sf[16 * r] = stored_byte(scale_byte<FMT>(top[r]), top[r], r < rows && b < blocks);
     }
   }
 
   if (p.qt != nullptr) {
     const int64_t b0 = static_cast<int64_t>(blockIdx.y), blocks = (p.rows + 127) / 128;
-    const int64_t b = b0 + rg;
-    const bool writes = rg == 0 || (b0 + 1 == gridDim.y && b < 4 * p.kt_t);
-    uint8_t* sf = p.sft + blockIdx.z * p.plane_t + scale_at(col, b, p.kt_t);
     uint8_t* slot = bytes + cg * 1024 + ((rg ^ cg) * 8);
+    uint32_t top[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t t = SQUARE ? 0 : col_top[cg * 4 + i], a = SQUARE ? 0 : col_all[cg * 4 + i];
+      const uint32_t t = SQUARE ? 0 : col_top[cg * 4 + i];
+      const uint32_t a = SQUARE || PLAIN ? 0 : col_all[cg * 4 + i];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int c = 2 * i + h;
-        const uint32_t byte = SQUARE ? tile_byte : scale_byte<FMT>(h ? t >> 16 : t & 0xffffu);
-        const bool inf = SQUARE ? tile_inf : (h ? a >> 16 : a & 0xffffu) == kInf;
+        top[c] = SQUARE ? tile_top : (h ? t >> 16 : t & 0xffffu);
+        const uint32_t byte = SQUARE ? tile_byte : scale_byte<FMT>(top[c]);
+        const bool inf = !PLAIN && (SQUARE ? tile_inf : (h ? a >> 16 : a & 0xffffu) == kInf);
         uint32_t v[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)     // rows 2 r and 2 r + 1 of this column
           v[r] = __byte_perm(w[2 * r][i], w[2 * r + 1][i], h ? 0x7632 : 0x5410);
         *reinterpret_cast<uint2*>(slot + c * 128) = quant8<FMT>(v, scale_inverse(byte), inf);
-        if (writes) sf[16 * c] = static_cast<uint8_t>(in_cols && b < blocks ? byte : 127u);
       }
+    }
+    // one byte a block; the last row tile fills its scale tile
+    const int64_t b = b0 + rg;
+    if (rg == 0 || (b0 + 1 == gridDim.y && b < 4 * p.kt_t)) {
+      uint8_t* sf = p.sft + blockIdx.z * p.plane_t + scale_at(col, b, p.kt_t);
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        sf[16 * c] = stored_byte(scale_byte<FMT>(top[c]), top[c], col < p.cols && b < blocks);
     }
     __syncthreads();
     // 8 lanes a column, 16 bytes a lane
     const int c0 = threadIdx.x >> 3, piece = threadIdx.x & 7;
-    const bool in_pitch = row0 + piece * 16 < p.pitch_t;
+    const bool in_pitch = PLAIN || row0 + piece * 16 < p.pitch_t;
     uint8_t* qt = p.qt + (blockIdx.z * p.cols + col0 + c0) * p.pitch_t + row0 + piece * 16;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -344,11 +319,79 @@ __global__ void __launch_bounds__(kThreads, 4) quant_tile_kernel(const QuantPara
       const uint8_t* at = bytes + c * 128;
       const uint2 lo = *reinterpret_cast<const uint2*>(at + (((2 * piece) ^ (c >> 3)) * 8));
       const uint2 hi = *reinterpret_cast<const uint2*>(at + (((2 * piece + 1) ^ (c >> 3)) * 8));
-      if (col0 + c < p.cols && in_pitch)
+      if (PLAIN || (col0 + c < p.cols && in_pitch))
         *reinterpret_cast<uint4*>(qt) = make_uint4(lo.x, lo.y, hi.x, hi.y);
       qt += 32 * p.pitch_t;
     }
   }
+}
+
+template <int FMT, bool SQUARE>
+__global__ void __launch_bounds__(kThreads, 4) quant_tile_kernel(const QuantParams p) {
+  pdl_enter();
+  __shared__ __align__(16) uint8_t bytes[128 * 128];
+  __shared__ uint32_t part[2][16][64];  // a row group's column maxima, in pairs:
+                                        // of all magnitudes, of the finite ones
+  __shared__ uint32_t col_all[64], col_top[64];         // the tile's
+  const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+  const int64_t row = static_cast<int64_t>(blockIdx.y) * 128 + rg * 8;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 128 + cg * 8;
+  const bool inside = row + 8 <= p.rows && col < p.cols;
+  uint32_t w[8][4];
+  {
+    const __nv_bfloat16* x = p.x + blockIdx.z * p.gstride + row * p.ldx + col;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (inside || (row + r < p.rows && col < p.cols)) v = __ldg(reinterpret_cast<const uint4*>(x));
+      x += p.ldx;
+      w[r][0] = v.x; w[r][1] = v.y; w[r][2] = v.z; w[r][3] = v.w;
+    }
+  }
+  if (p.gamma != nullptr) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      if (row + r < p.rows && col < p.cols) {
+        const float g = __bfloat162float(p.gamma[row + r]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[r][i] = pack_bf16x2(g * bf16_lo(w[r][i]), g * bf16_hi(w[r][i]));
+      }
+    }
+  }
+
+  bool other = !inside;                 // than PLAIN
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // (max.NaN would keep a NaN; here one gives way, so it is looked for in the sum of the
+    // exponents' overflow: 0x7f80 and above carry into bit 15)
+    uint32_t m = w[0][i] & 0x7fff7fffu, over = m + 0x00800080u;
+#pragma unroll
+    for (int r = 1; r < 8; ++r) {
+      const uint32_t a = w[r][i] & 0x7fff7fffu;
+      m = max2(m, a);
+      over |= a + 0x00800080u;
+    }
+    uint32_t f = m;
+    if ((over & 0x80008000u) != 0) {
+      other = true;
+      f = 0;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) f = max2(f, finite2(w[r][i]));
+    }
+    part[0][rg][cg * 4 + i] = m;
+    part[1][rg][cg * 4 + i] = f;
+  }
+  const bool plain = __syncthreads_or(other) == 0;
+  if (threadIdx.x < 128) {
+    const int which = threadIdx.x >> 6, c2 = threadIdx.x & 63;
+    uint32_t m = 0;
+#pragma unroll
+    for (int g = 0; g < 16; ++g) m = max2(m, part[which][g][c2]);
+    (which == 0 ? col_all : col_top)[c2] = m;
+  }
+  __syncthreads();
+  if (plain) write_tile<FMT, SQUARE, true>(p, w, col_all, col_top, bytes);
+  else write_tile<FMT, SQUARE, false>(p, w, col_all, col_top, bytes);
 }
 
 }  // namespace

@@ -212,3 +212,6 @@ def test_refusals():
     blk = Fp8Block(16, 64, 64, 2, 64, weights=w)
     with pytest.raises(ValueError):
         blk.forward(w["x"].cuda(), residual=normal(1, 16, 64))
+    _, layer, *_ = make_layer()
+    with pytest.raises(ValueError):
+        layer.forward(normal(2, 200, 128))              # no positions

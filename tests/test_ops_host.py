@@ -187,6 +187,9 @@ def matmul_call(L, G=1, M=16, N=64, K=64, a_pitch=64, b_pitch=64, fa=0, fb=0, ac
     (dict(fa=2), INVALID), (dict(fb=-1), INVALID), (dict(act=3), INVALID),
     (dict(a_pitch=48), INVALID), (dict(b_pitch=72), SHAPE), (dict(N=60), SHAPE),
     (dict(G=70000), SHAPE), (dict(M=1 << 31), SHAPE), (dict(N=1 << 21), SHAPE),
+    (dict(M=1 << 30, K=2048, a_pitch=2048, b_pitch=2048), SHAPE),      # a matrix of 2^41 bytes
+    (dict(M=1 << 29, N=2048), SHAPE),                                  # an output of 2^41 bytes
+    (dict(G=60000, M=1 << 20, N=128), SHAPE),                          # too many tiles
     (dict(a=0), INVALID), (dict(bsf=0), INVALID), (dict(out=0), INVALID),
     (dict(a=0x10008), ALIGN), (dict(rs=0x60004), ALIGN), (dict(out=0x50002), ALIGN),
     (dict(ws=0), WORKSPACE), (dict(ws=0x1000010), WORKSPACE), (dict(ws_bytes=128), WORKSPACE),
