@@ -495,27 +495,47 @@ def _raw_stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
-def _heads(t, name, T, dim, device):
-    """(address, token stride, head stride, heads) of a bf16 [T, heads, dim] tensor whose
-    values are adjacent."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [T, heads, dim]")
-    t0, heads, d0 = t.shape
-    if t.dtype is not torch.bfloat16 or t.get_device() != device or t0 != T or d0 != dim:
-        _refuse(t.contiguous(), name, torch.bfloat16, (T, heads, dim), device)
-    ts, hs, vs = t.stride()
-    if vs != 1 and dim > 1:
-        raise ValueError(f"{name} must have adjacent values, not a stride of {vs}")
+def _on(t, name, dtype, device):
+    """Address of a tensor of this type on the current device, whatever its strides (the call's
+    plan has checked those)."""
+    if t.dtype is not dtype or t.get_device() != device:
+        _refuse(t.contiguous(), name, dtype, t.shape, device)
+    return t.data_ptr()
+
+
+def _head_strides(shape, stride, name, T, dim):
+    """Token and head strides of a [T, heads, dim] tensor whose values are adjacent."""
+    if len(shape) != 3 or shape[0] != T or shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [T={T}, heads, dim={dim}]")
+    if stride[2] != 1 and dim > 1:
+        raise ValueError(f"{name} must have adjacent values, not a stride of {stride[2]}")
     # the stride of a single token or head says nothing: a plain one in its place
-    return (t.data_ptr(), ts if T > 1 else heads * dim, hs if heads > 1 else dim, heads)
+    heads = shape[1]
+    return stride[0] if T > 1 else heads * dim, stride[1] if heads > 1 else dim
 
 
 @functools.lru_cache(maxsize=512)
-def _rope_desc(T, hq, hk, dim, pairs, axes, interleaved, inverse, pos64, strides, sections,
+def _rope_plan(q, k, q_out, k_out, positions, pos64, freq, interleaved, inverse, sections,
                pair_axis):
+    """The descriptor of a call whose tensors have these (shape, stride) pairs."""
+    T, hq, dim = q[0] if len(q[0]) == 3 else (None, None, None)
+    if T is None:
+        raise ValueError("q must be [T, heads, dim]")
+    strides = [_head_strides(*q, "q", T, dim)]
+    strides.append(_head_strides(*k, "k", T, dim) if k else (0, 0))
+    strides.append(_head_strides(*q_out, "q_out", T, dim))
+    strides.append(_head_strides(*k_out, "k_out", T, dim) if k_out else (0, 0))
+    if q_out[0] != q[0] or (k and k_out[0] != k[0]):
+        raise ValueError("an output has another shape than its input")
+    if len(positions) not in (1, 2) or positions[-1] != T:
+        raise ValueError(f"positions has shape {tuple(positions)}, expected [T] or [axes, T]")
+    if len(freq) != 1:
+        raise ValueError("inv_freq must be a vector")
+    axes, pairs = (1 if len(positions) == 1 else positions[0]), freq[0]
     if 2 * pairs > ROPE_MAX_DIM:
         raise BoostError(2, "boost_rope")
-    D = RopeDesc(T, hq, hk, dim, 2 * pairs, axes, interleaved, inverse, pos64, *strides)
+    D = RopeDesc(T, hq, k[0][1] if k else 0, dim, 2 * pairs, axes, interleaved, inverse, pos64,
+                 *(v for pair in strides for v in pair))
     if pair_axis is not None:
         if sections is not None:
             raise ValueError("sections and pair_axis exclude each other")
@@ -540,39 +560,29 @@ def rope(q, k, positions, inv_freq, *, sections=None, pair_axis=None, interleave
     instead. q, k and the outputs take any token and head strides (multiples of 8), so slices
     of a packed projection and [heads, T, dim] tensors seen as [T, heads, dim] are fine, and
     q_out may be q (in place). Positions and frequencies are contiguous."""
-    if q.dim() != 3:
-        raise ValueError("q must be [T, heads, dim]")
-    device = torch.cuda.current_device()
-    T, _, dim = q.shape
-    qp, q_ts, q_hs, hq = _heads(q, "q", T, dim, device)
+    bf, device = torch.bfloat16, torch.cuda.current_device()
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    qop, qo_ts, qo_hs, ho = _heads(q_out, "q_out", T, dim, device)
-    kp = kop = None
-    k_ts = k_hs = ko_ts = ko_hs = hk = hko = 0
+        q_out = torch.empty(q.shape, dtype=bf, device=q.device)
+    ks = kos = kp = kop = None
     if k is not None:
-        kp, k_ts, k_hs, hk = _heads(k, "k", T, dim, device)
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
-        kop, ko_ts, ko_hs, hko = _heads(k_out, "k_out", T, dim, device)
+            k_out = torch.empty(k.shape, dtype=bf, device=k.device)
+        ks, kos = (k.shape, k.stride()), (k_out.shape, k_out.stride())
+        kp, kop = _on(k, "k", bf, device), _on(k_out, "k_out", bf, device)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    if ho != hq or hko != hk:
-        raise ValueError("an output has another number of heads than its input")
     pos64 = positions.dtype is torch.int64
     if not pos64 and positions.dtype is not torch.int32:
         raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    pp = _take(positions, "positions", positions.dtype,
-               (T,) if positions.dim() == 1 else (axes, T), device)
-    pairs = inv_freq.numel()
-    wp = _take(inv_freq, "inv_freq", torch.float64, (pairs,), device)
-    D = _rope_desc(T, hq, hk, dim, pairs, axes, bool(interleaved), bool(inverse), pos64,
-                   (q_ts, q_hs, k_ts, k_hs, qo_ts, qo_hs, ko_ts, ko_hs),
+    D = _rope_plan((q.shape, q.stride()), ks, (q_out.shape, q_out.stride()), kos,
+                   positions.shape, pos64, inv_freq.shape, bool(interleaved), bool(inverse),
                    None if sections is None else tuple(sections),
                    None if pair_axis is None else tuple(pair_axis))
-    _check(lib().boost_rope(D, qp, kp, pp, wp, qop, kop, _raw_stream(stream, device)),
-           "boost_rope")
+    _check(lib().boost_rope(
+        D, _on(q, "q", bf, device), kp,
+        _take(positions, "positions", positions.dtype, positions.shape, device),
+        _take(inv_freq, "inv_freq", torch.float64, inv_freq.shape, device),
+        _on(q_out, "q_out", bf, device), kop, _raw_stream(stream, device)), "boost_rope")
     return q_out, k_out
 
 
@@ -609,15 +619,33 @@ def fp8_scale_bytes(rows, K) -> int:
     return -(-rows // 128) * -(-K // 512) * 512
 
 
-def _operand_out(given, name, lead, rows, K, dtype, x, device):
+def _operand_out(given, name, shape, planes, dtype, device_of, device):
     """The (values, scales) tensors of a quantised operand and their addresses."""
-    shape, planes = lead + (rows, -(-K // 16) * 16), lead + (fp8_scale_bytes(rows, K),)
     if given is None:
-        q = torch.empty(shape, dtype=dtype, device=x.device)
-        sf = torch.empty(planes, dtype=torch.uint8, device=x.device)
+        q = torch.empty(shape, dtype=dtype, device=device_of)
+        sf = torch.empty(planes, dtype=torch.uint8, device=device_of)
         return (q, sf), q.data_ptr(), sf.data_ptr()
     return (given, _take(given[0], name, dtype, shape, device),
             _take(given[1], f"{name} scales", torch.uint8, planes, device))
+
+
+@functools.lru_cache(maxsize=512)
+def _fp8_quant_plan(dims, strides, fmt, block_rows):
+    """(descriptor, type, values' and scales' shapes by rows, by columns) of a matrix or
+    matrices with these dimensions and strides."""
+    code, dtype = FP8_FORMATS[fmt]
+    if len(dims) not in (2, 3) or (dims[-1] > 1 and strides[-1] != 1):
+        raise ValueError("x must be [rows, cols] or [G, rows, cols] with adjacent columns")
+    lead = tuple(dims[:-2])
+    G, (rows, cols) = (lead[0] if lead else 1), dims[-2:]
+    # the stride of a single row or matrix says nothing: a plain one in its place
+    D = Fp8QuantDesc(G, rows, cols, strides[-2] if rows > 1 else cols,
+                     strides[0] if G > 1 else 0, code, block_rows)
+
+    def shapes(r, K):
+        return lead + (r, -(-K // 16) * 16), lead + (fp8_scale_bytes(r, K),)
+
+    return D, dtype, shapes(rows, cols), shapes(cols, rows)
 
 
 def fp8_quantize(x, *, fmt="e4m3", block_rows=1, way="rows", gamma=None, rows_out=None,
@@ -632,30 +660,21 @@ def fp8_quantize(x, *, fmt="e4m3", block_rows=1, way="rows", gamma=None, rows_ou
     ``rows_out``, ``cols_out``: (q, scales) tensors to write into."""
     if fmt not in FP8_FORMATS or way not in ("rows", "columns", "both"):
         raise ValueError("fmt is 'e4m3' or 'e5m2', way 'rows', 'columns' or 'both'")
-    code, dtype = FP8_FORMATS[fmt]
     device = torch.cuda.current_device()
-    if x.dtype is not torch.bfloat16 or x.get_device() != device:
-        _refuse(x, "x", torch.bfloat16, x.shape, device)
-    dims, strides = x.shape, x.stride()
-    if len(dims) not in (2, 3) or (dims[-1] > 1 and strides[-1] != 1):
-        raise ValueError("x must be [rows, cols] or [G, rows, cols] with adjacent columns")
-    lead = tuple(dims[:-2])
-    G, (rows, cols) = (lead[0] if lead else 1), dims[-2:]
-    gp = None if gamma is None else _take(gamma, "gamma", torch.bfloat16, (rows,), device)
+    xp = _on(x, "x", torch.bfloat16, device)
+    D, dtype, of_rows, of_cols = _fp8_quant_plan(x.shape, x.stride(), fmt, block_rows)
+    gp = None if gamma is None else _take(gamma, "gamma", torch.bfloat16, (D.rows,), device)
     by_rows = by_cols = q = sf = qt = sft = None
     if way != "columns":
-        by_rows, q, sf = _operand_out(rows_out, "rows_out", lead, rows, cols, dtype, x, device)
+        by_rows, q, sf = _operand_out(rows_out, "rows_out", *of_rows, dtype, x.device, device)
     elif rows_out is not None:
         raise ValueError("rows_out given, but way is 'columns'")
     if way != "rows":
-        by_cols, qt, sft = _operand_out(cols_out, "cols_out", lead, cols, rows, dtype, x, device)
+        by_cols, qt, sft = _operand_out(cols_out, "cols_out", *of_cols, dtype, x.device, device)
     elif cols_out is not None:
         raise ValueError("cols_out given, but way is 'rows'")
-    # the stride of a single row or matrix says nothing: a plain one in its place
-    D = Fp8QuantDesc(G, rows, cols, strides[-2] if rows > 1 else cols,
-                     strides[0] if G > 1 else 0, code, block_rows)
-    _check(lib().boost_fp8_quantize(D, x.data_ptr(), gp, q, sf, qt, sft,
-                                    _raw_stream(stream, device)), "boost_fp8_quantize")
+    _check(lib().boost_fp8_quantize(D, xp, gp, q, sf, qt, sft, _raw_stream(stream, device)),
+           "boost_fp8_quantize")
     return by_rows, by_cols
 
 
@@ -665,32 +684,39 @@ def fp8_matmul_workspace_bytes(M, N, K, G=1) -> int:
         Fp8MatmulDesc(G, M, N, K, pitch, pitch, 0, 0, 0)))
 
 
+@functools.lru_cache(maxsize=512)
+def _fp8_matmul_plan(da, db, a_dtype, b_dtype, K, act):
+    """(descriptor, shapes of a's and b's scales, of the result, of a row scale)."""
+    lead = tuple(da[:-2])
+    if len(da) not in (2, 3) or len(db) != len(da) or tuple(db[:-2]) != lead:
+        raise ValueError("operands must be [M, pitch] and [N, pitch], or [G, ...] of them")
+    if a_dtype not in FP8_CODE or b_dtype not in FP8_CODE:
+        raise TypeError(f"operands must be float8_e4m3fn or float8_e5m2, got {a_dtype}, {b_dtype}")
+    M, N = da[-2], db[-2]
+    D = Fp8MatmulDesc(lead[0] if lead else 1, M, N, K, da[-1], db[-1], FP8_CODE[a_dtype],
+                      FP8_CODE[b_dtype], ACT[act])
+    return (D, lead + (fp8_scale_bytes(M, K),), lead + (fp8_scale_bytes(N, K),), lead + (M, N),
+            (M,))
+
+
 def fp8_matmul(a, a_scales, b, b_scales, K, ws: Workspace, *, row_scale=None, act="identity",
                out=None, stream=None):
     """act(row_scale * (A @ B^T)) [M, N] in bf16 of 8-bit operands A [M, pitch], B [N, pitch]
     with their scales (``fp8_quantize``), K values contracted; [G, ...] operands give the G
     products [G, M, N]. row_scale: float32 [M]."""
     device = torch.cuda.current_device()
-    da, db = a.shape, b.shape
-    lead = tuple(da[:-2])
-    if len(da) not in (2, 3) or len(db) != len(da) or tuple(db[:-2]) != lead:
-        raise ValueError("operands must be [M, pitch] and [N, pitch], or [G, ...] of them")
-    if a.dtype not in FP8_CODE or b.dtype not in FP8_CODE:
-        raise TypeError(f"operands must be float8_e4m3fn or float8_e5m2, got {a.dtype}, {b.dtype}")
-    G, M, N = (lead[0] if lead else 1), da[-2], db[-2]
+    da, db, ta, tb, wb = a.shape, b.shape, a.dtype, b.dtype, ws.buf
+    D, a_planes, b_planes, shape, rows = _fp8_matmul_plan(da, db, ta, tb, K, act)
     if out is None:
-        out = torch.empty(lead + (M, N), dtype=torch.bfloat16, device=a.device)
-    D = Fp8MatmulDesc(G, M, N, K, da[-1], db[-1], FP8_CODE[a.dtype], FP8_CODE[b.dtype], ACT[act])
-    wb = ws.buf
+        out = torch.empty(shape, dtype=torch.bfloat16, device=a.device)
     _check(lib().boost_fp8_matmul(
-        D, _take(a, "a", a.dtype, da, device),
-        _take(a_scales, "a_scales", torch.uint8, lead + (fp8_scale_bytes(M, K),), device),
-        _take(b, "b", b.dtype, db, device),
-        _take(b_scales, "b_scales", torch.uint8, lead + (fp8_scale_bytes(N, K),), device),
-        None if row_scale is None else _take(row_scale, "row_scale", torch.float32, (M,), device),
-        _take(out, "out", torch.bfloat16, lead + (M, N), device),
-        _take(wb, "ws", torch.uint8, wb.shape, device), ws.nbytes, _raw_stream(stream, device)),
-        "boost_fp8_matmul")
+        D, _take(a, "a", ta, da, device),
+        _take(a_scales, "a_scales", torch.uint8, a_planes, device),
+        _take(b, "b", tb, db, device),
+        _take(b_scales, "b_scales", torch.uint8, b_planes, device),
+        None if row_scale is None else _take(row_scale, "row_scale", torch.float32, rows, device),
+        _take(out, "out", torch.bfloat16, shape, device), _on(wb, "ws", torch.uint8, device),
+        ws.nbytes, _raw_stream(stream, device)), "boost_fp8_matmul")
     return out
 
 
