@@ -2,10 +2,12 @@
 // counter and never stored.
 //
 // One Philox4x32-10 block (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy
-// as 1, 2, 3", SC 2011) gives the 16-bit draws of 8 elements, one 16-byte vector. Two
-// draws a word rather than one: the ten rounds cost about 60 integer instructions, 7.5 an
-// element, which stay under the 6 bytes an element of HBM traffic; with one draw a word the
-// gradient pass (4 bytes an element) would be bound by the integer pipe.
+// as 1, 2, 3", SC 2011) gives the 16-bit draws of 8 elements, one 16-byte vector: 40
+// instructions for the ten rounds (the rounds' keys are launch parameters) and about 15 an
+// element in all. With a residual the pass is bound by HBM (6 bytes an element; 16384 x 4096:
+// 57 us, 7.0 TB/s, the measured copy rate). The gradient moves 4 bytes an element and issue slots
+// are 56% busy (8191 x 5120: 28 us, 6.0 TB/s, 88%), which is why a word gives two draws: with
+// one, the rounds would cost twice as much and bind it.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -26,46 +28,43 @@ struct DropoutParams {
   uint4* out;
   const uint64_t* counter;     // or NULL
   int64_t count;
-  uint64_t seed, offset;
+  uint64_t offset;
+  uint32_t key[10][2];         // the seed's words, raised by the generator's steps each round
   uint32_t drop;               // 65536 times the draw below which an element is dropped
   float scale;                 // 65536 / (65536 - drop)
 };
 
-// The Philox4x32-10 block of counter c and key (k0, k1), in place.
-__device__ __forceinline__ void philox(uint32_t (&c)[4], uint32_t k0, uint32_t k1) {
+// The Philox4x32-10 block of vector g.
+__device__ __forceinline__ void draw(const DropoutParams& p, uint64_t offset, int64_t g,
+                                     uint32_t (&c)[4]) {
+  c[0] = static_cast<uint32_t>(g);
+  c[1] = static_cast<uint32_t>(g >> 32);
+  c[2] = static_cast<uint32_t>(offset);
+  c[3] = static_cast<uint32_t>(offset >> 32);
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t p0 = static_cast<uint64_t>(c[0]) * 0xD2511F53u;
     const uint64_t p1 = static_cast<uint64_t>(c[2]) * 0xCD9E8D57u;
-    const uint32_t n0 = static_cast<uint32_t>(p1 >> 32) ^ c[1] ^ k0;
-    const uint32_t n2 = static_cast<uint32_t>(p0 >> 32) ^ c[3] ^ k1;
+    const uint32_t n0 = static_cast<uint32_t>(p1 >> 32) ^ c[1] ^ p.key[r][0];
+    const uint32_t n2 = static_cast<uint32_t>(p0 >> 32) ^ c[3] ^ p.key[r][1];
     c[1] = static_cast<uint32_t>(p1);
     c[3] = static_cast<uint32_t>(p0);
     c[0] = n0;
     c[2] = n2;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
 }
 
-// Which of vector g's 8 elements are kept, as masks of its words' halves: a draw is compared as
-// the upper half of a word, whose lower half cannot change the answer.
-__device__ __forceinline__ uint4 keep_masks(const DropoutParams& p, uint64_t offset, int64_t g) {
-  uint32_t c[4] = {static_cast<uint32_t>(g), static_cast<uint32_t>(g >> 32),
-                   static_cast<uint32_t>(offset), static_cast<uint32_t>(offset >> 32)};
-  philox(c, static_cast<uint32_t>(p.seed), static_cast<uint32_t>(p.seed >> 32));
-  uint32_t m[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    m[j] = (c[j] << 16 >= p.drop ? 0xffffu : 0u) | (c[j] >= p.drop ? 0xffff0000u : 0u);
-  return make_uint4(m[0], m[1], m[2], m[3]);
+// A word's two bf16 values with the dropped ones zero: a draw is compared as the upper half of
+// a word, whose lower half cannot change the answer.
+__device__ __forceinline__ uint32_t kept(uint32_t word, uint32_t c, uint32_t drop) {
+  if (c << 16 < drop) word &= 0xffff0000u;
+  if (c < drop) word &= 0xffffu;
+  return word;
 }
 
-__device__ __forceinline__ uint4 operator&(const uint4& a, const uint4& b) {
-  return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w);
-}
-
-constexpr int kBatch = 2;      // vectors in flight a thread
+// Vectors in flight a thread. With 1 to 4 (and the keys still formed here) the gradient took
+// 33.6, 30.2, 29.5, 29.5 us, a short batch (77 x 2048, both ways) 4.9, 4.9, 5.6, 6.3 us.
+constexpr int kBatch = 2;
 
 template <bool RES>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p) {
@@ -87,7 +86,10 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p
     const int64_t g = first + b * kThreads;
     if (g < vectors) {
       float f[8], s[8];
-      unpack8(x[b] & keep_masks(p, offset, g), f);
+      uint32_t c[4];
+      draw(p, offset, g, c);
+      unpack8(make_uint4(kept(x[b].x, c[0], p.drop), kept(x[b].y, c[1], p.drop),
+                         kept(x[b].z, c[2], p.drop), kept(x[b].w, c[3], p.drop)), f);
       if (RES) unpack8(r[b], s);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = RES ? fmaf(f[e], p.scale, s[e]) : f[e] * p.scale;
@@ -97,10 +99,11 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p
   // the last, partly filled vector
   const int tail = static_cast<int>(p.count & 7);
   if (blockIdx.x == 0 && threadIdx.x < tail) {
-    const uint4 m = keep_masks(p, offset, vectors);
+    uint32_t c[4];
+    draw(p, offset, vectors, c);
     const int j = threadIdx.x >> 1;
-    const uint32_t word = j == 0 ? m.x : j == 1 ? m.y : j == 2 ? m.z : m.w;
-    const bool keep = (threadIdx.x & 1 ? word >> 16 : word & 0xffffu) != 0;
+    const uint32_t word = j == 0 ? c[0] : j == 1 ? c[1] : j == 2 ? c[2] : c[3];
+    const bool keep = (threadIdx.x & 1 ? word : word << 16) >= p.drop;
     const int64_t e = vectors * 8 + threadIdx.x;
     const float f = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.x)[e]);
     const float s = RES ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.res)[e]) : 0.0f;
@@ -146,7 +149,10 @@ extern "C" boost_status boost_dropout(int64_t count, const void* x, const void* 
   d.out = static_cast<uint4*>(out);
   d.counter = counter;
   d.count = count;
-  d.seed = seed;
+  for (uint32_t r = 0; r < 10; ++r) {
+    d.key[r][0] = static_cast<uint32_t>(seed) + r * 0x9E3779B9u;
+    d.key[r][1] = static_cast<uint32_t>(seed >> 32) + r * 0xBB67AE85u;
+  }
   d.offset = offset;
   d.drop = static_cast<uint32_t>(drop) << 16;
   d.scale = static_cast<float>(65536.0 / (65536.0 - drop));
