@@ -201,6 +201,18 @@ def test_product(shape):
     product_check((), *shape)
 
 
+@pytest.mark.parametrize("shape", [(4700, 5128, 300), (2500, 6152, 1000), (100, 25608, 256)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_product_with_more_tiles_than_fit_at_once(shape):
+    """Several tiles a CTA: both accumulators in turn (the wide tile's share columns), the ring
+    and the scale buffers going on from tile to tile, for CTA pairs and single CTAs."""
+    product_check((), *shape, scaled=True)
+
+
+def test_product_batch_with_more_tiles_than_fit_at_once():
+    product_check((3,), 1300, 2056, 140)
+
+
 @pytest.mark.parametrize("fa", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("fb", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("M", [5, 300])
