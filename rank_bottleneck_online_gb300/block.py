@@ -1,5 +1,6 @@
 """Workloads composed from the C-ABI calls: one block, the LLaMA MLP, the full
-layer without its attention core, and the SVD-style pair.
+layer without its attention core, and the SVD-style pair; a block whose forward
+multiplies in 8 bits; rotary positions and dropout in the layer.
 
 Each workload owns its device tensors (weights, saved activations, gradients
 and one workspace) so that a training step is a fixed sequence of library
