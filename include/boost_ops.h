@@ -121,6 +121,7 @@ size_t boost_fp8_scale_bytes(int64_t rows, int64_t K);
  *   block_rows  1: each row (of q; each column for qt) has its own scales; 128: a block is
  *               128 x 128, so q and qt hold the same values
  *   ldx, gstride  row and matrix strides of x in elements, multiples of 8
+ *   rows        at most 2097120
  *   cols        a multiple of 8
  *   gamma       [rows] or NULL: x is replaced by bf16(gamma[row] * x), the fold of a
  *               norm's weight into a down-projection weight; block_rows 128 or qt only
@@ -140,12 +141,13 @@ boost_status boost_fp8_quantize(const boost_fp8_quant_desc* desc, const void* x,
 /*
  * out[g] = act(row_scale (.) (A[g] @ B[g]^T)), g < G, A [M, K], B [N, K], out [M, N] bf16,
  * products and sums in fp32 on the tensor cores.
- *   G, M, N, K   K >= 0 (K == 0: out = act(0) = 0)
+ *   G, M, N, K   K >= 0 (K == 0: out = act(0) = 0); a matrix of an operand or of out is
+ *                smaller than 2^40 bytes
  *   a_pitch, b_pitch   bytes between rows of the operands, multiples of 16, >= K
  *   a_fmt, b_fmt  boost_fp8
  *   act          boost_act, applied after the row scale
  *   row_scale    [M] fp32 or NULL: the deferred 1/rms of a normed block
- *   out          [G, M, N] bf16; N a multiple of 8
+ *   out          [G, M, N] bf16; N a multiple of 8, at most 1048560
  *   ws           workspace of boost_fp8_matmul_workspace_bytes(desc) bytes or more,
  *                256-byte aligned, error word cleared by boost_block_ws_init
  * A gradient is the same product on operands quantised the other way: for y = x W^T,

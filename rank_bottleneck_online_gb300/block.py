@@ -88,6 +88,8 @@ class Fp8Block(Block):
 
     def forward(self, x, stream=None, residual=None):
         D = self.desc
+        if residual is not None and D.k != 1:
+            raise ValueError("a residual needs one output group")
         if D.has_norm:
             B.rmsnorm_stats(D, x, self.ssq, self.rstd, stream)
         B.fp8_quantize(x, rows_out=self.x8, stream=stream)
@@ -97,8 +99,6 @@ class Fp8Block(Block):
         B.fp8_quantize(groups, rows_out=self.a8, stream=stream)
         B.fp8_matmul(*self.a8, *self.B8, D.r, self.ws8, out=self.y, stream=stream)
         if residual is not None:
-            if D.k != 1:
-                raise ValueError("a residual needs one output group")
             B.add(self.y[0], residual, self.y[0], stream=stream)
         return self.y
 
