@@ -491,6 +491,11 @@ def _take(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
+# the current device, and its current stream, of torch's own bookkeeping
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else \
+    torch.cuda.current_device
+
+
 def _raw_stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
@@ -560,7 +565,7 @@ def rope(q, k, positions, inv_freq, *, sections=None, pair_axis=None, interleave
     instead. q, k and the outputs take any token and head strides (multiples of 8), so slices
     of a packed projection and [heads, T, dim] tensors seen as [T, heads, dim] are fine, and
     q_out may be q (in place). Positions and frequencies are contiguous."""
-    bf, device = torch.bfloat16, torch.cuda.current_device()
+    bf, device = torch.bfloat16, _device()
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=bf, device=q.device)
     ks = kos = kp = kop = None
@@ -590,7 +595,7 @@ def dropout_add(x, p, seed, offset=0, *, residual=None, out=None, counter=None, 
     """residual + dropout(x): the element at flat index e is kept by a pure function of (e,
     seed, offset), so no mask is stored (``boost_dropout``). ``counter``: an int64 tensor of
     one value, added to the offset when the kernel runs, for replayed graphs."""
-    bf, shape, device = torch.bfloat16, x.shape, torch.cuda.current_device()
+    bf, shape, device = torch.bfloat16, x.shape, _device()
     xp = _take(x, "x", bf, shape, device)
     if out is None:
         out = torch.empty(shape, dtype=bf, device=x.device)
@@ -660,7 +665,7 @@ def fp8_quantize(x, *, fmt="e4m3", block_rows=1, way="rows", gamma=None, rows_ou
     ``rows_out``, ``cols_out``: (q, scales) tensors to write into."""
     if fmt not in FP8_FORMATS or way not in ("rows", "columns", "both"):
         raise ValueError("fmt is 'e4m3' or 'e5m2', way 'rows', 'columns' or 'both'")
-    device = torch.cuda.current_device()
+    device = _device()
     xp = _on(x, "x", torch.bfloat16, device)
     D, dtype, of_rows, of_cols = _fp8_quant_plan(x.shape, x.stride(), fmt, block_rows)
     gp = None if gamma is None else _take(gamma, "gamma", torch.bfloat16, (D.rows,), device)
@@ -704,7 +709,7 @@ def fp8_matmul(a, a_scales, b, b_scales, K, ws: Workspace, *, row_scale=None, ac
     """act(row_scale * (A @ B^T)) [M, N] in bf16 of 8-bit operands A [M, pitch], B [N, pitch]
     with their scales (``fp8_quantize``), K values contracted; [G, ...] operands give the G
     products [G, M, N]. row_scale: float32 [M]."""
-    device = torch.cuda.current_device()
+    device = _device()
     da, db, ta, tb, wb = a.shape, b.shape, a.dtype, b.dtype, ws.buf
     D, a_planes, b_planes, shape, rows = _fp8_matmul_plan(da, db, ta, tb, K, act)
     if out is None:
