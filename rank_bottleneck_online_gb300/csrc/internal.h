@@ -28,7 +28,7 @@ bool pdl_enabled();
 int current_num_sms();
 // Limit of every device-side wait (BOOST_WAIT_LIMIT_MS, 2 s by default).
 uint64_t wait_limit_ns();
-// The driver's cuTensorMapEncodeTiled, or NULL without a driver.
+// The CUDA driver API's cuTensorMapEncodeTiled, or NULL where there is none.
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                               const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
