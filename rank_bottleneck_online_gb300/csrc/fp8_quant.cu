@@ -39,6 +39,18 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
+// The same, but a NaN stays.
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// Whether a pair of magnitudes holds an infinity or a NaN: 0x7f80 and above carry into bit 15.
+__device__ __forceinline__ bool not_finite2(uint32_t m) {
+  return ((m + 0x00800080u) & 0x80008000u) != 0;
+}
+
 // Magnitudes of a pair, infinities and NaN as 0.
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
   uint32_t m = w & 0x7fff7fffu;
@@ -98,16 +110,16 @@ __device__ __forceinline__ float2 mul2(float a, float b, float f) {
   return r;
 }
 
-// 8 values (a vector's four words) times `inv` to 8 bytes.
+// 8 values (a vector's four words) times `inv` to 8 bytes; with `mend` there may be infinities.
 template <int FMT>
-__device__ __forceinline__ uint2 quant8(const uint32_t* w, float inv, bool inf) {
+__device__ __forceinline__ uint2 quant8(const uint32_t* w, float inv, bool mend) {
   uint32_t p[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 v = mul2(bf16_lo(w[i]), bf16_hi(w[i]), inv);
     p[i] = to8<FMT>(v.x, v.y);
   }
-  if (inf) {
+  if (mend) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       p[i] = mend_inf<FMT>(w[i] & 0xffffu, p[i] & 0xffu) |
@@ -116,14 +128,13 @@ __device__ __forceinline__ uint2 quant8(const uint32_t* w, float inv, bool inf) 
   return make_uint2(p[0] | p[1] << 16, p[2] | p[3] << 16);
 }
 
-// Largest magnitudes of kRows rows over the kLanes lanes (a power of two) that hold a block, in
-// `top`: with infinities where there are some, and those then again over the finite values,
-// which is what the scale comes from. Two rows go through the shuffles in the halves of a
-// word. Returns a bit for each row whose block holds an infinity (or nothing but NaN). Without
-// kMayInf every value is known to be finite.
+// Largest finite magnitudes of kRows rows over the kLanes lanes (a power of two) that hold a
+// block; two rows go through the shuffles in the halves of a word. Returns whether a block of
+// the warp holds an infinity (or nothing but NaN). Without kMayInf every value is known to be
+// finite.
 template <int kRows, int kWords, int kLanes, bool kMayInf = true>
-__device__ __forceinline__ uint32_t block_tops(const uint32_t (&w)[kRows][kWords],
-                                               uint32_t (&top)[kRows]) {
+__device__ __forceinline__ bool block_tops(const uint32_t (&w)[kRows][kWords],
+                                           uint32_t (&top)[kRows]) {
   uint32_t two[kRows / 2];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
@@ -141,18 +152,15 @@ __device__ __forceinline__ uint32_t block_tops(const uint32_t (&w)[kRows][kWords
 #pragma unroll
     for (int r = 0; r < kRows / 2; ++r)
       two[r] = max2(two[r], __shfl_xor_sync(0xffffffffu, two[r], o));
-  uint32_t inf = 0;
+  bool special = false;
 #pragma unroll
   for (int r = 0; r < kRows / 2; ++r) {
-    // (a block of NaN alone leaves a NaN here: no finite value, as 0)
     top[2 * r] = two[r] & 0xffffu;
     top[2 * r + 1] = two[r] >> 16;
-    if (kMayInf) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) inf |= (top[2 * r + h] >= kInf ? 1u : 0u) << (2 * r + h);
-    }
+    if (kMayInf) special |= not_finite2(two[r]);
   }
-  if (kMayInf && __any_sync(0xffffffffu, inf != 0)) {
+  if (kMayInf) special = __any_sync(0xffffffffu, special);
+  if (special) {                                   // again over the finite values
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       uint32_t f = 0;
@@ -161,10 +169,10 @@ __device__ __forceinline__ uint32_t block_tops(const uint32_t (&w)[kRows][kWords
       f = larger_half(f);
 #pragma unroll
       for (int o = 1; o < kLanes; o <<= 1) f = max(f, __shfl_xor_sync(0xffffffffu, f, o));
-      if (inf >> r & 1) top[r] = f;
+      top[r] = f;
     }
   }
-  return inf;
+  return special;
 }
 
 // ------------------------------------------------------------------- rows alone
@@ -192,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const QuantPara
     }
   }
   uint32_t top[4];
-  const uint32_t infs = block_tops<4, 8, 8>(w, top);
+  const bool mend = block_tops<4, 8, 8>(w, top);
   uint8_t* q = p.q + (blockIdx.z * p.rows + row0) * p.pitch + col;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * 4;      // block of lane 0
   uint8_t* sf = p.sf + blockIdx.z * p.plane + scale_at(row0, first, p.kt);
@@ -202,8 +210,7 @@ __global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const QuantPara
     const uint32_t byte = scale_byte<FMT>(top[r]);
     if (r < rows && col < p.pitch) {
       const float inv = scale_inverse(byte);
-      const bool inf = infs >> r & 1;
-      const uint2 a = quant8<FMT>(w[r], inv, inf), b = quant8<FMT>(w[r] + 4, inv, inf);
+      const uint2 a = quant8<FMT>(w[r], inv, mend), b = quant8<FMT>(w[r] + 4, inv, mend);
       *reinterpret_cast<uint4*>(q + r * p.pitch) = make_uint4(a.x, a.y, b.x, b.y);
     }
     // the four blocks' bytes, 127 outside the operand
@@ -223,15 +230,15 @@ __global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const QuantPara
 // pass is close to the issue rate, so every address is a base and a small stride, and tiles
 // that lie inside x and are finite, by far the most, skip the checks of both. (A persistent
 // form with the next tile on its way by cp.async was slower, 67 us against 57 before that
-// last step: its shared memory leaves three blocks an SM, not four.) 16384 x 4096 both ways: 50 us,
-// 5.4 TB/s, 79% of the measured copy rate.
+// last step: its shared memory leaves three blocks an SM, not four.) 16384 x 4096 both ways: 48 us,
+// 5.6 TB/s, 83% of the measured copy rate.
 // grid = (column tiles, row tiles, matrices).
 
-// Thread c2 < 64 stores the scales of the tile's columns 2 c2 and 2 c2 + 1, whose largest finite
+// Thread c < 64 stores the scales of the tile's columns 2 c and 2 c + 1, whose largest finite
 // magnitudes are `top`: one byte a block; the last row tile fills its scale tile.
 template <int FMT>
 __device__ __forceinline__ void column_scales(const QuantParams& p, uint32_t top) {
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 128 + 2 * (threadIdx.x & 63);
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 128 + 2 * threadIdx.x;
   const int64_t b0 = blockIdx.y, blocks = (p.rows + 127) / 128;
   const int64_t end = b0 + 1 == gridDim.y ? 4 * p.kt_t : b0 + 1;
 #pragma unroll
@@ -247,8 +254,7 @@ __device__ __forceinline__ void column_scales(const QuantParams& p, uint32_t top
 // inside x and holds finite values alone.
 template <int FMT, bool SQUARE, bool PLAIN>
 __device__ __forceinline__ void write_tile(const QuantParams& p, const uint32_t (&w)[8][4],
-                                           const uint32_t* col_all, const uint32_t* col_top,
-                                           uint8_t* bytes) {
+                                           const uint32_t* col_top, uint8_t* bytes) {
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
   const int64_t row0 = static_cast<int64_t>(blockIdx.y) * 128;
   const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 128;
@@ -256,26 +262,20 @@ __device__ __forceinline__ void write_tile(const QuantParams& p, const uint32_t 
   const int rows = PLAIN ? 8 : static_cast<int>(min(max(p.rows - row, static_cast<int64_t>(0)),
                                                     static_cast<int64_t>(8)));
   uint32_t tile_top = 0, tile_byte = 0;
-  bool tile_inf = false;
   if constexpr (SQUARE) {
     const int lane = threadIdx.x & 31;
-    uint32_t m = max2(col_all[lane], col_all[lane + 32]);
-    uint32_t f = max2(col_top[lane], col_top[lane + 32]);
+    uint32_t m = max2(col_top[lane], col_top[lane + 32]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      m = max2(m, __shfl_xor_sync(0xffffffffu, m, o));
-      f = max2(f, __shfl_xor_sync(0xffffffffu, f, o));
-    }
-    tile_top = larger_half(f);
+    for (int o = 16; o > 0; o >>= 1) m = max2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    tile_top = larger_half(m);
     tile_byte = scale_byte<FMT>(tile_top);
-    tile_inf = !PLAIN && larger_half(m) == kInf;
   }
 
   if (p.q != nullptr) {
     const int64_t b0 = static_cast<int64_t>(blockIdx.x), blocks = (p.cols + 127) / 128;
     uint8_t* q = p.q + (blockIdx.z * p.rows + row) * p.pitch + col;
-    uint32_t top[8], infs = 0;
-    if constexpr (!SQUARE) infs = block_tops<8, 4, 16, !PLAIN>(w, top);
+    uint32_t top[8];
+    if constexpr (!SQUARE) block_tops<8, 4, 16, !PLAIN>(w, top);
     // one byte a block; the last column tile fills its scale tile
     const int64_t b = b0 + cg;
     const bool writes = cg == 0 || (b0 + 1 == gridDim.x && b < 4 * p.kt);
@@ -287,8 +287,7 @@ __device__ __forceinline__ void write_tile(const QuantParams& p, const uint32_t 
       // (eight rows of one quarter of a scale tile lie 16 bytes apart)
       if (writes) sf[16 * r] = stored_byte(byte, top[r], r < rows && b < blocks);
       if (PLAIN || (r < rows && col < p.pitch))
-        *reinterpret_cast<uint2*>(q) = quant8<FMT>(
-            w[r], scale_inverse(byte), !PLAIN && (SQUARE ? tile_inf : (infs >> r & 1) != 0));
+        *reinterpret_cast<uint2*>(q) = quant8<FMT>(w[r], scale_inverse(byte), !PLAIN);
       q += p.pitch;
     }
   }
@@ -298,18 +297,16 @@ __device__ __forceinline__ void write_tile(const QuantParams& p, const uint32_t 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t t = SQUARE ? 0 : col_top[cg * 4 + i];
-      const uint32_t a = SQUARE || PLAIN ? 0 : col_all[cg * 4 + i];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int c = 2 * i + h;
         const uint32_t byte =
             SQUARE ? tile_byte : scale_byte<FMT>(h ? t >> 16 : t & 0xffffu);
-        const bool inf = !PLAIN && (SQUARE ? tile_inf : (h ? a >> 16 : a & 0xffffu) == kInf);
         uint32_t v[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)     // rows 2 r and 2 r + 1 of this column
           v[r] = __byte_perm(w[2 * r][i], w[2 * r + 1][i], h ? 0x7632 : 0x5410);
-        *reinterpret_cast<uint2*>(slot + c * 128) = quant8<FMT>(v, scale_inverse(byte), inf);
+        *reinterpret_cast<uint2*>(slot + c * 128) = quant8<FMT>(v, scale_inverse(byte), !PLAIN);
       }
     }
     if (SQUARE && threadIdx.x < 64) column_scales<FMT>(p, tile_top | tile_top << 16);
@@ -335,9 +332,8 @@ template <int FMT, bool SQUARE>
 __global__ void __launch_bounds__(kThreads, 4) quant_tile_kernel(const QuantParams p) {
   pdl_enter();
   __shared__ __align__(16) uint8_t bytes[128 * 128];
-  __shared__ uint32_t part[2][16][64];  // a row group's column maxima, in pairs:
-                                        // of all magnitudes, of the finite ones
-  __shared__ uint32_t col_all[64], col_top[64];         // the tile's
+  __shared__ uint32_t part[16][64];     // a row group's largest finite column magnitudes, in pairs
+  __shared__ uint32_t col_top[64];      // the tile's
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
   const int64_t row = static_cast<int64_t>(blockIdx.y) * 128 + rg * 8;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 128 + cg * 8;
@@ -367,37 +363,28 @@ __global__ void __launch_bounds__(kThreads, 4) quant_tile_kernel(const QuantPara
   bool other = !inside;                 // than PLAIN
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    // (max.NaN would keep a NaN; here one gives way, so it is looked for in the sum of the
-    // exponents' overflow: 0x7f80 and above carry into bit 15)
-    uint32_t m = w[0][i] & 0x7fff7fffu, over = m + 0x00800080u;
+    uint32_t m = w[0][i] & 0x7fff7fffu;
 #pragma unroll
-    for (int r = 1; r < 8; ++r) {
-      const uint32_t a = w[r][i] & 0x7fff7fffu;
-      m = max2(m, a);
-      over |= a + 0x00800080u;
-    }
-    uint32_t f = m;
-    if ((over & 0x80008000u) != 0) {
+    for (int r = 1; r < 8; ++r) m = max2_nan(m, w[r][i] & 0x7fff7fffu);
+    if (not_finite2(m)) {
       other = true;
-      f = 0;
+      m = 0;
 #pragma unroll
-      for (int r = 0; r < 8; ++r) f = max2(f, finite2(w[r][i]));
+      for (int r = 0; r < 8; ++r) m = max2(m, finite2(w[r][i]));
     }
-    part[0][rg][cg * 4 + i] = m;
-    part[1][rg][cg * 4 + i] = f;
+    part[rg][cg * 4 + i] = m;
   }
   const bool plain = __syncthreads_or(other) == 0;
-  if (threadIdx.x < 128) {
-    const int which = threadIdx.x >> 6, c2 = threadIdx.x & 63;
+  if (threadIdx.x < 64) {
     uint32_t m = 0;
 #pragma unroll
-    for (int g = 0; g < 16; ++g) m = max2(m, part[which][g][c2]);
-    (which == 0 ? col_all : col_top)[c2] = m;
-    if (!SQUARE && which == 1 && p.qt != nullptr) column_scales<FMT>(p, m);
+    for (int g = 0; g < 16; ++g) m = max2(m, part[g][threadIdx.x]);
+    col_top[threadIdx.x] = m;
+    if (!SQUARE && p.qt != nullptr) column_scales<FMT>(p, m);
   }
   __syncthreads();
-  if (plain) write_tile<FMT, SQUARE, true>(p, w, col_all, col_top, bytes);
-  else write_tile<FMT, SQUARE, false>(p, w, col_all, col_top, bytes);
+  if (plain) write_tile<FMT, SQUARE, true>(p, w, col_top, bytes);
+  else write_tile<FMT, SQUARE, false>(p, w, col_top, bytes);
 }
 
 }  // namespace
