@@ -62,7 +62,7 @@ struct Fp8Cfg {
   static constexpr int kBRows = BN / CG;               // B rows staged by one CTA
   static constexpr int kABytes = kBM * kKBytes;
   static constexpr int kBBytes = kBRows * kKBytes;
-  static constexpr int kSfTilesB = (BN + 127) / 128;
+  static constexpr int kSfTilesB = BN / 128;
   static constexpr int kSfBytes = kScaleTile * (1 + kSfTilesB);
   static constexpr int kStgBytes = kEpiW * 2048;
   static constexpr int kStages0 = (232448 - 2048 - kStgBytes) / (kABytes + kBBytes + kSfBytes);
@@ -78,7 +78,7 @@ struct Fp8Cfg {
   static constexpr int kSmemBytes = 1024 + kStgOffset + kStgBytes;
   static constexpr int kPartPitch = BN * 4 + 16;       // bytes a row of a shared tile's part
   static constexpr int kTileM = kBM * CG;
-  static_assert(BN % 64 == 0 && BN <= 256, "a tile begins on a pair of scale columns");
+  static_assert(BN % 128 == 0 && BN <= 256, "whole scale tiles");
   static_assert(kAcc1 + BN <= kSfCol && 2 * kSfCols <= 32, "TMEM");
   static_assert(kStages >= 4 && kSmemBytes <= 232448, "shared memory");
   static_assert(kBM * kPartPitch <= kSfOffset, "the part fits the operand ring");
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG>::kThreads, 1)
     // ----------------------------------------------------------- MMA issuer
     // The whole warp runs the loop and one elected lane issues: with the loop itself on one
     // lane, the descriptors live in ordinary registers and each MMA took about 250 cycles to
-    // issue, twice its execution (8192^3: 335 us, so 292 us).
+    // issue, twice its execution (8192^3: 335 us, and 292 us like this).
     if (leader) {
       int stage = 0;
       uint32_t phase = 0, sf = 0;                      // sf: which scale buffer
@@ -264,9 +264,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG>::kThreads, 1)
           break;
         }
         tc_fence_after();
-        const Tile t = tile_at<BN, CG>(p, tile);
         const uint32_t d_tmem = tmem_base + acc * Cfg::kAcc1;
-        const uint32_t sb_at = 4 + ((t.n0 & 127) >> 5);  // the first row within its scale tile
         uint32_t sa = 0;
         for (int32_t kb = kb0; kb < kb1; ++kb) {
           if (!warp_wait(&full_bar[stage], phase, p.err, 23, p.wait_limit_ns)) {
@@ -291,7 +289,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG>::kThreads, 1)
             }
 #pragma unroll
             for (int kk = 0; kk < kKBytes / 32; ++kk)
-              tc_mma_mxf8<CG>(d_tmem, ad + 2 * kk, bd + 2 * kk, id, sa, sa + sb_at,
+              tc_mma_mxf8<CG>(d_tmem, ad + 2 * kk, bd + 2 * kk, id, sa, sa + 4,
                               kk > 0 ? 1u : (kb > kb0 ? 1u : 0u));
             if constexpr (CG == 2)
               tc_commit_pair_mc(&empty_bar[stage], static_cast<uint16_t>(3));
