@@ -358,3 +358,28 @@ def test_another_stream_and_a_replayed_graph():
         graph.replay()
         B.check(ws)
         assert torch.equal(z, step())
+
+
+def test_offsets_beyond_32_bits():
+    """An operand of 4.3e9 values: its last rows, quantised both ways and multiplied, are what
+    those rows alone give."""
+    rows, K, N = 8281 * 128 + 37, 4096, 64
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 20 GB")
+    x = torch.empty(rows, K, dtype=BF, device="cuda").normal_()
+    w, wsf = B.fp8_quantize(normal(40, N, K), block_rows=128)[0]
+    (q, sf), (qt, _) = B.fp8_quantize(x, way="both")
+    only, only_sf = B.fp8_quantize(x)[0]
+    assert torch.equal(sf, only_sf) and torch.equal(q[-1].view(torch.uint8), only[-1].view(torch.uint8))
+    del only
+    first = 8275 * 128
+    (tq, tsf), (tqt, _) = B.fp8_quantize(x[first:], way="both")
+    assert torch.equal(q[first:].view(torch.uint8), tq.view(torch.uint8))
+    assert torch.equal(sf[-tsf.numel():], tsf)
+    n = rows - first
+    assert torch.equal(qt[:, first:rows].view(torch.uint8), tqt[:, :n].view(torch.uint8))
+    out = B.fp8_matmul(q, sf, w, wsf, K, workspace(rows, N, K))
+    tail = B.fp8_matmul(tq, tsf, w, wsf, K, workspace(n, N, K))
+    # another order of the sums: a bf16 step where a value lies between two, and the fp32 sums'
+    # loss near zero (K = 4096 values of about 1: 160 additions of 2^-23 of 4096)
+    torch.testing.assert_close(out[first:], tail, rtol=torch.finfo(BF).eps, atol=160 * 2.0 ** -23 * 4096)
