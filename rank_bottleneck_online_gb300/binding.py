@@ -491,13 +491,15 @@ def _take(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
-# the current device, and its current stream, of torch's own bookkeeping
-_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else \
-    torch.cuda.current_device
+# The current device and its current stream straight from torch's bookkeeping where it offers
+# them (0.2 us a call instead of 1.5), by the public functions otherwise.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _raw_stream(stream, device):
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    return _current_raw_stream(device) if stream is None else stream.cuda_stream
 
 
 def _on(t, name, dtype, device):
