@@ -177,8 +177,8 @@ __device__ __forceinline__ bool block_tops(const uint32_t (&w)[kRows][kWords],
 
 // ------------------------------------------------------------------- rows alone
 // A warp takes rows of 512 columns: 8 lanes a block of 128, 16 values a lane, four rows in
-// flight. A block of 8 warps covers 32 rows. grid = (scale tiles along the columns,
-// 4 x row tiles of 128, matrices).
+// flight. A block of 8 warps covers 32 rows. grid = (scale tiles along the columns, lines of
+// 32 rows, matrices); the last line's block also fills the scale tile's lines behind it.
 template <int FMT>
 __global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const QuantParams p) {
   pdl_enter();
@@ -219,6 +219,12 @@ __global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const QuantPara
     word |= __shfl_xor_sync(0xffffffffu, word, 16);
     // (four rows of one quarter of a scale tile lie 16 bytes apart)
     if (lane == 0) *reinterpret_cast<uint32_t*>(sf + 16 * r) = word;
+  }
+  if (blockIdx.y + 1 == gridDim.y) {
+    const int64_t row = static_cast<int64_t>(gridDim.y) * 32 + threadIdx.x;
+    if (row < (p.rows + 127) / 128 * 128)
+      *reinterpret_cast<uint32_t*>(p.sf + blockIdx.z * p.plane + scale_at(row, first, p.kt)) =
+          0x7f7f7f7fu;
   }
 }
 
@@ -410,15 +416,15 @@ cudaError_t launch_fp8_quantize(const boost_fp8_quant_desc& d, const void* x, co
   p.plane_t = scale_plane(d.cols, d.rows);
   const unsigned G = static_cast<unsigned>(d.G);
   const bool e4m3 = d.fmt == BOOST_E4M3;
-  const unsigned row_tiles = static_cast<unsigned>((d.rows + 127) / 128);
   // Rows alone take the kernel without barriers: 16384 x 4096 in 33 us, 6.1 TB/s, against 35 for
   // the rows of square blocks and 37 for the columns alone, both of the tile kernel.
   if (d.block_rows == 1 && qt == nullptr) {
-    const dim3 grid(static_cast<unsigned>(p.kt), row_tiles * 4, G);
+    const dim3 grid(static_cast<unsigned>(p.kt), static_cast<unsigned>((d.rows + 31) / 32), G);
     return launch_grid(e4m3 ? quant_rows_kernel<BOOST_E4M3> : quant_rows_kernel<BOOST_E5M2>, grid,
                        stream, p);
   }
-  const dim3 grid(static_cast<unsigned>((d.cols + 127) / 128), row_tiles, G);
+  const dim3 grid(static_cast<unsigned>((d.cols + 127) / 128),
+                  static_cast<unsigned>((d.rows + 127) / 128), G);
   if (d.block_rows == 128)
     return launch_grid(e4m3 ? quant_tile_kernel<BOOST_E4M3, true>
                             : quant_tile_kernel<BOOST_E5M2, true>, grid, stream, p);
