@@ -10,6 +10,8 @@ in the library's CUDA kernels; Python only sequences the calls.
 
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import binding as B
@@ -117,17 +119,20 @@ class Rotary:
         self.inv_freq = inv_freq.to(device=device, dtype=torch.float64).contiguous()
 
     def __call__(self, q, k, positions, *, inverse=False, q_out=None, k_out=None, stream=None):
-        """Turn q and k [T, heads * dim] (back, for gradients, when ``inverse``)."""
+        """Turn q and k [T, heads * dim] or [T, heads, dim] (back, for gradients, when
+        ``inverse``): returns (q_out, k_out), new tensors where none are given; k may be None."""
         if positions is None:
             raise ValueError("rotary positions need the tokens' positions")
 
         def split(t):
-            return None if t is None else t.view(t.shape[0], -1, self.dim)
+            return None if t is None else t.view(
+                t.shape[0], math.prod(t.shape[1:]) // self.dim, self.dim)
 
-        B.rope(split(q), split(k), positions, self.inv_freq, sections=self.sections,
-               interleaved=self.interleaved, inverse=inverse, q_out=split(q_out),
-               k_out=split(k_out), stream=stream)
-        return q_out, k_out
+        turned = B.rope(split(q), split(k), positions, self.inv_freq, sections=self.sections,
+                        interleaved=self.interleaved, inverse=inverse, q_out=split(q_out),
+                        k_out=split(k_out), stream=stream)
+        return tuple(t.view(x.shape) if given is None and x is not None else given
+                     for x, given, t in zip((q, k), (q_out, k_out), turned))
 
 
 class MLP:
