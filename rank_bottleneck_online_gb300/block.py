@@ -231,8 +231,9 @@ class Layer:
     rotary (a ``Rotary``): q and k are turned in place in the QKV block's output, and the
     attention core's gradients of the turned q and k back on their way into the QKV block's
     upstream gradient. dropout (p > 0): x1 = x + dropout(O(v)), out = x1 + dropout(MLP(x1)),
-    with the masks of (``seed``, ``mask`` of the call) and none stored. fp8: the blocks'
-    forward in 8 bits (``Fp8Block``)."""
+    with the masks of (``seed``, ``mask`` of the call) and none stored. Give the layers of a
+    model different seeds, any ones: branches share a mask only where seed, mask and branch are
+    the same. fp8: the blocks' forward in 8 bits (``Fp8Block``)."""
 
     def __init__(self, T, d, r, ffn, *, S=1, eps=1e-5, act="silu", weights=None, device="cuda",
                  rotary=None, dropout=0.0, seed=0, fp8=False):
@@ -278,21 +279,30 @@ class Layer:
         """Gradient at x: dx1 + the QKV block's input gradient (its dx buffer)."""
         return self.qkv.dx
 
+    def _words(self, which, mask):
+        """The generator's seed and offset of branch ``which``: seed + which, so layers with
+        neighbouring seeds meet in one of them, and odd and even seeds therefore have offsets
+        of their own, below and from 2^63."""
+        if not 0 <= mask < 1 << 63:
+            raise ValueError("mask must be an unsigned 63-bit value")
+        return (self.seed + which) % (1 << 64), mask + ((self.seed + 1) % 2 << 63)
+
     def _join(self, branch, residual, which, mask, counter, stream):
         """residual + dropout(branch), in the branch's buffer."""
-        return B.dropout_add(branch, self.dropout, (self.seed + which) % (1 << 64), mask,
-                             residual=residual, out=branch, counter=counter, stream=stream)
+        return B.dropout_add(branch, self.dropout, *self._words(which, mask), residual=residual,
+                             out=branch, counter=counter, stream=stream)
 
     def _split(self, grad, which, mask, counter, stream):
         """Gradient of the branch whose dropout joined it to the residual."""
         if not self.dropout:
             return grad
-        return B.dropout_bwd(grad, self.dropout, (self.seed + which) % (1 << 64), mask,
-                             dx=self.dbranch, counter=counter, stream=stream)
+        return B.dropout_bwd(grad, self.dropout, *self._words(which, mask), dx=self.dbranch,
+                             counter=counter, stream=stream)
 
     def forward(self, x, stream=None, positions=None, mask=0, counter=None):
         """positions ([T] or [axes, T]): those of the tokens, with ``rotary``. mask: which
-        dropout masks (plus ``counter``, a device value, as in ``binding.dropout_add``)."""
+        dropout masks (plus ``counter``, a device value, as in ``binding.dropout_add``), below
+        2^63 together."""
         qkv = self.qkv.forward(x, stream)
         if self.rotary is not None:
             self.rotary(qkv[0], qkv[1], positions, q_out=qkv[0], k_out=qkv[1], stream=stream)
