@@ -24,7 +24,7 @@ extern "C" {
  *     (u, v) -> (u cos phi - v sin phi, v cos phi + u sin phi)
  * in fp32, rounded once to bf16. The angle is reduced to a fraction of a turn in 64-bit
  * fixed point, so it is as exact at position 2^31 as at position 1 (a position p loses
- * 2^-63 |p| turns, which begins to show behind 2^37). The inverse is the transpose of the
+ * less than 2^-63 |p| turns at any frequency, which begins to show behind 2^37). The inverse is the transpose of the
  * rotation: it takes the gradients of the rotated q and k to those of q and k. Several
  * axes (time, height, width) turn different pairs of the same head.
  *
@@ -55,7 +55,8 @@ typedef struct {
 /*
  *   q, k        inputs (strides in the desc)
  *   positions   [axes, T] int32 or int64
- *   inv_freq    [rot / 2] fp64, radians per position (a non-finite value gives NaN)
+ *   inv_freq    [rot / 2] fp64, radians per position (one that is not finite, or is 2^64 or
+ *               more in magnitude, gives NaN)
  *   q_out, k_out  out; an output may be its own input with the same strides (in place),
  *               and slices of one packed buffer [T, heads, dim] may be given side by
  *               side. Any other overlap of an output with a tensor of the call is

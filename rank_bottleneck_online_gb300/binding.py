@@ -562,7 +562,7 @@ def rope(q, k, positions, inv_freq, *, sections=None, pair_axis=None, interleave
     (q_out, k_out). ``inverse`` takes the gradients of the rotated q and k back.
 
     positions: [T] or [axes, T], int32 or int64. inv_freq: float64 [rot / 2], radians per
-    position; the first rot values of each head turn. ``sections``: how many pairs turn with
+    position, below 2^64 in magnitude; the first rot values of each head turn. ``sections``: how many pairs turn with
     each axis, in order (default: all with the first); ``pair_axis``: the axis of each pair
     instead. q, k and the outputs take any token and head strides (multiples of 8), so slices
     of a packed projection and [heads, T, dim] tensors seen as [T, heads, dim] are fine, and

@@ -9,8 +9,10 @@
 // The angle: phi = p w with p a 64-bit integer and w an fp64 frequency. In turns,
 // p w / (2 pi) mod 1 is wanted. F = floor(2^64 w / (2 pi)) mod 2^64 holds the frequency as a
 // 64-bit fixed-point fraction of a turn, and p F mod 2^64, the integer product's own wrap,
-// is the fraction of a turn to 2^-63 |p|, whatever the size of p. Its upper 32 bits go to
-// sincospif. No fp64 arithmetic is used (its rate is a 60th of fp32's here).
+// is the fraction of a turn to 2^-63 |p|, whatever the size of p: F loses its floor, and
+// |w| 2^-64 for the 128 bits that 1 / (2 pi) is held to, so frequencies are taken below 2^64.
+// Its upper 32 bits go to sincospif. No fp64 arithmetic is used (its rate is a 60th of fp32's
+// here).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -38,19 +40,30 @@ struct RopeParams {
   int head_step, tok_step;         // heads and tokens that a block turns at a time
 };
 
-// 2^64 w / (2 pi) mod 2^64, from the bits of w (finite).
+// Exponent field of a frequency; from kNoAngle on (2^64, infinities and NaN) there is no angle.
+constexpr int kNoAngle = 1023 + 64;
+__device__ __forceinline__ int exponent_field(double w) {
+  return static_cast<int>((__double_as_longlong(w) >> 52) & 0x7ff);
+}
+
+// 2^64 w / (2 pi) mod 2^64, from the bits of w (0 where it has no angle).
 __device__ __forceinline__ uint64_t turns_fixed(double w) {
-  constexpr uint64_t kInvTwoPi = 0x28be60db9391054aull;   // 2^64 / (2 pi)
+  // 2^128 / (2 pi), upper and lower word
+  constexpr uint64_t kHigh = 0x28be60db9391054aull, kLow = 0x7f09d5f47d4d3770ull;
   const uint64_t b = __double_as_longlong(w);
-  const int e = static_cast<int>((b >> 52) & 0x7ff);
-  if (e == 0) return 0;            // zero and subnormals: no angle for any 64-bit position
+  const int e = exponent_field(w);
+  // (zero and subnormals turn by nothing at any 64-bit position)
+  if (e == 0 || e >= kNoAngle) return 0;
   const uint64_t m = (b & 0xfffffffffffffull) | (1ull << 52);
-  const uint64_t hi = __umul64hi(m, kInvTwoPi), lo = m * kInvTwoPi;
-  const int sh = 52 - (e - 1023);  // w = m 2^-sh
+  // m 2^128 / (2 pi) in three words, upper one first
+  const uint64_t low = m * kHigh, w1 = low + __umul64hi(m, kLow), w0 = m * kLow;
+  const uint64_t w2 = __umul64hi(m, kHigh) + (w1 < low ? 1 : 0);
+  const int sh = 52 - (e - 1023);  // w = m 2^-sh, so the words go down by 64 + sh bits
   uint64_t f;
-  if (sh <= 0) f = sh > -64 ? lo << -sh : 0;
-  else if (sh < 64) f = (hi << (64 - sh)) | (lo >> sh);
-  else f = sh < 128 ? hi >> (sh - 64) : 0;
+  if (sh < 0) f = (w1 << -sh) | (w0 >> (64 + sh));
+  else if (sh == 0) f = w1;
+  else if (sh < 64) f = (w2 << (64 - sh)) | (w1 >> sh);
+  else f = sh < 128 ? w2 >> (sh - 64) : 0;
   return (b >> 63) ? 0 - f : f;
 }
 
@@ -175,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     // half turns in [-1, 1): the phase's upper 32 bits as a signed fraction
     float s, c;
     sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &s, &c);
-    if (!isfinite(w)) s = c = nanf("");
+    if (exponent_field(w) >= kNoAngle) s = c = nanf("");
     cs[a] = c;
     sn[a] = p.d.inverse ? -s : s;
   }
