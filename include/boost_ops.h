@@ -58,9 +58,10 @@ typedef struct {
  *   inv_freq    [rot / 2] fp64, radians per position (one that is not finite, or is 2^64 or
  *               more in magnitude, gives NaN)
  *   q_out, k_out  out; an output may be its own input with the same strides (in place),
- *               and slices of one packed buffer [T, heads, dim] may be given side by
- *               side. Any other overlap of an output with a tensor of the call is
- *               BOOST_ERR_INVALID_ARG.
+ *               and operands may lie in one packed buffer: heads side by side in a token's
+ *               row ([T, heads, dim]), or with the same strides and no element in common
+ *               ([T, heads, 3, dim], [heads, 3, T, dim] and the like). Any other overlap of
+ *               an output with a tensor of the call is BOOST_ERR_INVALID_ARG.
  */
 boost_status boost_rope(const boost_rope_desc* desc, const void* q, const void* k,
                         const void* positions, const double* inv_freq, void* q_out, void* k_out,
