@@ -38,6 +38,9 @@ extern "C" {
  *   pos64    0: positions are int32, 1: int64 (any sign)
  *   q_ts, q_hs, ...  token and head strides in elements, multiples of 8, >= 0. In an
  *            output no two elements may coincide.
+ *   pos_at   where in `positions` the tokens begin, >= 0 (a decoding step takes one column
+ *            of a table, whose address is aligned although the column's is not)
+ *   pos_as   positions from one axis to the next, >= T; 0: T
  *   axis     [rot / 2] the axis of each pair, each < axes (the rest of the array unused)
  */
 #define BOOST_ROPE_MAX_DIM 512
@@ -49,12 +52,14 @@ typedef struct {
     int32_t axes, interleaved, inverse, pos64;
     int64_t q_ts, q_hs, k_ts, k_hs;
     int64_t qo_ts, qo_hs, ko_ts, ko_hs;
+    int64_t pos_at, pos_as;
     uint8_t axis[BOOST_ROPE_MAX_DIM / 2];
 } boost_rope_desc;
 
 /*
  *   q, k        inputs (strides in the desc)
- *   positions   [axes, T] int32 or int64
+ *   positions   int32 or int64, that of token t on axis a at pos_at + a pos_as + t: [axes, T]
+ *               with both 0
  *   inv_freq    [rot / 2] fp64, radians per position (one that is not finite, or is 2^64 or
  *               more in magnitude, gives NaN)
  *   q_out, k_out  out; an output may be its own input with the same strides (in place),

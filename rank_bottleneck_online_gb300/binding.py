@@ -65,7 +65,7 @@ class RopeDesc(ctypes.Structure):
         [(f, ctypes.c_int32) for f in ("hq", "hk", "dim", "rot", "axes", "interleaved", "inverse",
                                        "pos64")] + \
         [(f, ctypes.c_int64) for f in ("q_ts", "q_hs", "k_ts", "k_hs", "qo_ts", "qo_hs", "ko_ts",
-                                       "ko_hs")] + \
+                                       "ko_hs", "pos_at", "pos_as")] + \
         [("axis", ctypes.c_uint8 * (ROPE_MAX_DIM // 2))]
 
 
@@ -522,7 +522,7 @@ def _head_strides(shape, stride, name, T, dim):
 
 
 @functools.lru_cache(maxsize=512)
-def _rope_plan(q, k, q_out, k_out, positions, pos64, freq, interleaved, inverse, sections,
+def _rope_plan(q, k, q_out, k_out, positions, pos64, pos_at, freq, interleaved, inverse, sections,
                pair_axis):
     """The descriptor of a call whose tensors have these (shape, stride) pairs."""
     T, hq, dim = q[0] if len(q[0]) == 3 else (None, None, None)
@@ -534,15 +534,21 @@ def _rope_plan(q, k, q_out, k_out, positions, pos64, freq, interleaved, inverse,
     strides.append(_head_strides(*k_out, "k_out", T, dim) if k_out else (0, 0))
     if q_out[0] != q[0] or (k and k_out[0] != k[0]):
         raise ValueError("an output has another shape than its input")
-    if len(positions) not in (1, 2) or positions[-1] != T:
-        raise ValueError(f"positions has shape {tuple(positions)}, expected [T] or [axes, T]")
+    shape, step = positions
+    if len(shape) not in (1, 2) or shape[-1] != T:
+        raise ValueError(f"positions has shape {tuple(shape)}, expected [T] or [axes, T]")
+    axes = 1 if len(shape) == 1 else shape[0]
+    # the stride of a single token or axis says nothing: a plain one in its place
+    pos_as = step[0] if axes > 1 else T
+    if (T > 1 and step[-1] != 1) or pos_as < T:
+        raise ValueError("positions must be contiguous, or columns of a contiguous table")
     if len(freq) != 1:
         raise ValueError("inv_freq must be a vector")
-    axes, pairs = (1 if len(positions) == 1 else positions[0]), freq[0]
+    pairs = freq[0]
     if 2 * pairs > ROPE_MAX_DIM:
         raise BoostError(2, "boost_rope")
     D = RopeDesc(T, hq, k[0][1] if k else 0, dim, 2 * pairs, axes, interleaved, inverse, pos64,
-                 *(v for pair in strides for v in pair))
+                 *(v for pair in strides for v in pair), pos_at, pos_as)
     if pair_axis is not None:
         if sections is not None:
             raise ValueError("sections and pair_axis exclude each other")
@@ -566,7 +572,8 @@ def rope(q, k, positions, inv_freq, *, sections=None, pair_axis=None, interleave
     each axis, in order (default: all with the first); ``pair_axis``: the axis of each pair
     instead. q, k and the outputs take any token and head strides (multiples of 8), so slices
     of a packed projection and [heads, T, dim] tensors seen as [T, heads, dim] are fine, and
-    q_out may be q (in place). Positions and frequencies are contiguous."""
+    q_out may be q (in place). positions may be a slice of a vector or columns of a table
+    [axes, any]; frequencies are contiguous."""
     bf, device = torch.bfloat16, _device()
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=bf, device=q.device)
@@ -581,13 +588,19 @@ def rope(q, k, positions, inv_freq, *, sections=None, pair_axis=None, interleave
     pos64 = positions.dtype is torch.int64
     if not pos64 and positions.dtype is not torch.int32:
         raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
+    # the call takes an aligned address and where the positions begin behind it
+    pp = _on(positions, "positions", positions.dtype, device)
+    behind = pp & 15
+    if behind & (7 if pos64 else 3):
+        raise BoostError(3, "boost_rope")
     D = _rope_plan((q.shape, q.stride()), ks, (q_out.shape, q_out.stride()), kos,
-                   positions.shape, pos64, inv_freq.shape, bool(interleaved), bool(inverse),
+                   (positions.shape, positions.stride()), pos64, behind >> (3 if pos64 else 2),
+                   inv_freq.shape, bool(interleaved), bool(inverse),
                    None if sections is None else tuple(sections),
                    None if pair_axis is None else tuple(pair_axis))
     _check(lib().boost_rope(
         D, _on(q, "q", bf, device), kp,
-        _take(positions, "positions", positions.dtype, positions.shape, device),
+        pp - behind,
         _take(inv_freq, "inv_freq", torch.float64, inv_freq.shape, device),
         _on(q_out, "q_out", bf, device), kop, _raw_stream(stream, device)), "boost_rope")
     return q_out, k_out

@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 
   for (int a = threadIdx.x; a < tokens * pairs; a += kThreads) {
     const int ta = a / pairs, i = a - ta * pairs;
-    const int64_t at = p.d.axis[i] * p.d.T + t0 + ta;
+    const int64_t at = p.d.pos_at + p.d.axis[i] * p.d.pos_as + t0 + ta;
     const int64_t pos = p.d.pos64 ? static_cast<const int64_t*>(p.positions)[at]
                                   : static_cast<const int32_t*>(p.positions)[at];
     const double w = p.inv_freq[i];
@@ -343,6 +343,9 @@ extern "C" boost_status boost_rope(const boost_rope_desc* desc, const void* q, c
     const double n = i % 2 == 0 ? static_cast<double>(D.T) : (i & 2) ? D.hk : D.hq;
     if (n * static_cast<double>(strides[i]) > 0x1p50) return BOOST_ERR_UNSUPPORTED_SHAPE;
   }
+  if (D.pos_at < 0 || D.pos_as < 0 || (D.pos_as > 0 && D.pos_as < D.T)) return BOOST_ERR_INVALID_ARG;
+  if (D.pos_at > (int64_t{1} << 50) || D.pos_as > (int64_t{1} << 50))
+    return BOOST_ERR_UNSUPPORTED_SHAPE;
   if (D.hk == 0 && (k != nullptr || k_out != nullptr)) return BOOST_ERR_INVALID_ARG;
   if (D.T == 0) return BOOST_OK;
   if (q == nullptr || positions == nullptr || inv_freq == nullptr || q_out == nullptr)
@@ -361,12 +364,15 @@ extern "C" boost_status boost_rope(const boost_rope_desc* desc, const void* q, c
       !disjoint(sq, ko) || !disjoint(sk, qo) || !disjoint(qo, ko))
     return BOOST_ERR_INVALID_ARG;
   // positions and frequencies are read while the outputs are written: nothing shared there
-  const uint64_t pos_bytes = (D.pos64 ? 8ull : 4ull) * D.axes * D.T, freq_bytes = 4ull * D.rot;
+  const uint64_t pos_size = D.pos64 ? 8 : 4, freq_bytes = 4ull * D.rot;
+  const int64_t pos_as = D.pos_as > 0 ? D.pos_as : D.T;
+  const uint64_t pos_bytes = pos_size * ((D.axes - 1) * pos_as + D.T);
+  const void* first_pos = static_cast<const char*>(positions) + pos_size * D.pos_at;
   auto meets = [](const Slice& o, const void* in, uint64_t bytes) {
     const uintptr_t b = reinterpret_cast<uintptr_t>(in);
     return o.extent() > 0 && b < o.base + o.extent() && o.base < b + bytes;
   };
-  if (meets(qo, positions, pos_bytes) || meets(ko, positions, pos_bytes) ||
+  if (meets(qo, first_pos, pos_bytes) || meets(ko, first_pos, pos_bytes) ||
       meets(qo, inv_freq, freq_bytes) || meets(ko, inv_freq, freq_bytes))
     return BOOST_ERR_INVALID_ARG;
 
@@ -378,8 +384,9 @@ extern "C" boost_status boost_rope(const boost_rope_desc* desc, const void* q, c
   p.positions = positions;
   p.inv_freq = inv_freq;
   p.d = D;
+  p.d.pos_as = pos_as;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const double values = static_cast<double>(D.T) * (D.hq + D.hk) * D.dim;
-  ProfScope ps(s, K_ROPE, 0.0, 4.0 * values + static_cast<double>(pos_bytes));
+  ProfScope ps(s, K_ROPE, 0.0, 4.0 * values + static_cast<double>(pos_size * D.axes * D.T));
   return launch_rope(p, s) == cudaSuccess ? BOOST_OK : BOOST_ERR_CUDA;
 }
