@@ -77,10 +77,16 @@ class Fp8Block(Block):
         self.x8, self.a8 = operand((), T, d), operand((k,), T, r)
         self.a = torch.empty(T, k * r, dtype=bf, device=dev)
         self.ssq = torch.empty(D.S, T, dtype=torch.float32, device=dev) if D.has_norm else None
-        self.ws8 = B.Workspace(max(B.fp8_matmul_workspace_bytes(T, k * r, d),
-                                   B.fp8_matmul_workspace_bytes(T, n, r, k)), dev)
+        self.ws.ensure(max(B.fp8_matmul_workspace_bytes(T, k * r, d),
+                           B.fp8_matmul_workspace_bytes(T, n, r, k)))
         self.act = "silu" if D.act else "identity"
         self.quantize_weights()
+
+    @property
+    def ws8(self):
+        """The products' workspace: the block's own, so that one check of it sees their errors
+        too."""
+        return self.ws
 
     def quantize_weights(self, stream=None):
         """Take the 8-bit weights from A, B and gamma again (after an update of them)."""
