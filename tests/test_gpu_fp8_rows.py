@@ -22,21 +22,22 @@ def _lib():
     B.lib()
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("rows", [MOST - 96, MOST - 95, MOST - 32, MOST - 31, MOST])
-def test_rows_alone_to_the_limit(rows):
+def test_rows_alone_to_the_limit(rows, fmt):
     """What the tile kernel gives, which holds 128 rows a block: values, scales and the bytes of
     the last tile's missing rows; and the definition over the last rows."""
     g = torch.Generator(device="cuda").manual_seed(rows)
     x = torch.randn(rows, 8, generator=g, device="cuda").to(BF)
-    q, whole_q = guarded((rows, 16), torch.float8_e4m3fn)
+    q, whole_q = guarded((rows, 16), B.FP8_FORMATS[fmt][1])
     sf, whole_s = guarded((B.fp8_scale_bytes(rows, 8),), torch.uint8)
-    B.fp8_quantize(x, rows_out=(q, sf))
+    B.fp8_quantize(x, fmt=fmt, rows_out=(q, sf))
     assert whole_q() and whole_s()
-    (want_q, want_sf), _ = B.fp8_quantize(x, way="both")
+    (want_q, want_sf), _ = B.fp8_quantize(x, fmt=fmt, way="both")
     assert torch.equal(q.view(torch.uint8), want_q.view(torch.uint8)) and torch.equal(sf, want_sf)
     first = MOST - 96                                   # the last tile's first row
     tail = x[first - 128:]
-    values, e = ops.fp8_quantize(f64(tail), "e4m3")
+    values, e = ops.fp8_quantize(f64(tail), fmt)
     assert (f64(q[first - 128:])[:, :8] == values).all()
     assert (sf[-1024:].cpu().numpy() == ops.fp8_scales(e)).all() if rows > first else True
 
