@@ -22,7 +22,7 @@
 // and shares 32 columns with the first; the epilogue reads those first and lets the next
 // tile's MMAs start, so the two tiles still overlap but for that read.
 //
-// Measured (alone; back to back the power cap takes 10-15%): 8192^3 292 us, 3.76 PFLOP/s, twice
+// Measured (alone; back to back the power cap takes 13-18%): 8192^3 292 us, 3.76 PFLOP/s, twice
 // the measured bf16 burst; 16384 x 2048 x 4096 81 us, 3.40 PFLOP/s, the tensor pipe busy 75% of
 // the time (waves 6.7 of 7, the first loads, the last epilogue); 2 x 16384 x 11008 x 1024
 // 233 us, 3.17 PFLOP/s, where 721 MB of stores share L2 with the operand loads. Clusters of two
@@ -250,8 +250,8 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, CG>::kThreads, 1)
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
     // The whole warp runs the loop and one elected lane issues: with the loop itself on one
-    // lane, the descriptors live in ordinary registers and each MMA took about 250 cycles to
-    // issue, twice its execution (8192^3: 335 us, and 292 us like this).
+    // lane, the descriptors live in ordinary registers and the issue of an MMA takes longer than
+    // its 128 cycles (8192^3: 335 us, about 185 cycles an MMA, and 292 us like this).
     if (leader) {
       int stage = 0;
       uint32_t phase = 0, sf = 0;                      // sf: which scale buffer

@@ -6,8 +6,9 @@
 // so byte = E - 8 (or 15) + (1.f > 1.75), read from m's bits: no logarithm, no rounding.
 // x 2^(127 - byte) is exact in fp32, and one conversion rounds it.
 //
-// Both kernels are bound by HBM (2 bytes read and 129/128 written a value and layout) and
-// keep every value in registers between its one reading and its writing.
+// Both kernels keep every value in registers between its one reading and its writing, so they
+// move what they must: 2 bytes read and 129/128 written a value and layout. Rows alone run near
+// the copy rate; what holds the tiles back stands beside their kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -231,12 +232,13 @@ __global__ void __launch_bounds__(kThreads, 4) quant_rows_kernel(const QuantPara
 // A block holds one tile in registers: thread (rg, cg), rg = threadIdx.x / 16, has rows
 // 8 rg .. 8 rg + 7 of columns 8 cg .. 8 cg + 7, so that 16 lanes read a row's 256 bytes. The
 // transposed bytes go through shared memory: column c's 128 bytes lie at 128 c, the 8 bytes
-// of row group rg in slot rg ^ (c / 8), which keeps both sides free of bank conflicts. The
-// pass is close to the issue rate, so every address is a base and a small stride, and tiles
-// that lie inside x and are finite, by far the most, skip the checks of both. (A persistent
-// form with the next tile on its way by cp.async was slower, 67 us against 57 before that
-// last step: its shared memory leaves three blocks an SM, not four.) 16384 x 4096 both ways: 48 us,
-// 5.6 TB/s, 83% of the measured copy rate.
+// of row group rg in slot rg ^ (c / 8), which keeps both sides free of bank conflicts. Every
+// address is a base and a small stride, and tiles that lie inside x and are finite, by far the
+// most, skip the checks of both: at 28 instructions a value the pass was bound by them, at 15.5
+// (both ways) they take 55% of the issue slots. (A persistent form with the next tile on its way
+// by cp.async was slower, 67 us against 57 before that last step: its shared memory leaves three
+// blocks an SM, not four.) 16384 x 4096 both ways: 48 us, 5.6 TB/s, 83% of the measured copy rate;
+// what is left is the latency of a tile's three barriers at four blocks an SM.
 // grid = (column tiles, row tiles, matrices).
 
 // Thread c < 64 stores the scales of the tile's columns 2 c and 2 c + 1, whose largest finite
