@@ -1,7 +1,8 @@
 /*
  * boost_ops.h -- C ABI of the layer's operators around the bottleneck block
- * (boost_block.h): rotary positions of q and k, dropout of a residual branch, and the
- * 8-bit floating-point quantiser and matrix product.
+ * (boost_block.h): rotary positions of q and k, dropout of a residual branch, the 8-bit
+ * floating-point quantiser and matrix product, attention and its gradients, the norm with an
+ * 8-bit output, and gradient clipping.
  *
  * The conventions of boost_block.h hold here too: row-major tensors (bf16 unless
  * stated) of the current device, 16-byte aligned pointers, caller-owned buffers,
@@ -170,6 +171,119 @@ size_t boost_fp8_matmul_workspace_bytes(const boost_fp8_matmul_desc* desc);
 boost_status boost_fp8_matmul(const boost_fp8_matmul_desc* desc, const void* a, const void* a_sf,
                               const void* b, const void* b_sf, const float* row_scale, void* out,
                               void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------- attention
+ *
+ * The layer's attention core over packed sequences:
+ *     s_ij = scale q_i . k_j     for the keys j that query i sees
+ *     out_i = sum_j exp(s_ij - lse_i) v_j,     lse_i = ln sum_j exp(s_ij)
+ * Sequence s has the queries [q_starts[s], q_starts[s + 1]) and the keys [k_starts[s],
+ * k_starts[s + 1]); with `causal` its last query sees all its keys, the one before all but the
+ * last, and so on, so that new tokens can follow a context, and queries beyond the number of
+ * keys, the first ones, see none: their out and gradients are 0, their lse is -infinity. Query
+ * head h reads key head h / (hq / hk). Products of bf16 values, sums and the softmax's
+ * statistics in fp32; the probabilities and their gradients are rounded to bf16 as the operands
+ * of the second products.
+ *
+ *   Tq, Tk    rows of q and of k and v, >= 0
+ *   hq, hk    query and key heads, hq a multiple of hk
+ *   dim       values per head, a multiple of 8, <= 128
+ *   sequences >= 1
+ *   causal    0 or 1
+ *   scale     > 0, finite
+ *   q_ts, q_hs, ...  token and head strides in elements, multiples of 8, positive where there is
+ *             more than one token or head. In an output no two elements may coincide.
+ * The strides of dout, dq, dk and dv are the backward's alone.
+ */
+#define BOOST_ATTENTION_MAX_DIM 128
+
+typedef struct {
+    int64_t Tq, Tk;
+    int32_t hq, hk, dim, sequences, causal;
+    float scale;
+    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;
+    int64_t do_ts, do_hs, dq_ts, dq_hs, dk_ts, dk_hs, dv_ts, dv_hs;
+} boost_attention_desc;
+
+/* Bytes of the workspace of either call (0 for a desc that the calls refuse). */
+size_t boost_attention_workspace_bytes(const boost_attention_desc* desc);
+
+/*
+ *   q, k, v    [T, heads, dim] (strides in the desc)
+ *   q_starts, k_starts   device int32 [sequences + 1], ascending, from 0 to at most Tq (Tk).
+ *              Either may be NULL with one sequence: then it holds all rows. Rows behind the last
+ *              sequence are not read as its keys, and left as they were in the outputs. (Values
+ *              outside of 0..T are taken as its bounds; what sequences that overlap give is not
+ *              defined.)
+ *   out        out; shares no element with an input, but may lie between their heads in one
+ *              packed buffer
+ *   lse        out, [hq, Tq] fp32, or NULL
+ *   ws         workspace, 256-byte aligned, error word cleared by boost_block_ws_init. Calls that
+ *              may run at the same time need one each.
+ * A NaN or an infinity in k or v may reach every row of its own sequence, and no other's.
+ */
+boost_status boost_attention(const boost_attention_desc* desc, const void* q, const void* k,
+                             const void* v, const int32_t* q_starts, const int32_t* k_starts,
+                             void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of q, k and v from dout, the gradient of out; out and lse are the forward's. The
+ * probabilities are regenerated from q, k and lse. Sums over the query heads that share a key
+ * head are in fp32 too, and every sum is taken in a fixed order: two calls give the same bits.
+ */
+boost_status boost_attention_bwd(const boost_attention_desc* desc, const void* q, const void* k,
+                                 const void* v, const void* out, const float* lse,
+                                 const void* dout, const int32_t* q_starts,
+                                 const int32_t* k_starts, void* dq, void* dk, void* dv, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/* ----------------------------------------------- norm with an 8-bit output
+ *
+ * The residual's addition and the statistics of the root-mean-square norm behind it, with the
+ * sum quantised for the 8-bit product that follows:
+ *     h = x + residual (bf16)          rstd[t] = (mean_j h[t][j]^2 + eps)^-1/2
+ *     q, sf = 8-bit operand of h, or of bf16(gamma[j] h[t][j]), rows alone (block_rows 1)
+ * as boost_fp8_quantize gives it. The norm's value is q's times rstd of its row, which the product
+ * applies (row_scale). Its gradient is the normed block's (boost_block_bwd).
+ *   T, d       d a multiple of 8
+ *   fmt        boost_fp8
+ *   residual   [T, d] or NULL
+ *   gamma      [d] or NULL
+ *   h          out, [T, d], or NULL; may be x or residual
+ *   rstd       out, [T] fp32
+ *   q, sf      out, [T, d rounded up to 16] with zeros behind the columns, and its scales
+ */
+boost_status boost_norm_quantize(int64_t T, int64_t d, int32_t fmt, float eps, const void* x,
+                                 const void* residual, const void* gamma, void* h, float* rstd,
+                                 void* q, void* sf, void* stream);
+
+/* --------------------------------------------------------- gradient clipping
+ *
+ *     norm = sqrt(sum over all tensors of g^2),     out = g min(1, max_norm / (norm + 1e-6))
+ * Squares in fp32, their sums in fp64 in a fixed order: two calls give the same bits. A norm
+ * that is not finite gives what the formula gives (NaN where it is NaN; 0, or NaN from an
+ * infinity, where it is infinite).
+ *   count      tensors, >= 0
+ *   g          16-byte aligned
+ *   out        may be g (then nothing is written where nothing is to be scaled); NULL: the tensor
+ *              only counts in the norm. Otherwise it shares no byte with any tensor of the call.
+ *   n          elements, >= 0
+ *   wide       0: bf16, 1: fp32
+ *   max_norm   >= 0; infinity: no scaling
+ *   norm       out, fp32 [1]
+ *   ws         workspace of boost_grad_clip_workspace_bytes() bytes, 256-byte aligned
+ */
+typedef struct {
+    const void* g;
+    void* out;
+    int64_t n;
+    int32_t wide;
+} boost_grad;
+
+size_t boost_grad_clip_workspace_bytes(void);
+
+boost_status boost_grad_clip(int64_t count, const boost_grad* grads, double max_norm, float* norm,
+                             void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

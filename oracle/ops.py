@@ -1,7 +1,8 @@
 """fp64 definitions of the layer's operators around the bottleneck block: rotary
 positions, the counter-based dropout mask, 8-bit floating point with a power-of-two scale
-for each block of 128, and the product of such operands. NumPy on the CPU, written from
-the formulas; nothing here is shared with the CUDA path.
+for each block of 128, and the product of such operands; attention over packed sequences
+and its gradients, the norm behind a residual, and gradient clipping. NumPy on the CPU,
+written from the formulas; nothing here is shared with the CUDA path.
 """
 
 from __future__ import annotations
@@ -165,3 +166,68 @@ def fp8_matmul(a, b, row_scale=None, act="identity"):
     if row_scale is not None:
         z, size = z * row_scale[:, None], size * np.abs(row_scale)[:, None]
     return (silu(z) if act == "silu" else z), size
+
+
+# ----------------------------------------------------------------------- attention
+def attention(q, k, v, lengths, causal=True, scale=None, dout=None):
+    """q [Tq, hq, dim], k and v [Tk, hk, dim]; lengths: (queries, keys) of each sequence. A dict
+    of out, lse [hq, Tq] and, with dout, dq, dk, dv; rows of no sequence are NaN. Also the sums of
+    magnitudes that a relative rounding of the probabilities P, of their gradients dS and of out
+    scales with: out_size = sum P |v|, dv_size = sum P |dout|, dq_size and dk_size = sum E |k|,
+    sum E |q| with E = |dS| + scale P sum |dout| (|out| + out_size), the last for what a rounded
+    out makes of dS = scale P (dP - sum dout out)."""
+    group = q.shape[1] // k.shape[1]
+    scale = q.shape[2] ** -0.5 if scale is None else scale
+    like = {"out": q, "out_size": q}
+    if dout is not None:
+        like |= {"dq": q, "dq_size": q, "dk": k, "dk_size": k, "dv": k, "dv_size": k}
+    r = {name: np.full(x.shape, np.nan) for name, x in like.items()}
+    r["lse"] = np.full((q.shape[1], q.shape[0]), np.nan)
+    q0 = k0 = 0
+    for nq, nk in lengths:
+        i, j = slice(q0, q0 + nq), slice(k0, k0 + nk)
+        seen = np.ones((nq, nk), dtype=bool)
+        if causal:
+            seen = np.arange(nk)[None] <= np.arange(nq)[:, None] + nk - nq
+        for name in like:
+            if name[:2] in ("dk", "dv"):
+                r[name][j] = 0.0
+        for h in range(q.shape[1]):
+            g = h // group
+            s = np.where(seen, scale * q[i, h] @ k[j, g].T, -np.inf)
+            top = s.max(1, initial=-np.inf)
+            e = np.exp(s - np.where(np.isinf(top), 0.0, top)[:, None])
+            total = e.sum(1)
+            with np.errstate(divide="ignore"):
+                r["lse"][h, i] = top + np.log(total)
+            p = e / np.where(total == 0, 1.0, total)[:, None]
+            r["out"][i, h] = p @ v[j, g]
+            r["out_size"][i, h] = p @ np.abs(v[j, g])
+            if dout is None:
+                continue
+            do = dout[i, h]
+            dp = do @ v[j, g].T
+            ds = scale * p * (dp - (p * dp).sum(1)[:, None])
+            size = (np.abs(do) * (np.abs(r["out"][i, h]) + r["out_size"][i, h])).sum(1)
+            size = np.abs(ds) + scale * p * size[:, None]
+            r["dq"][i, h], r["dq_size"][i, h] = ds @ k[j, g], size @ np.abs(k[j, g])
+            r["dk"][j, g] += ds.T @ q[i, h]
+            r["dk_size"][j, g] += size.T @ np.abs(q[i, h])
+            r["dv"][j, g] += p.T @ do
+            r["dv_size"][j, g] += p.T @ np.abs(do)
+        q0, k0 = q0 + nq, k0 + nk
+    return r
+
+
+# ------------------------------------------------------- norm behind a residual
+def row_scale(h, eps):
+    """1 / rms of the rows of h."""
+    return 1.0 / np.sqrt(np.mean(np.square(h), axis=1) + eps)
+
+
+# --------------------------------------------------------------- gradient clipping
+def grad_clip(grads, max_norm):
+    """(norm over all, gradients scaled to it)."""
+    norm = np.sqrt(sum(float(np.sum(np.square(g))) for g in grads))
+    by = max_norm / (norm + 1e-6)
+    return norm, [g if by >= 1 else g * by for g in grads]

@@ -38,6 +38,8 @@ EXPORTS = (
     "boost_profile_only", "boost_block_fwd_residual", "boost_block_bwd_residual",
     "boost_rope", "boost_dropout", "boost_fp8_scale_bytes", "boost_fp8_quantize",
     "boost_fp8_matmul_workspace_bytes", "boost_fp8_matmul",
+    "boost_attention_workspace_bytes", "boost_attention", "boost_attention_bwd",
+    "boost_norm_quantize", "boost_grad_clip_workspace_bytes", "boost_grad_clip",
 )
 
 
@@ -77,6 +79,22 @@ class Fp8QuantDesc(ctypes.Structure):
 class Fp8MatmulDesc(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int64) for f in ("G", "M", "N", "K", "a_pitch", "b_pitch")] + \
         [(f, ctypes.c_int32) for f in ("a_fmt", "b_fmt", "act")]
+
+
+ATTENTION_MAX_DIM = 128
+
+
+class AttentionDesc(ctypes.Structure):
+    _fields_ = [("Tq", ctypes.c_int64), ("Tk", ctypes.c_int64)] + \
+        [(f, ctypes.c_int32) for f in ("hq", "hk", "dim", "sequences", "causal")] + \
+        [("scale", ctypes.c_float)] + \
+        [(f"{x}_{y}", ctypes.c_int64) for x in ("q", "k", "v", "o", "do", "dq", "dk", "dv")
+         for y in ("ts", "hs")]
+
+
+class Grad(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("wide", ctypes.c_int32)]
 
 
 def lib_path() -> str:
@@ -122,6 +140,15 @@ def lib():
     L.boost_fp8_matmul_workspace_bytes.argtypes = [ctypes.POINTER(Fp8MatmulDesc)]
     L.boost_fp8_matmul_workspace_bytes.restype = sz
     L.boost_fp8_matmul.argtypes = [ctypes.POINTER(Fp8MatmulDesc)] + [vp] * 7 + [sz, vp]
+    ap = ctypes.POINTER(AttentionDesc)
+    L.boost_attention_workspace_bytes.argtypes = [ap]
+    L.boost_attention_workspace_bytes.restype = sz
+    L.boost_attention.argtypes = [ap] + [vp] * 8 + [sz, vp]
+    L.boost_attention_bwd.argtypes = [ap] + [vp] * 12 + [sz, vp]
+    L.boost_norm_quantize.argtypes = [i64, i64, ctypes.c_int32, ctypes.c_float] + [vp] * 8
+    L.boost_grad_clip_workspace_bytes.argtypes = []
+    L.boost_grad_clip_workspace_bytes.restype = sz
+    L.boost_grad_clip.argtypes = [i64, ctypes.POINTER(Grad), ctypes.c_double, vp, vp, sz, vp]
     L.boost_status_string.argtypes = [ctypes.c_int]
     L.boost_status_string.restype = ctypes.c_char_p
     L.boost_swiglu_fwd.argtypes = [i64, i64, vp, vp, vp, vp]
@@ -142,7 +169,8 @@ def lib():
     for name in EXPORTS:
         if name not in ("boost_block_workspace_bytes", "boost_status_string",
                         "boost_debug_count_log", "boost_fp8_scale_bytes",
-                        "boost_fp8_matmul_workspace_bytes"):
+                        "boost_fp8_matmul_workspace_bytes", "boost_attention_workspace_bytes",
+                        "boost_grad_clip_workspace_bytes"):
             getattr(L, name).restype = ctypes.c_int
     _LIB = L
     return L
@@ -738,6 +766,166 @@ def fp8_matmul(a, a_scales, b, b_scales, K, ws: Workspace, *, row_scale=None, ac
         _take(out, "out", torch.bfloat16, shape, device), _on(wb, "ws", torch.uint8, device),
         ws.nbytes, _raw_stream(stream, device)), "boost_fp8_matmul")
     return out
+
+
+# ------------------------------------------------------------------------ attention
+def attention_workspace_bytes(Tq, Tk, hq, hk, dim, sequences=1) -> int:
+    """Bytes of a workspace for ``attention`` and ``attention_bwd`` at these sizes."""
+    return int(lib().boost_attention_workspace_bytes(
+        AttentionDesc(Tq, Tk, hq, hk, dim, sequences, 0, 1.0)))
+
+
+@functools.lru_cache(maxsize=512)
+def _attention_plan(q, k, v, out, grads, causal, scale, starts):
+    """The descriptor of a call whose tensors have these (shape, stride) pairs; grads: those of
+    dout, dq, dk, dv; starts: the shapes of q_starts and k_starts."""
+    if len(q[0]) != 3 or len(k[0]) != 3:
+        raise ValueError("q, k and v must be [T, heads, dim]")
+    Tq, hq, dim = q[0]
+    Tk, hk = k[0][:2]
+    like_q, like_k = (Tq, hq, dim), (Tk, hk, dim)
+    named = [("q", q, like_q), ("k", k, like_k), ("v", v, like_k), ("out", out, like_q)]
+    if grads:
+        named += list(zip(("dout", "dq", "dk", "dv"), grads, (like_q, like_q, like_k, like_k)))
+    strides = []
+    for name, (shape, stride), want in named:
+        if tuple(shape) != want:
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected {want}")
+        strides += _head_strides(shape, stride, name, want[0], dim)
+    given = [s for s in starts if s is not None]
+    if any(len(s) != 1 or s[0] < 2 or s != given[0] for s in given):
+        raise ValueError("q_starts and k_starts are vectors of one length, sequences + 1")
+    sequences = given[0][0] - 1 if given else 1
+    if sequences > 1 and len(given) != 2:
+        raise ValueError("several sequences need both q_starts and k_starts")
+    return AttentionDesc(Tq, Tk, hq, hk, dim, sequences, causal,
+                         dim ** -0.5 if scale is None else scale, *strides)
+
+
+def _of(t):
+    return t.shape, t.stride()
+
+
+def _starts(t, name, device):
+    return None if t is None else _take(t, name, torch.int32, t.shape, device)
+
+
+def attention(q, k, v, ws: Workspace, *, causal=True, scale=None, q_starts=None, k_starts=None,
+              out=None, lse=None, stream=None):
+    """softmax(scale q k^T) v of q [Tq, hq, dim], k and v [Tk, hk, dim] (hq a multiple of hk, dim
+    a multiple of 8 up to 128, scale dim^-1/2 where none is given): returns (out [Tq, hq, dim],
+    lse [hq, Tq] float32, the logarithms of the rows' sums, which the backward takes).
+
+    q_starts, k_starts: int32 [sequences + 1] on the device, where the packed sequences begin;
+    one sequence of all rows without them. causal: a sequence's last query sees all its keys, each
+    one before one key less, so new tokens may follow a context; a query that sees none gives 0
+    (lse -inf). Rows behind the last sequence are left as they were. q, k, v and out take any
+    token and head strides that are multiples of 8."""
+    bf, device = torch.bfloat16, _device()
+    if out is None:
+        out = torch.empty(q.shape, dtype=bf, device=q.device)
+    D = _attention_plan(_of(q), _of(k), _of(v), _of(out), None, bool(causal), scale,
+                        (None if q_starts is None else q_starts.shape,
+                         None if k_starts is None else k_starts.shape))
+    if lse is None:
+        lse = torch.empty((D.hq, D.Tq), dtype=torch.float32, device=q.device)
+    _check(lib().boost_attention(
+        D, _on(q, "q", bf, device), _on(k, "k", bf, device), _on(v, "v", bf, device),
+        _starts(q_starts, "q_starts", device), _starts(k_starts, "k_starts", device),
+        _on(out, "out", bf, device), _take(lse, "lse", torch.float32, (D.hq, D.Tq), device),
+        _on(ws.buf, "ws", torch.uint8, device), ws.nbytes, _raw_stream(stream, device)),
+        "boost_attention")
+    return out, lse
+
+
+def attention_bwd(q, k, v, out, lse, dout, ws: Workspace, *, causal=True, scale=None,
+                  q_starts=None, k_starts=None, dq=None, dk=None, dv=None, stream=None):
+    """Gradients (dq, dk, dv) of ``attention`` from its out and lse and the gradient of out; the
+    other arguments are the forward's. Every sum is taken in a fixed order."""
+    bf, device = torch.bfloat16, _device()
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=bf, device=q.device)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=bf, device=q.device)
+    if dv is None:
+        dv = torch.empty(v.shape, dtype=bf, device=q.device)
+    D = _attention_plan(_of(q), _of(k), _of(v), _of(out), (_of(dout), _of(dq), _of(dk), _of(dv)),
+                        bool(causal), scale,
+                        (None if q_starts is None else q_starts.shape,
+                         None if k_starts is None else k_starts.shape))
+    _check(lib().boost_attention_bwd(
+        D, _on(q, "q", bf, device), _on(k, "k", bf, device), _on(v, "v", bf, device),
+        _on(out, "out", bf, device), _take(lse, "lse", torch.float32, (D.hq, D.Tq), device),
+        _on(dout, "dout", bf, device), _starts(q_starts, "q_starts", device),
+        _starts(k_starts, "k_starts", device), _on(dq, "dq", bf, device),
+        _on(dk, "dk", bf, device), _on(dv, "dv", bf, device),
+        _on(ws.buf, "ws", torch.uint8, device), ws.nbytes, _raw_stream(stream, device)),
+        "boost_attention_bwd")
+    return dq, dk, dv
+
+
+# ------------------------------------------------------- norm with an 8-bit output
+def norm_quantize(x, *, residual=None, gamma=None, eps=1e-5, fmt="e4m3", h=None, rstd=None,
+                  rows_out=None, stream=None):
+    """h = x + residual [T, d], rstd [T] = (mean h^2 + eps)^-1/2 and the 8-bit operand of h, or of
+    bf16(gamma h): returns (h, rstd, (q, scales)) with (q, scales) as ``fp8_quantize`` gives it by
+    rows. The norm's value is q's times rstd, the product's ``row_scale``. Without a residual h is
+    x itself, unless a tensor to copy it into is given; with one, h may be x or the residual."""
+    if fmt not in FP8_FORMATS:
+        raise ValueError("fmt is 'e4m3' or 'e5m2'")
+    bf, device = torch.bfloat16, _device()
+    if x.dim() != 2:
+        raise ValueError("x must be [T, d]")
+    shape = T, d = x.shape
+    code, dtype = FP8_FORMATS[fmt]
+    xp = _take(x, "x", bf, shape, device)
+    rp = None if residual is None else _take(residual, "residual", bf, shape, device)
+    gp = None if gamma is None else _take(gamma, "gamma", bf, (d,), device)
+    if h is None and residual is not None:
+        h = torch.empty(shape, dtype=bf, device=x.device)
+    hp = None if h is None else _take(h, "h", bf, shape, device)
+    if rstd is None:
+        rstd = torch.empty((T,), dtype=torch.float32, device=x.device)
+    by_rows, q, sf = _operand_out(rows_out, "rows_out", (T, -(-d // 16) * 16),
+                                  (fp8_scale_bytes(T, d),), dtype, x.device, device)
+    _check(lib().boost_norm_quantize(
+        T, d, code, eps, xp, rp, gp, hp, _take(rstd, "rstd", torch.float32, (T,), device), q, sf,
+        _raw_stream(stream, device)), "boost_norm_quantize")
+    return x if h is None else h, rstd, by_rows
+
+
+# ------------------------------------------------------------- gradient clipping
+def grad_clip_workspace_bytes() -> int:
+    return int(lib().boost_grad_clip_workspace_bytes())
+
+
+def grad_clip(grads, max_norm, ws: Workspace, *, outs=None, norm=None, stream=None):
+    """The norm over all gradients (float32 [1], on the device), and each scaled in place by
+    min(1, max_norm / (norm + 1e-6)), or into ``outs``. max_norm None: the norm alone. Gradients
+    are contiguous, bfloat16 or float32, of any number, sizes and shapes."""
+    device = _device()
+    grads = list(grads)
+    outs = grads if outs is None else list(outs)
+    if len(outs) != len(grads):
+        raise ValueError(f"{len(outs)} outs for {len(grads)} gradients")
+    if norm is None:
+        norm = torch.empty((1,), dtype=torch.float32, device=ws.buf.device)
+    table = (Grad * len(grads))()
+    bf, wide = torch.bfloat16, torch.float32
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        dtype, shape = g.dtype, g.shape
+        if dtype is not bf and dtype is not wide:
+            raise TypeError(f"gradient {i} must be bfloat16 or float32, got {dtype}")
+        at = _take(g, f"gradient {i}", dtype, shape, device)
+        to = None
+        if max_norm is not None:
+            to = at if o is g else _take(o, f"out {i}", dtype, shape, device)
+        table[i] = (at, to, g.numel(), dtype is wide)
+    _check(lib().boost_grad_clip(
+        len(grads), table, float("inf") if max_norm is None else max_norm,
+        _take(norm, "norm", wide, (1,), device), _on(ws.buf, "ws", torch.uint8, device), ws.nbytes,
+        _raw_stream(stream, device)), "boost_grad_clip")
+    return norm
 
 
 def check(ws: Workspace, stream=None):

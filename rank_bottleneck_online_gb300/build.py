@@ -26,7 +26,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libboost_block.so")
 
 SOURCES = ["boost_block.cu", "kernels_simple.cu", "gemm_fwd.cu", "gemm_bwd.cu", "profile.cu",
-           "noalloc.cu", "rope.cu", "dropout.cu", "fp8.cu", "fp8_quant.cu", "fp8_gemm.cu"]
+           "noalloc.cu", "rope.cu", "dropout.cu", "fp8.cu", "fp8_quant.cu", "fp8_gemm.cu",
+           "attention.cu", "attention_fwd.cu", "attention_bwd.cu", "norm_quant.cu", "grad_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

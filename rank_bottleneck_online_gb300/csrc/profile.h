@@ -32,6 +32,10 @@ enum KernelId : int {
   K_DROPOUT,
   K_FP8_QUANT,
   K_FP8_GEMM,
+  K_ATTENTION,
+  K_ATTENTION_BWD,
+  K_NORM_QUANT,
+  K_GRAD_CLIP,
   K_COUNT
 };
 

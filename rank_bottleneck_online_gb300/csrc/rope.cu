@@ -20,6 +20,7 @@
 #include <cstdlib>
 
 #include "boost_ops.h"
+#include "heads.h"
 #include "internal.h"
 #include "profile.h"
 #include "simple.cuh"
@@ -258,61 +259,6 @@ cudaError_t launch_rope(const RopeParams& p_in, cudaStream_t stream) {
     return launch_k(n == 8 ? rope_kernel<kAdjacent, 8> : rope_kernel<kAdjacent, 4>, grid, stream, p);
   return launch_k(n == 8 ? rope_kernel<kHalf, 8> : rope_kernel<kHalf, 4>, grid, stream, p);
 }
-
-// ------------------------------------------------------------------ host checks
-// One [T, heads, dim] operand as it lies in memory (strides in elements).
-struct Slice {
-  uintptr_t base;
-  int64_t T, heads, dim, ts, hs;
-  // bytes from the first to behind the last element
-  uint64_t extent() const {
-    return T * heads == 0 ? 0 : 2ull * ((T - 1) * ts + (heads - 1) * hs + dim);
-  }
-  bool same(const Slice& o) const {
-    return base == o.base && heads == o.heads && (T == 1 || ts == o.ts) &&
-           (heads == 1 || hs == o.hs);
-  }
-  // no two elements coincide: tokens apart by more than a token's heads, or heads by more
-  // than a head's tokens
-  bool one_to_one() const {
-    const int64_t token = (heads - 1) * hs + dim, head = (T - 1) * ts + dim;
-    return (heads == 1 || hs >= dim) && (T == 1 || ts >= dim) &&
-           (T == 1 || heads == 1 || ts >= token || hs >= head);
-  }
-};
-
-// Whether |x + i step| >= apart for every i from -times to times.
-bool stays_away(int64_t x, int64_t step, int64_t times, int64_t apart) {
-  if (step == 0) times = 0;
-  const int64_t n = times == 0 ? 0 : -x / step;        // the nearest is one of n - 1 .. n + 1
-  for (int64_t i = n - 1; i <= n + 1; ++i)
-    if (std::abs(x + std::clamp(i, -times, times) * step) < apart) return false;
-  return true;
-}
-
-// Whether two operands share no element: disjoint ranges; heads side by side in the rows of one
-// packed buffer (the same token stride, and spans that do not meet modulo it); or heads that lie
-// between each other's (the same strides, and no pair of heads and tokens that meet).
-bool disjoint(const Slice& a, const Slice& b) {
-  if (a.extent() == 0 || b.extent() == 0) return true;
-  if (a.base + a.extent() <= b.base || b.base + b.extent() <= a.base) return true;
-  if (a.T > 1 && a.ts != b.ts) return false;
-  const int64_t away = static_cast<int64_t>(b.base) - static_cast<int64_t>(a.base);   // bytes
-  if (a.T > 1 && a.ts > 0) {
-    const int64_t sa = 2 * ((a.heads - 1) * a.hs + a.dim), sb = 2 * ((b.heads - 1) * b.hs + b.dim);
-    const int64_t row = 2 * a.ts;
-    // where b's span begins within a's rows
-    const int64_t o = (away % row + row) % row;
-    if (o >= sa && o + sb <= row) return true;
-  }
-  if (a.heads > 1 && b.heads > 1 && a.hs != b.hs) return false;
-  const int64_t hs = a.heads > 1 ? a.hs : b.hs;
-  for (int64_t h = 1 - a.heads; h < b.heads; ++h)      // b's head less a's
-    if (!stays_away(away / 2 + h * hs, a.ts, a.T - 1, a.dim)) return false;
-  return true;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
 
