@@ -1,84 +1,505 @@
-// attention_fwd.cu -- softmax attention over packed sequences, one warp a row.
+// attention_fwd.cu -- softmax attention over packed sequences on the tensor cores.
+//
+// A CTA has two tiles of 128 query rows of a head (A and B) and goes once through the keys they
+// see, 128 at a time: S = Q K^T into TMEM, one thread a row takes its scores, keeps the running
+// maximum and sum, and writes P = 2^(c S - c m) back over them as bf16, which the second product
+// reads from there (O += P V, in TMEM too). While one tile's softmax runs, the tensor core has the
+// other's products. Warp 0 loads K and V tiles through a ring, warp 1 issues, warps 4..7 and 8..11
+// are the rows of A and of B.
+//
+// The maximum that P is taken against only moves when a row's true maximum passes it by more than
+// 2^8 (in the exponent's units: P <= 256, sums in fp32 and a bf16 P lose nothing by that), so O is
+// hardly ever rescaled. P is rounded to bf16 as the second product's operand; the sum takes it
+// before that.
+//
+// Query heads that share a key head share a tile: its rows are `pack` heads of 128 / pack tokens.
+// Where the tiles leave SMs idle, a tile's keys are split over several CTAs, whose parts (fp32,
+// with their own sums) a second kernel joins in order.
 #include <math_constants.h>
 
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
 #include "attention.cuh"
+#include "attention_tc.cuh"
 #include "simple.cuh"
 
 namespace boost_gb300 {
 
 namespace {
 
-struct SimpleParams {
-  AttentionArgs a;
+struct FwdParams {
+  CUtensorMap tmQ, tmK, tmV;             // boxes of 64 values x (pack heads x tok tokens, 128 rows)
+  HeadsOut out;
+  float* lse;                            // [hq, Tq] or NULL
+  const int32_t *q_starts, *k_starts;
+  float *part, *part_lse;                // of the splits: [splits, Tq, hq, dim], [splits, Tq, hq]
+  int64_t Tq, Tk;
+  int32_t hq, dim, sequences, causal;
+  int32_t pack, tok;                     // heads and tokens of a tile
+  int32_t heads, group;                  // hq / pack; of those that share a key head
+  int32_t splits;
+  float scale_log2;
+  DeviceError* err;
+  uint64_t wait_limit_ns;
 };
 
-// Sequence that row t lies in (the last whose start is not behind it), or -1.
-__device__ __forceinline__ int sequence_of(const int32_t* starts, int n, int64_t T, int64_t t) {
-  if (starts == nullptr) return t < T ? 0 : -1;
-  for (int s = 0; s < n; ++s)
-    if (t >= starts[s] && t < min(static_cast<int64_t>(starts[s + 1]), T)) return s;
-  return -1;
-}
+template <int HD>
+struct FwdCfg {
+  static constexpr int kBoxes = HD / 64;
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;
+  static constexpr int kStages = HD == 128 ? 5 : 8;
+  static constexpr int kBars = 2 * kStages + 8;
+  static constexpr int kBarOffset = (2 + kStages) * kTileBytes;
+  static constexpr int kSmemBytes = 1024 + kBarOffset + 8 * kBars + 16;
+  static constexpr int kThreads = 384;
+  static_assert(kSmemBytes <= 232448, "shared memory");
+};
 
-__device__ __forceinline__ float dot(const __nv_bfloat16* a, const __nv_bfloat16* b, int dim) {
-  float s = 0.0f;
-  for (int e = 0; e < dim; e += 8) {
-    float x[8], y[8];
-    unpack8(*reinterpret_cast<const uint4*>(a + e), x);
-    unpack8(*reinterpret_cast<const uint4*>(b + e), y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
+constexpr float kSlack = 8.0f;           // log2 of the largest P
+
+template <int HD>
+__global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
+    attention_fwd_kernel(const __grid_constant__ FwdParams p) {
+  using Cfg = FwdCfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;                                   // A, B
+  uint8_t* sKV = smem + 2 * Cfg::kTileBytes;            // K(0), V(0), K(1), ...
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOffset);
+  uint64_t* empty_bar = full_bar + Cfg::kStages;
+  uint64_t* q_bar = empty_bar + Cfg::kStages;
+  uint64_t* s_bar = q_bar + 1;                          // [2] scores are complete
+  uint64_t* p_bar = s_bar + 2;                          // [2] probabilities are written
+  uint64_t* o_bar = p_bar + 2;                          // [2] the last product is complete
+  uint64_t* done_bar = o_bar + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    mbar_init(q_bar, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_bar[x], 1);
+      mbar_init(&p_bar[x], 4);
+      mbar_init(&o_bar[x], 1);
+    }
+    mbar_init(done_bar, 1);
+    fence_barrier_init();
   }
-  return s;
-}
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.tmQ);
+    tma_prefetch_desc(&p.tmK);
+    tma_prefetch_desc(&p.tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 256 + HD};
+  griddep_wait();
+  griddep_launch_dependents();
 
-__global__ void __launch_bounds__(kThreads) attention_row_kernel(const SimpleParams p) {
-  pdl_enter();
-  const AttentionArgs& a = p.a;
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = item / a.d.hq;
-  const int h = static_cast<int>(item % a.d.hq);
-  if (t >= a.d.Tq) return;
-  const int s = sequence_of(a.q_starts, a.d.sequences, a.d.Tq, t);
-  if (s < 0) return;
-  int32_t q0, nq, k0, nk;
-  sequence_bounds(a.q_starts, a.d.Tq, s, q0, nq);
-  sequence_bounds(a.k_starts, a.d.Tk, s, k0, nk);
-  const int64_t sees = a.d.causal ? min(static_cast<int64_t>(nk), t - q0 + 1 + nk - nq) : nk;
-  const int hk = h / (a.d.hq / a.d.hk);
-  float m = -CUDART_INF_F, l = 0.0f, o[4] = {};
-  for (int64_t j0 = 0; j0 < sees; j0 += 32) {
-    const bool in = j0 + lane < sees;
-    const float x = in ? a.d.scale * dot(a.q.row(t, h), a.k.row(k0 + j0 + lane, hk), a.d.dim) : -CUDART_INF_F;
-    float top = x;
-    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-    const float next = fmaxf(m, top), f = m == -CUDART_INF_F ? 0.0f : __expf(m - next);
-    const float w = in ? __expf(x - next) : 0.0f;
-    l = l * f + warp_sum(w);
-    m = next;
-    for (int i = 0; i < 4; ++i) o[i] *= f;
-    for (int j = 0; j < 32 && j0 + j < sees; ++j) {
-      const float pj = __shfl_sync(0xffffffffu, w, j);
-      const __nv_bfloat16* v = a.v.row(k0 + j0 + j, hk);
-      for (int i = 0; i < 4; ++i)
-        if (i * 32 + lane < a.d.dim) o[i] = fmaf(pj, __bfloat162float(v[i * 32 + lane]), o[i]);
+  // This CTA's pair of tiles, longest rows first.
+  const int32_t head = static_cast<int32_t>(blockIdx.x) % p.heads;
+  Place at = find_tile(p.q_starts, p.k_starts, p.Tq, p.Tk, p.sequences,
+                       static_cast<int32_t>(blockIdx.x) / p.heads, 2 * p.tok, false);
+  const int32_t t0 = (at.tiles - 1 - at.tile) * 2 * p.tok;       // first token in the sequence
+  const int32_t off = at.nk - at.nq;                              // keys before the first query
+  // key tiles [first, first + n) of each, and of this split alone
+  int32_t n[2], first = 0;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int32_t begin = t0 + x * p.tok, last = min(begin + p.tok, at.nq) - 1;
+    int32_t keys = 0;
+    if (at.tiles > 0 && last >= begin) keys = p.causal ? min(at.nk, last + off + 1) : at.nk;
+    n[x] = keys > 0 ? (keys + kTile - 1) / kTile : 0;
+  }
+  if (p.splits > 1) {
+    const int32_t most = max(n[0], n[1]), each = (most + p.splits - 1) / p.splits;
+    first = static_cast<int32_t>(blockIdx.y) * each;
+    n[0] = max(min(n[0] - first, each), 0);
+    n[1] = max(min(n[1] - first, each), 0);
+  }
+  const int32_t steps = max(n[0], n[1]);
+  const int ksteps = (p.dim + 15) / 16;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    uint32_t armed = 0, parities = 0;
+    if (steps > 0) {
+      const int32_t kh = head / p.group;
+      const uint32_t q_bytes = Cfg::kBoxes * 128 * p.pack * p.tok;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(q_bar, ((n[0] > 0) + (n[1] > 0)) * q_bytes);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (n[x] > 0)
+            for (int b = 0; b < Cfg::kBoxes; ++b)
+              tma_load_3d(sQ + x * Cfg::kTileBytes + b * kBoxBytes, &p.tmQ, q_bar, 64 * b,
+                          head * p.pack, at.q0 + t0 + x * p.tok);
+      }
+      __syncwarp();
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int32_t i = 0; i < 2 * steps; ++i) {
+        if (!warp_wait_all(&empty_bar[stage], phase ^ 1u, p.err, 41, p.wait_limit_ns)) break;
+        armed |= 1u << stage;
+        parities = (parities & ~(1u << stage)) | (phase << stage);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&full_bar[stage], Cfg::kTileBytes);
+          for (int b = 0; b < Cfg::kBoxes; ++b)
+            tma_load_3d(sKV + stage * Cfg::kTileBytes + b * kBoxBytes, i & 1 ? &p.tmV : &p.tmK,
+                        &full_bar[stage], 64 * b, kh, at.k0 + (first + (i >> 1)) * kTile);
+        }
+        __syncwarp();
+        if (++stage == Cfg::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      // the copies started here have landed before the CTA exits
+      for (int s = 0; s < Cfg::kStages; ++s)
+        if (armed >> s & 1u)
+          warp_wait_all(&full_bar[s], parities >> s & 1u, nullptr, 47, p.wait_limit_ns);
+      warp_wait_all(q_bar, 0, nullptr, 47, p.wait_limit_ns);
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- MMA issuer
+    const uint32_t id_s = idesc_bf16_f32(kTile, kTile, 0, 0);
+    const uint32_t id_o = idesc_bf16_f32(kTile, 16 * ksteps, 0, 1);
+    const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV);
+    const uint64_t dk = desc_k_major(), dmn = desc_mn_major();
+    auto scores = [&](int x, uint32_t k) {               // S_x = Q_x K^T
+      for (int kk = 0; kk < ksteps; ++kk)
+        tc_mma_bf16(tS[x], dk | k_step(q0 + x * Cfg::kTileBytes, kk), dk | k_step(k, kk), id_s, kk > 0);
+    };
+    auto values = [&](int x, uint32_t v, bool more) {    // O_x += P_x V
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk)
+        tc_mma_bf16_ts(tO[x], tS[x] + 8 * kk, dmn | mn_step(v, kk), id_o, more || kk > 0);
+    };
+    int stage = 0;
+    uint32_t phase = 0;
+    auto next = [&]() {
+      if (++stage == Cfg::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    bool ok = steps > 0 && warp_wait_all(q_bar, 0, p.err, 42, p.wait_limit_ns) &&
+              warp_wait_all(&full_bar[0], 0, p.err, 43, p.wait_limit_ns);
+    if (ok) {
+      tc_fence_after();
+      if (elect_one()) {
+        for (int x = 0; x < 2; ++x)
+          if (n[x] > 0) {
+            scores(x, kv0);
+            tc_commit(&s_bar[x]);
+          }
+        tc_commit(&empty_bar[0]);
+      }
+      __syncwarp();
+      next();
+    }
+    for (int32_t j = 0; j < steps && ok; ++j) {
+      const int v_stage = stage;
+      ok = warp_wait_all(&full_bar[stage], phase, p.err, 44, p.wait_limit_ns);
+      next();
+      const bool more = j + 1 < steps;
+      if (ok && more) ok = warp_wait_all(&full_bar[stage], phase, p.err, 45, p.wait_limit_ns);
+      if (!ok) break;
+      const int32_t left = at.nk - (first + j) * kTile;
+      if (left < kTile) zero_rows(sKV + v_stage * Cfg::kTileBytes, Cfg::kBoxes, left, lane);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (j < n[x]) {
+          if (!warp_wait_all(&p_bar[x], j & 1, p.err, 46, p.wait_limit_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            values(x, kv0 + v_stage * Cfg::kTileBytes, j > 0);
+            if (j + 1 < n[x]) {
+              scores(x, kv0 + stage * Cfg::kTileBytes);
+              tc_commit(&s_bar[x]);
+            } else {
+              tc_commit(&o_bar[x]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
+      if (elect_one()) {
+        tc_commit(&empty_bar[v_stage]);
+        if (more) tc_commit(&empty_bar[stage]);
+      }
+      __syncwarp();
+      if (more) next();
+    }
+    // every MMA issued here is complete before TMEM is released
+    if (elect_one()) tc_commit(done_bar);
+    __syncwarp();
+    warp_wait_all(done_bar, 0, nullptr, 48, p.wait_limit_ns);
+  } else if (warp >= 4 && at.tiles > 0) {
+    // -------------------------------------------------------------- softmax
+    const int x = (warp >> 2) - 1, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_at = tS[x] + lane_base, o_at = tO[x] + lane_base;
+    const int32_t tq = t0 + x * p.tok + row / p.pack;     // token in the sequence
+    const bool valid = row < p.pack * p.tok && tq < at.nq;
+    // keys that this row sees, from this CTA's first
+    const int32_t sees = (p.causal ? min(at.nk, tq + off + 1) : at.nk) - first * kTile;
+    float m = -CUDART_INF_F, l = 0.0f;                    // reference in S's units, sum of P
+    bool ok = true;
+    for (int32_t j = 0; j < n[x]; ++j) {
+      if (!warp_wait_all(&s_bar[x], j & 1, p.err, 49, p.wait_limit_ns)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float s[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        tmem_ld_32x32b_x32(s_at + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
+      tmem_ld_wait();
+      const int32_t lim = sees - j * kTile;
+      if (__any_sync(0xffffffffu, lim < kTile)) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) s[c] = c < lim ? s[c] : -CUDART_INF_F;
+      }
+      float t[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < 128; c += 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = fmaxf(t[i], s[c + i]);
+      const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+      const bool raise = (top - m) * p.scale_log2 > kSlack || (m == -CUDART_INF_F && top > m);
+      if (__any_sync(0xffffffffu, raise)) {
+        const float to = raise ? top : m;
+        const float f = to == m ? 1.0f : exp2_fast((m - to) * p.scale_log2);
+        m = to;
+        l *= f;
+        if (j > 0) {
+#pragma unroll 1
+          for (int c = 0; c < 16 * ksteps; c += 16) {
+            float o[16];
+            tmem_ld_32x32b_x16(o_at + c, o);
+            tmem_ld_wait();
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f);
+            tmem_st_32x32b_x16(o_at + c, w);
+          }
+        }
+      }
+      // (a row that sees nothing yet: all its scores are -inf, and so are their exponents)
+      const float shift = m == -CUDART_INF_F ? 0.0f : -m * p.scale_log2;
+      float sum[4] = {};
+      uint32_t w[64];
+#pragma unroll
+      for (int c = 0; c < 128; c += 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[c + i] = exp2_fast(fmaf(s[c + i], p.scale_log2, shift));
+          sum[i] += s[c + i];
+        }
+        w[c / 2] = pack_bf16x2(s[c], s[c + 1]);
+        w[c / 2 + 1] = pack_bf16x2(s[c + 2], s[c + 3]);
+      }
+      tmem_st_32x32b_x32(s_at, w);
+      tmem_st_32x32b_x32(s_at + 32, w + 32);
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_bar[x]);
+    }
+    // O / l, and the logarithm of the sum
+    if (ok && n[x] > 0) ok = warp_wait_all(&o_bar[x], 0, p.err, 50, p.wait_limit_ns);
+    if (ok) {
+      tc_fence_after();
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // (NaN stays)
+      const float lse2 = l == 0.0f ? -CUDART_INF_F : fmaf(m, p.scale_log2, __log2f(l));
+      const int64_t token = at.q0 + static_cast<int64_t>(tq);
+      const int32_t h = head * p.pack + row % p.pack;
+      __nv_bfloat16* dst = p.out.row(token, h);
+      const int64_t item = (static_cast<int64_t>(blockIdx.y) * p.Tq + token) * p.hq + h;
+      float* part = p.part + item * p.dim;
+      if (valid) {
+        if (p.splits > 1)
+          p.part_lse[item] = lse2;
+        else if (p.lse != nullptr)
+          p.lse[h * p.Tq + token] = lse2 * kLn2;
+      }
+#pragma unroll
+      for (int c = 0; c < HD; c += 32) {
+        float o[32];
+        if (n[x] > 0) {
+          tmem_ld_32x32b_x32(o_at + c, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          if (valid && c + i < p.dim) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = inv == 0.0f ? 0.0f : o[i + e] * inv;
+            if (p.splits > 1) {
+              *reinterpret_cast<float4*>(part + c + i) = make_float4(f[0], f[1], f[2], f[3]);
+              *reinterpret_cast<float4*>(part + c + i + 4) = make_float4(f[4], f[5], f[6], f[7]);
+            } else {
+              *reinterpret_cast<uint4*>(dst + c + i) = pack8(f);
+            }
+          }
+        }
+      }
+      tc_fence_before();
     }
   }
-  for (int i = 0; i < 4; ++i)
-    if (i * 32 + lane < a.d.dim)
-      a.out.row(t, h)[i * 32 + lane] = __float2bfloat16_rn(l == 0.0f ? 0.0f : o[i] / l);
-  if (lane == 0 && a.lse != nullptr) a.lse[h * a.d.Tq + t] = m + logf(l);
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the splits of a row's keys: a warp a row of one head.
+__global__ void __launch_bounds__(kThreads) attention_join_kernel(const FwdParams p) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t rows = p.Tq * p.hq;
+  if (item >= rows) return;
+  const int32_t token = static_cast<int32_t>(item / p.hq), h = static_cast<int32_t>(item % p.hq);
+  bool in = false;                                       // rows of no sequence stay
+  for (int s = lane; s < p.sequences; s += 32) {
+    int32_t q0, nq;
+    sequence_bounds(p.q_starts, p.Tq, s, q0, nq);
+    in |= token >= q0 && token < q0 + nq;
+  }
+  if (!__any_sync(0xffffffffu, in)) return;
+  float top = -CUDART_INF_F;
+  for (int i = 0; i < p.splits; ++i) top = fmaxf(top, p.part_lse[i * rows + item]);
+  const float base = top == -CUDART_INF_F ? 0.0f : top;
+  float sum = 0.0f, o[4] = {};
+  const int c = lane * 4;
+  for (int i = 0; i < p.splits; ++i) {
+    const float w = exp2_fast(p.part_lse[i * rows + item] - base);
+    sum += w;
+    if (c < p.dim && w != 0.0f) {
+      const float4 v = *reinterpret_cast<const float4*>(p.part + (i * rows + item) * p.dim + c);
+      o[0] = fmaf(w, v.x, o[0]); o[1] = fmaf(w, v.y, o[1]);
+      o[2] = fmaf(w, v.z, o[2]); o[3] = fmaf(w, v.w, o[3]);
+    }
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (c < p.dim)
+    *reinterpret_cast<uint2*>(p.out.row(token, h) + c) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  if (lane == 0 && p.lse != nullptr) p.lse[h * p.Tq + token] = (top + __log2f(sum)) * kLn2;
+}
+
+// Heads that share a tile's rows.
+int packed_heads(const boost_attention_desc& d) {
+  const int group = d.hq / d.hk;
+  return group <= 32 ? group : 1;        // (128 / 33 tokens would leave a fifth of the rows idle)
+}
+
+int64_t tile_pairs(const boost_attention_desc& d) {
+  return most_tiles(d.Tq, 2 * (kTile / packed_heads(d)), d.sequences);
+}
+
+// CTAs that share a tile's keys: as many as fill the SMs, each with four tiles of an average
+// sequence's keys at least.
+int key_splits(const boost_attention_desc& d) {
+  const int64_t ctas = tile_pairs(d) * (d.hq / packed_heads(d));
+  const int64_t tiles = d.Tk / d.sequences / kTile;
+  if (ctas == 0) return 1;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({304 / ctas, tiles / 4, 64})));
+}
+
+template <int HD>
+cudaError_t launch_fwd(const FwdParams& p, int64_t pairs, cudaStream_t stream) {
+  using Cfg = FwdCfg<HD>;
+  const auto kern = attention_fwd_kernel<HD>;
+  static std::atomic<bool> ready[64];    // per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs * p.heads), p.splits, 1);
+  cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace
 
 size_t attention_workspace(const boost_attention_desc& d) {
-  return 256 + 8 * static_cast<size_t>(d.hq) * d.Tq;
+  const size_t rows = static_cast<size_t>(d.hq) * d.Tq, splits = key_splits(d);
+  const size_t fwd = splits > 1 ? 4 * splits * rows * (d.dim + 1) : 0;
+  return 256 + std::max(fwd, 8 * rows);
 }
 
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream) {
-  return launch_k(attention_row_kernel, (a.d.Tq * a.d.hq + 7) / 8, stream, SimpleParams{a});
+  const boost_attention_desc& d = a.d;
+  FwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.pack = packed_heads(d);
+  p.tok = kTile / p.pack;
+  p.heads = d.hq / p.pack;
+  p.group = p.heads / d.hk;
+  if (!heads_map(&p.tmQ, a.q.at, a.ws, d.Tq, d.hq, d.dim, d.q_ts, d.q_hs, p.pack, p.tok) ||
+      !heads_map(&p.tmK, a.k.at, a.ws, d.Tk, d.hk, d.dim, d.k_ts, d.k_hs, 1, kTile) ||
+      !heads_map(&p.tmV, a.v.at, a.ws, d.Tk, d.hk, d.dim, d.v_ts, d.v_hs, 1, kTile))
+    return cudaErrorInvalidValue;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.q_starts = a.q_starts;
+  p.k_starts = a.k_starts;
+  p.Tq = d.Tq;
+  p.Tk = d.Tk;
+  p.hq = d.hq;
+  p.dim = d.dim;
+  p.sequences = d.sequences;
+  p.causal = d.causal;
+  p.splits = key_splits(d);
+  p.scale_log2 = d.scale * kLog2e;
+  p.err = static_cast<DeviceError*>(a.ws);
+  p.wait_limit_ns = wait_limit_ns();
+  const int64_t rows = d.Tq * d.hq;
+  p.part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + 256);
+  p.part_lse = p.part + p.splits * rows * d.dim;
+  const int64_t pairs = tile_pairs(d);
+  cudaError_t e = d.dim <= 64 ? launch_fwd<64>(p, pairs, stream) : launch_fwd<128>(p, pairs, stream);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  return launch_k(attention_join_kernel, (rows + kThreads / 32 - 1) / (kThreads / 32), stream, p);
 }
 
 }  // namespace boost_gb300

@@ -1,0 +1,166 @@
+// attention_tc.cuh -- what the tensor-core attention kernels share: MMAs with an operand in TMEM,
+// tiles of [T, heads, dim] operands in shared memory, and how a tile finds its sequence.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "attention.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace boost_gb300 {
+
+constexpr int kTile = 128;               // rows of a tile: lanes of TMEM
+
+// D[tmem] (+)= A[tmem] * B[smem], kind::f16: A holds two bf16 values a column, 128 rows.
+__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Each thread of the warp writes 32 consecutive columns of its TMEM lane.
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// Each thread of the warp writes 16 consecutive columns of its TMEM lane.
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// 2^x; results below 2^-126 are 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A wait of the whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait_all(uint64_t* bar, uint32_t parity, DeviceError* err,
+                                              uint32_t where, uint64_t limit_ns) {
+  return __all_sync(0xffffffffu, bounded_wait(bar, parity, err, where, limit_ns));
+}
+
+// A tile lies in shared memory as boxes of 64 values a row: rows of 128 bytes, 128-byte swizzle,
+// 16 KB a box. As K-major operand (the values are contracted) a step of 16 values is 32 bytes
+// within a box; as MN-major operand (the rows are contracted) a step of 16 rows is 2048 bytes, and
+// the next 64 values are the next box.
+constexpr int kBoxBytes = kTile * 128;
+
+__device__ __forceinline__ uint64_t desc_k_major() { return desc_hi_sw128(16u, 1024u); }
+__device__ __forceinline__ uint64_t desc_mn_major() { return desc_hi_sw128(kBoxBytes, 1024u); }
+
+// Start addresses (>> 4) of K step kk of a tile at shared address `base`.
+__device__ __forceinline__ uint32_t k_step(uint32_t base, int kk) {
+  return (base + (kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+}
+__device__ __forceinline__ uint32_t mn_step(uint32_t base, int kk) { return (base + kk * 2048) >> 4; }
+
+// Zero rows [from, 128) of a tile of `boxes` boxes that a TMA load has filled, by a whole warp:
+// rows of another sequence may hold NaN, which a probability of 0 would not hide.
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, int from, int lane) {
+  for (int b = 0; b < boxes; ++b)
+    for (int i = from * 8 + lane; i < kTile * 8; i += 32)
+      *reinterpret_cast<uint4*>(tile + b * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// A sequence's bounds, and the number of one of its tiles.
+struct Place {
+  int32_t tile, tiles;                   // tiles < 0: none
+  int32_t q0, nq, k0, nk;
+};
+
+// Where tile `index` of all sequences lies, sequence s having ceil(rows / per) tiles; by a whole
+// warp, each lane with a sequence of its own at a time. `keys`: the tiles are of the keys.
+__device__ __forceinline__ Place find_tile(const int32_t* q_starts, const int32_t* k_starts,
+                                           int64_t Tq, int64_t Tk, int sequences, int32_t index,
+                                           int32_t per, bool keys) {
+  const int lane = threadIdx.x & 31;
+  Place f{0, -1, 0, 0, 0, 0};
+  for (int s0 = 0; s0 < sequences; s0 += 32) {
+    Place mine{0, 0, 0, 0, 0, 0};
+    if (s0 + lane < sequences) {
+      sequence_bounds(q_starts, Tq, s0 + lane, mine.q0, mine.nq);
+      sequence_bounds(k_starts, Tk, s0 + lane, mine.k0, mine.nk);
+      mine.tiles = ((keys ? mine.nk : mine.nq) + per - 1) / per;
+    }
+    int32_t sum = mine.tiles;            // up to and with this lane's
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t below = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += below;
+    }
+    const uint32_t has = __ballot_sync(0xffffffffu, index < sum);
+    if (has != 0) {
+      const int src = __ffs(has) - 1;
+      f.tile = index - __shfl_sync(0xffffffffu, sum - mine.tiles, src);
+      f.tiles = __shfl_sync(0xffffffffu, mine.tiles, src);
+      f.q0 = __shfl_sync(0xffffffffu, mine.q0, src);
+      f.nq = __shfl_sync(0xffffffffu, mine.nq, src);
+      f.k0 = __shfl_sync(0xffffffffu, mine.k0, src);
+      f.nk = __shfl_sync(0xffffffffu, mine.nk, src);
+      return f;
+    }
+    index -= __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return f;
+}
+
+// Most tiles that sequences of T rows in all can have.
+inline int64_t most_tiles(int64_t T, int64_t per, int64_t sequences) {
+  const int64_t n = T / per + (sequences < T ? sequences : T);
+  return n < T ? n : T;
+}
+
+// Tensor map of a [T, heads, dim] operand with boxes of 64 values, `box_heads` heads and `rows`
+// tokens; an empty operand (whose tiles are never loaded) as one row of `any`.
+inline bool heads_map(CUtensorMap* m, const __nv_bfloat16* at, const void* any, int64_t T,
+                      int64_t heads, int64_t dim, int64_t ts, int64_t hs, uint32_t box_heads,
+                      uint32_t rows) {
+  EncodeFn enc = get_encode();
+  if (enc == nullptr) return false;
+  const bool none = T == 0;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(none ? 1 : T)};
+  // the stride of a single head or token says nothing: a plain one in its place
+  const cuuint64_t strides[2] = {2ull * (heads > 1 ? hs : dim), 2ull * (T > 1 ? ts : heads * dim)};
+  const cuuint32_t box[3] = {64, box_heads, rows}, ones[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             none ? const_cast<void*>(any) : const_cast<__nv_bfloat16*>(at), dims, strides, box,
+             ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace boost_gb300
