@@ -1,121 +1,550 @@
-// attention_bwd.cu -- gradients of attention, one warp a row of dq or of dk and dv.
+// attention_bwd.cu -- gradients of attention on the tensor cores, in two passes of one kernel.
+//
+//     P = exp(scale S - lse), S = q k^T      dP = dout v^T      dS = P (dP - delta)
+//     dv = P^T dout        dk = scale dS^T q        dq = scale dS k,   delta = sum_j P dP
+//
+// Both passes keep two tiles of 128 rows (X0, X1) and go through tiles of 128 rows of the other
+// side (Y0, Y1), forming S = X0 Y0^T and dP = X1 Y1^T in TMEM; threads turn them into P and dS,
+// written back over them as bf16, which are the first operands of two more products, summed in
+// TMEM. The first pass keeps q and dout of 128 queries and sums dS k; the second keeps k and v of
+// 128 keys (S and dP transposed), goes through the queries of all heads that share the key head,
+// and sums P^T dout and dS^T q. So no sum leaves the SM, none is taken in another order from call
+// to call, and S and dP are formed twice (8 products of 128^3 a pair of tiles instead of 5) where
+// one pass would add dq to memory by atomics.
+//
+// delta: sum_d dout out is its value but for the rounding of out, which is of the size of dS
+// where a row's probability lies on few keys (a row of one key: dS = 0). The first pass takes
+// delta from out and sums what is missing, e = sum_j P (dP - delta), beside sum_j P k in TMEM;
+// dq = scale (sum dS k - e sum P k), and the second pass reads delta + e. (Without that the
+// gradients of 77 tokens were off by 0.0030, relative to all, with it by the 0.002 of a bf16
+// result and bf16 dS.)
+//
+// Warp 0 loads the tiles through a ring, warp 1 issues the products, warp 2 fetches the second
+// pass's lse and delta, eight warps are the rows of a tile, two threads a row. The products of
+// one kind run while the threads work on the other's scores: acc1 += P B and the next S during dS,
+// acc2 += dS Y0 and the next dP during P.
 #include <math_constants.h>
 
+#include <atomic>
+#include <cstring>
+
 #include "attention.cuh"
+#include "attention_tc.cuh"
 #include "simple.cuh"
 
 namespace boost_gb300 {
 
 namespace {
 
-struct SimpleBwdParams {
-  AttentionArgs a;
-  float* delta;                          // [hq, Tq]
+enum Pass : int { kDq = 0, kDkv = 1 };
+
+struct BwdParams {
+  CUtensorMap tmX0, tmX1, tmY0, tmY1;    // boxes of 64 values x 128 rows of one head
+  HeadsIn o, dout;                       // kDq
+  HeadsOut g1, g2;                       // kDq: -, dq; kDkv: dv, dk
+  const float* lse;                      // [hq, Tq]
+  float* delta;                          // [hq, Tq]: written by kDq, read by kDkv
+  const int32_t *q_starts, *k_starts;
+  int64_t Tq, Tk;
+  int32_t heads, group;                  // of the tiles' side; query heads of a key head
+  int32_t dim, sequences, causal;
+  float scale, scale_log2;
+  DeviceError* err;
+  uint64_t wait_limit_ns;
 };
 
-__device__ __forceinline__ int sequence_of(const int32_t* starts, int n, int64_t T, int64_t t) {
-  if (starts == nullptr) return t < T ? 0 : -1;
-  for (int s = 0; s < n; ++s)
-    if (t >= starts[s] && t < min(static_cast<int64_t>(starts[s + 1]), T)) return s;
-  return -1;
-}
+template <int HD>
+struct BwdCfg {
+  static constexpr int kBoxes = HD / 64;
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;
+  static constexpr int kStages = HD == 128 ? 4 : 8;      // Y0(0), Y1(0), Y0(1), ...
+  static constexpr int kBars = 2 * kStages + 11;
+  static constexpr int kStatOffset = (2 + kStages) * kTileBytes;
+  static constexpr int kStatBytes = 2 * 2 * 4 * kTile;   // two buffers of lse and delta
+  static constexpr int kBarOffset = kStatOffset + kStatBytes;
+  static constexpr int kSmemBytes = 1024 + kBarOffset + 8 * kBars + 16;
+  static constexpr int kThreads = 384;
+  static_assert(kSmemBytes <= 232448, "shared memory");
+};
 
-__device__ __forceinline__ float dot(const __nv_bfloat16* a, const __nv_bfloat16* b, int dim) {
+// Sum of a row's products over `n` values (a multiple of 8).
+__device__ __forceinline__ float dot_row(const __nv_bfloat16* a, const __nv_bfloat16* b, int n) {
   float s = 0.0f;
-  for (int e = 0; e < dim; e += 8) {
+  for (int e = 0; e < n; e += 8) {
     float x[8], y[8];
-    unpack8(*reinterpret_cast<const uint4*>(a + e), x);
-    unpack8(*reinterpret_cast<const uint4*>(b + e), y);
+    unpack8(__ldg(reinterpret_cast<const uint4*>(a + e)), x);
+    unpack8(__ldg(reinterpret_cast<const uint4*>(b + e)), y);
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
   }
   return s;
 }
 
-__global__ void __launch_bounds__(kThreads) attention_dq_row_kernel(const SimpleBwdParams p) {
-  pdl_enter();
-  const AttentionArgs& a = p.a;
-  const int lane = threadIdx.x & 31, dim = a.d.dim;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = item / a.d.hq;
-  const int h = static_cast<int>(item % a.d.hq);
-  if (t >= a.d.Tq) return;
-  const int s = sequence_of(a.q_starts, a.d.sequences, a.d.Tq, t);
-  if (s < 0) return;
-  int32_t q0, nq, k0, nk;
-  sequence_bounds(a.q_starts, a.d.Tq, s, q0, nq);
-  sequence_bounds(a.k_starts, a.d.Tk, s, k0, nk);
-  const int64_t sees = a.d.causal ? min(static_cast<int64_t>(nk), t - q0 + 1 + nk - nq) : nk;
-  const int hk = h / (a.d.hq / a.d.hk);
-  const float delta = dot(a.dout.row(t, h), a.o.row(t, h), dim), lse = a.lse[h * a.d.Tq + t];
-  if (lane == 0) p.delta[h * a.d.Tq + t] = delta;
-  float g[4] = {};
-  for (int64_t j0 = 0; j0 < sees; j0 += 32) {
-    float ds = 0.0f;
-    if (j0 + lane < sees) {
-      const float w = __expf(a.d.scale * dot(a.q.row(t, h), a.k.row(k0 + j0 + lane, hk), dim) - lse);
-      ds = w * (dot(a.dout.row(t, h), a.v.row(k0 + j0 + lane, hk), dim) - delta);
+template <int HD, int PASS>
+__global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
+    attention_bwd_kernel(const __grid_constant__ BwdParams p) {
+  using Cfg = BwdCfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sX = smem;                                   // X0, X1
+  uint8_t* sY = smem + 2 * Cfg::kTileBytes;
+  float* stat = reinterpret_cast<float*>(smem + Cfg::kStatOffset);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOffset);
+  uint64_t* empty_bar = full_bar + Cfg::kStages;
+  uint64_t* x_bar = empty_bar + Cfg::kStages;
+  uint64_t* s_bar = x_bar + 1;                          // S is complete
+  uint64_t* d_bar = s_bar + 1;                          // dP is complete
+  uint64_t* p_bar = d_bar + 1;                          // P is written
+  uint64_t* ds_bar = p_bar + 1;                         // dS is written
+  uint64_t* acc_bar = ds_bar + 1;                       // the sums are complete
+  uint64_t* stat_full = acc_bar + 1;                    // [2]
+  uint64_t* stat_empty = stat_full + 2;                 // [2]
+  uint64_t* done_bar = stat_empty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
     }
-    for (int j = 0; j < 32 && j0 + j < sees; ++j) {
-      const float d = __shfl_sync(0xffffffffu, ds, j);
-      const __nv_bfloat16* k = a.k.row(k0 + j0 + j, hk);
-      for (int i = 0; i < 4; ++i)
-        if (i * 32 + lane < dim) g[i] = fmaf(d, __bfloat162float(k[i * 32 + lane]), g[i]);
+    mbar_init(x_bar, 1);
+    mbar_init(s_bar, 1);
+    mbar_init(d_bar, 1);
+    mbar_init(p_bar, 8);
+    mbar_init(ds_bar, 8);
+    mbar_init(acc_bar, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&stat_full[b], 1);
+      mbar_init(&stat_empty[b], 8);
+    }
+    mbar_init(done_bar, 1);
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.tmX0);
+    tma_prefetch_desc(&p.tmX1);
+    tma_prefetch_desc(&p.tmY0);
+    tma_prefetch_desc(&p.tmY1);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t tS = tmem, tD = tmem + 128, tAcc1 = tmem + 256, tAcc2 = tmem + 256 + HD;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // This CTA's tile of queries (kDq, longest rows first) or keys, and the tiles [first, first +
+  // count) of the other side that its rows see; kDkv has those once for each head of the group.
+  const int32_t head = static_cast<int32_t>(blockIdx.x) % p.heads;
+  Place at = find_tile(p.q_starts, p.k_starts, p.Tq, p.Tk, p.sequences,
+                       static_cast<int32_t>(blockIdx.x) / p.heads, kTile, PASS == kDkv);
+  const int32_t off = at.nk - at.nq;                     // keys before the first query
+  const int32_t x0 = (PASS == kDq ? at.tiles - 1 - at.tile : at.tile) * kTile;
+  const int32_t nx = PASS == kDq ? at.nq : at.nk, ny = PASS == kDq ? at.nk : at.nq;
+  int32_t first = 0, count = 0;
+  if (at.tiles > 0) {
+    if (PASS == kDq) {
+      const int32_t keys = p.causal ? min(at.nk, min(x0 + kTile, at.nq) + off) : at.nk;
+      count = keys > 0 ? (keys + kTile - 1) / kTile : 0;
+    } else {
+      first = p.causal ? max(x0 - off, 0) / kTile : 0;
+      count = max((at.nq + kTile - 1) / kTile - first, 0);
     }
   }
-  for (int i = 0; i < 4; ++i)
-    if (i * 32 + lane < dim) a.dq.row(t, h)[i * 32 + lane] = __float2bfloat16_rn(g[i] * a.d.scale);
+  const int32_t steps = PASS == kDq ? count : count * p.group;
+  const int32_t x_row = (PASS == kDq ? at.q0 : at.k0) + x0;
+  const int32_t y_row = PASS == kDq ? at.k0 : at.q0;
+  const int32_t y_head = PASS == kDq ? head / p.group : head * p.group;
+  const int ksteps = (p.dim + 15) / 16;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    uint32_t armed = 0, parities = 0;
+    if (steps > 0) {
+      if (elect_one()) {
+        mbar_arrive_expect_tx(x_bar, 2 * Cfg::kTileBytes);
+        for (int b = 0; b < Cfg::kBoxes; ++b) {
+          tma_load_3d(sX + b * kBoxBytes, &p.tmX0, x_bar, 64 * b, head, x_row);
+          tma_load_3d(sX + Cfg::kTileBytes + b * kBoxBytes, &p.tmX1, x_bar, 64 * b, head, x_row);
+        }
+      }
+      __syncwarp();
+      int stage = 0;
+      uint32_t phase = 0;
+      int32_t tile = first, h = y_head;
+      for (int32_t i = 0; i < 2 * steps; ++i) {
+        if (!warp_wait_all(&empty_bar[stage], phase ^ 1u, p.err, 61, p.wait_limit_ns)) break;
+        armed |= 1u << stage;
+        parities = (parities & ~(1u << stage)) | (phase << stage);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&full_bar[stage], Cfg::kTileBytes);
+          for (int b = 0; b < Cfg::kBoxes; ++b)
+            tma_load_3d(sY + stage * Cfg::kTileBytes + b * kBoxBytes, i & 1 ? &p.tmY1 : &p.tmY0,
+                        &full_bar[stage], 64 * b, h, y_row + tile * kTile);
+        }
+        __syncwarp();
+        if ((i & 1) && ++tile == first + count) {
+          tile = first;
+          ++h;
+        }
+        if (++stage == Cfg::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      // the copies started here have landed before the CTA exits
+      for (int s = 0; s < Cfg::kStages; ++s)
+        if (armed >> s & 1u)
+          warp_wait_all(&full_bar[s], parities >> s & 1u, nullptr, 67, p.wait_limit_ns);
+      warp_wait_all(x_bar, 0, nullptr, 67, p.wait_limit_ns);
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- MMA issuer
+    const uint32_t id_s = idesc_bf16_f32(kTile, kTile, 0, 0);
+    const uint32_t id_acc = idesc_bf16_f32(kTile, 16 * ksteps, 0, 1);
+    const uint32_t x_at = smem_u32(sX), y_at = smem_u32(sY);
+    const uint64_t dk = desc_k_major(), dmn = desc_mn_major();
+    auto scores = [&](uint32_t d, uint32_t x, uint32_t y) {          // X Y^T
+      for (int kk = 0; kk < ksteps; ++kk)
+        tc_mma_bf16(d, dk | k_step(x, kk), dk | k_step(y, kk), id_s, kk > 0);
+    };
+    // the two halves of a row's 128 values lie 64 columns apart, over their own scores
+    auto sums = [&](uint32_t d, uint32_t a, uint32_t y, bool more) {  // acc += A Y
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk)
+        tc_mma_bf16_ts(d, a + 8 * kk + (kk >= 4 ? 32 : 0), dmn | mn_step(y, kk), id_acc,
+                       more || kk > 0);
+    };
+    // Wait for tile `u` of the ring; rows behind the sequence become 0.
+    auto take = [&](int32_t u, int32_t step) {
+      const int s = u % Cfg::kStages;
+      if (!warp_wait_all(&full_bar[s], u / Cfg::kStages & 1, p.err, 63, p.wait_limit_ns))
+        return false;
+      const int32_t left = ny - (first + step % max(count, 1)) * kTile;
+      if (left < kTile) zero_rows(sY + s * Cfg::kTileBytes, Cfg::kBoxes, left, lane);
+      tc_fence_after();
+      return true;
+    };
+    auto slot = [&](int32_t u) { return y_at + u % Cfg::kStages * Cfg::kTileBytes; };
+    bool ok = steps > 0 && warp_wait_all(x_bar, 0, p.err, 62, p.wait_limit_ns) && take(0, 0);
+    if (ok) {
+      if (elect_one()) {
+        scores(tS, x_at, slot(0));
+        tc_commit(s_bar);
+      }
+      __syncwarp();
+      ok = take(1, 0);
+    }
+    if (ok) {
+      if (elect_one()) {
+        scores(tD, x_at + Cfg::kTileBytes, slot(1));
+        tc_commit(d_bar);
+        if (PASS == kDq) tc_commit(&empty_bar[1]);
+      }
+      __syncwarp();
+    }
+    for (int32_t i = 0; i < steps && ok; ++i) {
+      const int32_t y0 = 2 * i, y1 = 2 * i + 1;
+      const bool more = i + 1 < steps;
+      ok = warp_wait_all(p_bar, i & 1, p.err, 64, p.wait_limit_ns);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        sums(tAcc1, tS, slot(PASS == kDq ? y0 : y1), i > 0);
+        if (PASS == kDkv) tc_commit(&empty_bar[y1 % Cfg::kStages]);
+      }
+      __syncwarp();
+      if (more) {
+        ok = take(y0 + 2, i + 1);
+        if (!ok) break;
+        if (elect_one()) {
+          scores(tS, x_at, slot(y0 + 2));
+          tc_commit(s_bar);
+        }
+        __syncwarp();
+      }
+      ok = warp_wait_all(ds_bar, i & 1, p.err, 65, p.wait_limit_ns);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        sums(tAcc2, tD, slot(y0), i > 0);
+        tc_commit(more ? &empty_bar[y0 % Cfg::kStages] : acc_bar);
+      }
+      __syncwarp();
+      if (more) {
+        ok = take(y1 + 2, i + 1);
+        if (!ok) break;
+        if (elect_one()) {
+          scores(tD, x_at + Cfg::kTileBytes, slot(y1 + 2));
+          tc_commit(d_bar);
+          if (PASS == kDq) tc_commit(&empty_bar[(y1 + 2) % Cfg::kStages]);
+        }
+        __syncwarp();
+      }
+    }
+    // every MMA issued here is complete before TMEM is released
+    if (elect_one()) tc_commit(done_bar);
+    __syncwarp();
+    warp_wait_all(done_bar, 0, nullptr, 68, p.wait_limit_ns);
+  } else if (warp == 2 && PASS == kDkv) {
+    // ----------------------------------------------- lse and delta of the queries
+    for (int32_t i = 0; i < steps; ++i) {
+      const int b = i & 1;
+      if (!warp_wait_all(&stat_empty[b], (i >> 1 & 1) ^ 1, p.err, 66, p.wait_limit_ns)) break;
+      const int32_t q = (first + i % count) * kTile, h = y_head + i / count;
+#pragma unroll
+      for (int k = 0; k < kTile; k += 32) {
+        // (a query that is none, or sees no key, has no probabilities)
+        float l = CUDART_INF_F, d = 0.0f;
+        if (q + k + lane < at.nq) {
+          const int64_t t = static_cast<int64_t>(h) * p.Tq + at.q0 + q + k + lane;
+          const float v = p.lse[t];
+          if (v != -CUDART_INF_F) {
+            l = v * kLog2e;
+            d = p.delta[t];
+          }
+        }
+        stat[b * 2 * kTile + k + lane] = l;
+        stat[b * 2 * kTile + kTile + k + lane] = d;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&stat_full[b]);
+    }
+  } else if (warp >= 4 && at.tiles > 0) {
+    // ------------------------------------------------------ probabilities, dS
+    const int half = (warp >> 2) - 1, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_at = tS + lane_base + 64 * half, d_at = tD + lane_base + 64 * half;
+    const int32_t x = x0 + row;                           // in the sequence
+    const bool valid = x < nx;
+    const int64_t token = x_row + static_cast<int64_t>(row);
+    float lse = 0.0f, delta = 0.0f, e = 0.0f;             // kDq: of this row; what delta lacks
+    if (PASS == kDq) {
+      if (valid) {
+        lse = p.lse[head * p.Tq + token] * kLog2e;
+        const int32_t c0 = half * (HD / 2);
+        delta = dot_row(p.dout.row(token, head) + c0, p.o.row(token, head) + c0,
+                        min(max(p.dim - c0, 0), HD / 2));
+      }
+      // (the two halves of a row, in order)
+      stat[half * kTile + row] = delta;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      delta = stat[row] + stat[kTile + row];
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+    }
+    // kDq: keys that this row sees; kDkv: the first query that sees this row
+    const int32_t bound = PASS == kDq ? (p.causal ? min(at.nk, x + off + 1) : at.nk)
+                                      : (p.causal ? x - off : 0);
+    bool ok = true;
+    int32_t tile = first;
+    for (int32_t i = 0; i < steps; ++i) {
+      const float* st = stat + (i & 1) * 2 * kTile + half * 64;
+      if (PASS == kDkv) ok = warp_wait_all(&stat_full[i & 1], i >> 1 & 1, p.err, 69, p.wait_limit_ns);
+      ok = ok && warp_wait_all(s_bar, i & 1, p.err, 70, p.wait_limit_ns);
+      if (!ok) break;
+      tc_fence_after();
+      float s[64];
+      tmem_ld_32x32b_x32(s_at, *reinterpret_cast<float(*)[32]>(s));
+      tmem_ld_32x32b_x32(s_at + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+      tmem_ld_wait();
+      const int32_t lim = bound - tile * kTile - 64 * half;   // of this half's columns
+      if (PASS == kDq) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) s[c] = exp2_fast(fmaf(s[c], p.scale_log2, -lse));
+        if (__any_sync(0xffffffffu, lim < 64)) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) s[c] = c < lim ? s[c] : 0.0f;
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(st + c);
+          s[c] = exp2_fast(fmaf(s[c], p.scale_log2, -l.x));
+          s[c + 1] = exp2_fast(fmaf(s[c + 1], p.scale_log2, -l.y));
+          s[c + 2] = exp2_fast(fmaf(s[c + 2], p.scale_log2, -l.z));
+          s[c + 3] = exp2_fast(fmaf(s[c + 3], p.scale_log2, -l.w));
+        }
+        if (__any_sync(0xffffffffu, lim > 0)) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) s[c] = c >= lim ? s[c] : 0.0f;
+        }
+      }
+      uint32_t w[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
+      tmem_st_32x32b_x32(s_at, w);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_bar);
+
+      ok = warp_wait_all(d_bar, i & 1, p.err, 71, p.wait_limit_ns);
+      if (!ok) break;
+      tc_fence_after();
+      float d[64];
+      tmem_ld_32x32b_x32(d_at, *reinterpret_cast<float(*)[32]>(d));
+      tmem_ld_32x32b_x32(d_at + 32, *reinterpret_cast<float(*)[32]>(d + 32));
+      tmem_ld_wait();
+      if (PASS == kDq) {
+        float sum[4] = {};
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          d[c] = s[c] * (d[c] - delta);
+          sum[c & 3] += d[c];
+        }
+        e += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 l = *reinterpret_cast<const float4*>(st + kTile + c);
+          d[c] = s[c] * (d[c] - l.x);
+          d[c + 1] = s[c + 1] * (d[c + 1] - l.y);
+          d[c + 2] = s[c + 2] * (d[c + 2] - l.z);
+          d[c + 3] = s[c + 3] * (d[c + 3] - l.w);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(d[2 * c], d[2 * c + 1]);
+      tmem_st_32x32b_x32(d_at, w);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(ds_bar);
+        if (PASS == kDkv) mbar_arrive(&stat_empty[i & 1]);
+      }
+      if (++tile == first + count) tile = first;
+    }
+    if (ok && steps > 0) ok = warp_wait_all(acc_bar, 0, p.err, 72, p.wait_limit_ns);
+    tc_fence_after();
+    if (PASS == kDq) {
+      stat[half * kTile + row] = e;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      e = stat[row] + stat[kTile + row];
+      if (valid && half == 0) p.delta[head * p.Tq + token] = delta + e;
+    }
+    if (ok) {
+#pragma unroll
+      for (int c = half * (HD / 2); c < (half + 1) * (HD / 2); c += 32) {
+        float a1[32], a2[32];
+        if (steps > 0) {
+          tmem_ld_32x32b_x32(tAcc1 + lane_base + c, a1);
+          tmem_ld_32x32b_x32(tAcc2 + lane_base + c, a2);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) a1[k] = a2[k] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) {
+          if (valid && c + k < p.dim) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              f[j] = p.scale * (PASS == kDq ? fmaf(-e, a1[k + j], a2[k + j]) : a2[k + j]);
+            *reinterpret_cast<uint4*>(p.g2.row(token, head) + c + k) = pack8(f);
+            if (PASS == kDkv) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) f[j] = a1[k + j];
+              *reinterpret_cast<uint4*>(p.g1.row(token, head) + c + k) = pack8(f);
+            }
+          }
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
-__global__ void __launch_bounds__(kThreads) attention_dkv_row_kernel(const SimpleBwdParams p) {
-  pdl_enter();
-  const AttentionArgs& a = p.a;
-  const int lane = threadIdx.x & 31, dim = a.d.dim;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = item / a.d.hk;
-  const int hk = static_cast<int>(item % a.d.hk), group = a.d.hq / a.d.hk;
-  if (t >= a.d.Tk) return;
-  const int s = sequence_of(a.k_starts, a.d.sequences, a.d.Tk, t);
-  if (s < 0) return;
-  int32_t q0, nq, k0, nk;
-  sequence_bounds(a.q_starts, a.d.Tq, s, q0, nq);
-  sequence_bounds(a.k_starts, a.d.Tk, s, k0, nk);
-  const int64_t first = a.d.causal ? max(static_cast<int64_t>(0), t - k0 - (nk - nq)) : 0;
-  float gk[4] = {}, gv[4] = {};
-  for (int h = hk * group; h < (hk + 1) * group; ++h)
-    for (int64_t i0 = first; i0 < nq; i0 += 32) {
-      float w = 0.0f, ds = 0.0f;
-      if (i0 + lane < nq) {
-        const int64_t q = q0 + i0 + lane;
-        w = __expf(a.d.scale * dot(a.q.row(q, h), a.k.row(t, hk), dim) - a.lse[h * a.d.Tq + q]);
-        ds = w * (dot(a.dout.row(q, h), a.v.row(t, hk), dim) - p.delta[h * a.d.Tq + q]);
-      }
-      for (int j = 0; j < 32 && i0 + j < nq; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, w, j), dj = __shfl_sync(0xffffffffu, ds, j);
-        for (int i = 0; i < 4; ++i)
-          if (i * 32 + lane < dim) {
-            gv[i] = fmaf(wj, __bfloat162float(a.dout.row(q0 + i0 + j, h)[i * 32 + lane]), gv[i]);
-            gk[i] = fmaf(dj, __bfloat162float(a.q.row(q0 + i0 + j, h)[i * 32 + lane]), gk[i]);
-          }
-      }
-    }
-  for (int i = 0; i < 4; ++i)
-    if (i * 32 + lane < dim) {
-      a.dk.row(t, hk)[i * 32 + lane] = __float2bfloat16_rn(gk[i] * a.d.scale);
-      a.dv.row(t, hk)[i * 32 + lane] = __float2bfloat16_rn(gv[i]);
-    }
+template <int HD, int PASS>
+cudaError_t launch_pass(const BwdParams& p, int64_t tiles, cudaStream_t stream) {
+  using Cfg = BwdCfg<HD>;
+  const auto kern = attention_bwd_kernel<HD, PASS>;
+  static std::atomic<bool> ready[64];    // per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.heads), 1, 1);
+  cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_bwd(const AttentionArgs& a, cudaStream_t stream) {
-  SimpleBwdParams p{a, reinterpret_cast<float*>(static_cast<char*>(a.ws) + 256)};
-  if (a.d.Tq > 0) {
-    const cudaError_t e = launch_k(attention_dq_row_kernel, (a.d.Tq * a.d.hq + 7) / 8, stream, p);
+  const boost_attention_desc& d = a.d;
+  BwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  CUtensorMap q, k, v, dout;
+  if (!heads_map(&q, a.q.at, a.ws, d.Tq, d.hq, d.dim, d.q_ts, d.q_hs, 1, kTile) ||
+      !heads_map(&k, a.k.at, a.ws, d.Tk, d.hk, d.dim, d.k_ts, d.k_hs, 1, kTile) ||
+      !heads_map(&v, a.v.at, a.ws, d.Tk, d.hk, d.dim, d.v_ts, d.v_hs, 1, kTile) ||
+      !heads_map(&dout, a.dout.at, a.ws, d.Tq, d.hq, d.dim, d.do_ts, d.do_hs, 1, kTile))
+    return cudaErrorInvalidValue;
+  p.lse = a.lse;
+  p.delta = reinterpret_cast<float*>(static_cast<char*>(a.ws) + 256);
+  p.q_starts = a.q_starts;
+  p.k_starts = a.k_starts;
+  p.Tq = d.Tq;
+  p.Tk = d.Tk;
+  p.group = d.hq / d.hk;
+  p.dim = d.dim;
+  p.sequences = d.sequences;
+  p.causal = d.causal;
+  p.scale = d.scale;
+  p.scale_log2 = d.scale * kLog2e;
+  p.err = static_cast<DeviceError*>(a.ws);
+  p.wait_limit_ns = wait_limit_ns();
+  if (d.Tq > 0) {
+    p.tmX0 = q;
+    p.tmX1 = dout;
+    p.tmY0 = k;
+    p.tmY1 = v;
+    p.o = a.o;
+    p.dout = a.dout;
+    p.g2 = a.dq;
+    p.heads = d.hq;
+    const int64_t tiles = most_tiles(d.Tq, kTile, d.sequences);
+    const cudaError_t e = d.dim <= 64 ? launch_pass<64, kDq>(p, tiles, stream)
+                                      : launch_pass<128, kDq>(p, tiles, stream);
     if (e != cudaSuccess) return e;
   }
-  if (a.d.Tk == 0) return cudaSuccess;
-  return launch_k(attention_dkv_row_kernel, (a.d.Tk * a.d.hk + 7) / 8, stream, p);
+  if (d.Tk == 0) return cudaSuccess;
+  p.tmX0 = k;
+  p.tmX1 = v;
+  p.tmY0 = q;
+  p.tmY1 = dout;
+  p.g1 = a.dv;
+  p.g2 = a.dk;
+  p.heads = d.hk;
+  const int64_t tiles = most_tiles(d.Tk, kTile, d.sequences);
+  return d.dim <= 64 ? launch_pass<64, kDkv>(p, tiles, stream)
+                     : launch_pass<128, kDkv>(p, tiles, stream);
 }
 
 }  // namespace boost_gb300

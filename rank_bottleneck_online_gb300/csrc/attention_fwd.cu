@@ -464,7 +464,7 @@ cudaError_t launch_fwd(const FwdParams& p, int64_t pairs, cudaStream_t stream) {
 size_t attention_workspace(const boost_attention_desc& d) {
   const size_t rows = static_cast<size_t>(d.hq) * d.Tq, splits = key_splits(d);
   const size_t fwd = splits > 1 ? 4 * splits * rows * (d.dim + 1) : 0;
-  return 256 + std::max(fwd, 8 * rows);
+  return 256 + std::max(fwd, 4 * rows);                  // (the backward keeps a value a row)
 }
 
 cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream) {
