@@ -20,7 +20,7 @@
 // result and bf16 dS.)
 //
 // Warp 0 loads the tiles through a ring, warp 1 issues the products, warp 2 fetches the second
-// pass's lse and delta, eight warps are the rows of a tile, two threads a row. The products of
+// pass's lse and delta, sixteen warps are the rows of a tile, four threads a row. The products of
 // one kind run while the threads work on the other's scores: acc1 += P B and the next S during dS,
 // acc2 += dS Y0 and the next dP during P.
 #include <math_constants.h>
@@ -60,10 +60,13 @@ struct BwdCfg {
   static constexpr int kStages = HD == 128 ? 4 : 8;      // Y0(0), Y1(0), Y0(1), ...
   static constexpr int kBars = 2 * kStages + 11;
   static constexpr int kStatOffset = (2 + kStages) * kTileBytes;
-  static constexpr int kStatBytes = 2 * 2 * 4 * kTile;   // two buffers of lse and delta
+  static constexpr int kParts = 4;                       // threads of a row
+  static constexpr int kCols = kTile / kParts;           // of its scores, each
+  static constexpr int kStatBytes = 4 * 4 * kTile;       // two buffers of lse and delta
   static constexpr int kBarOffset = kStatOffset + kStatBytes;
   static constexpr int kSmemBytes = 1024 + kBarOffset + 8 * kBars + 16;
-  static constexpr int kThreads = 384;
+  static constexpr int kWarps = 4 * kParts;              // that work on the scores
+  static constexpr int kThreads = 128 + 32 * kWarps;
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
@@ -112,12 +115,12 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
     mbar_init(x_bar, 1);
     mbar_init(s_bar, 1);
     mbar_init(d_bar, 1);
-    mbar_init(p_bar, 8);
-    mbar_init(ds_bar, 8);
+    mbar_init(p_bar, Cfg::kWarps);
+    mbar_init(ds_bar, Cfg::kWarps);
     mbar_init(acc_bar, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&stat_full[b], 1);
-      mbar_init(&stat_empty[b], 8);
+      mbar_init(&stat_empty[b], Cfg::kWarps);
     }
     mbar_init(done_bar, 1);
     fence_barrier_init();
@@ -209,19 +212,10 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
     // ----------------------------------------------------------- MMA issuer
     const uint32_t id_s = idesc_bf16_f32(kTile, kTile, 0, 0);
     const uint32_t id_acc = idesc_bf16_f32(kTile, 16 * ksteps, 0, 1);
-    const uint32_t x_at = smem_u32(sX), y_at = smem_u32(sY);
-    const uint64_t dk = desc_k_major(), dmn = desc_mn_major();
-    auto scores = [&](uint32_t d, uint32_t x, uint32_t y) {          // X Y^T
-      for (int kk = 0; kk < ksteps; ++kk)
-        tc_mma_bf16(d, dk | k_step(x, kk), dk | k_step(y, kk), id_s, kk > 0);
-    };
-    // the two halves of a row's 128 values lie 64 columns apart, over their own scores
-    auto sums = [&](uint32_t d, uint32_t a, uint32_t y, bool more) {  // acc += A Y
-#pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk)
-        tc_mma_bf16_ts(d, a + 8 * kk + (kk >= 4 ? 32 : 0), dmn | mn_step(y, kk), id_acc,
-                       more || kk > 0);
-    };
+    const uint64_t x0_desc = desc_k_major(smem_u32(sX));
+    const uint64_t x1_desc = desc_k_major(smem_u32(sX) + Cfg::kTileBytes);
+    const uint64_t yk_desc = desc_k_major(smem_u32(sY)), ymn_desc = desc_mn_major(smem_u32(sY));
+    auto slot = [&](int32_t u) { return u % Cfg::kStages * (Cfg::kTileBytes >> 4); };
     // Wait for tile `u` of the ring; rows behind the sequence become 0.
     auto take = [&](int32_t u, int32_t step) {
       const int s = u % Cfg::kStages;
@@ -232,19 +226,19 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
       tc_fence_after();
       return true;
     };
-    auto slot = [&](int32_t u) { return y_at + u % Cfg::kStages * Cfg::kTileBytes; };
     bool ok = steps > 0 && warp_wait_all(x_bar, 0, p.err, 62, p.wait_limit_ns) && take(0, 0);
     if (ok) {
       if (elect_one()) {
-        scores(tS, x_at, slot(0));
+        issue_scores<HD / 16>(tS, x0_desc, yk_desc, id_s, ksteps);
         tc_commit(s_bar);
       }
       __syncwarp();
       ok = take(1, 0);
     }
     if (ok) {
+      const uint64_t y = yk_desc + slot(1);
       if (elect_one()) {
-        scores(tD, x_at + Cfg::kTileBytes, slot(1));
+        issue_scores<HD / 16>(tD, x1_desc, y, id_s, ksteps);
         tc_commit(d_bar);
         if (PASS == kDq) tc_commit(&empty_bar[1]);
       }
@@ -256,8 +250,10 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
       ok = warp_wait_all(p_bar, i & 1, p.err, 64, p.wait_limit_ns);
       if (!ok) break;
       tc_fence_after();
+      const uint64_t b1 = ymn_desc + slot(PASS == kDq ? y0 : y1), b2 = ymn_desc + slot(y0);
+      const uint64_t next0 = yk_desc + slot(y0 + 2), next1 = yk_desc + slot(y1 + 2);
       if (elect_one()) {
-        sums(tAcc1, tS, slot(PASS == kDq ? y0 : y1), i > 0);
+        issue_sums<Cfg::kCols>(tAcc1, tS, b1, id_acc, i > 0);
         if (PASS == kDkv) tc_commit(&empty_bar[y1 % Cfg::kStages]);
       }
       __syncwarp();
@@ -265,7 +261,7 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
         ok = take(y0 + 2, i + 1);
         if (!ok) break;
         if (elect_one()) {
-          scores(tS, x_at, slot(y0 + 2));
+          issue_scores<HD / 16>(tS, x0_desc, next0, id_s, ksteps);
           tc_commit(s_bar);
         }
         __syncwarp();
@@ -274,7 +270,7 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
-        sums(tAcc2, tD, slot(y0), i > 0);
+        issue_sums<Cfg::kCols>(tAcc2, tD, b2, id_acc, i > 0);
         tc_commit(more ? &empty_bar[y0 % Cfg::kStages] : acc_bar);
       }
       __syncwarp();
@@ -282,7 +278,7 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
         ok = take(y1 + 2, i + 1);
         if (!ok) break;
         if (elect_one()) {
-          scores(tD, x_at + Cfg::kTileBytes, slot(y1 + 2));
+          issue_scores<HD / 16>(tD, x1_desc, next1, id_s, ksteps);
           tc_commit(d_bar);
           if (PASS == kDq) tc_commit(&empty_bar[(y1 + 2) % Cfg::kStages]);
         }
@@ -295,49 +291,65 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
     warp_wait_all(done_bar, 0, nullptr, 68, p.wait_limit_ns);
   } else if (warp == 2 && PASS == kDkv) {
     // ----------------------------------------------- lse and delta of the queries
+    // (loaded a step ahead, all at once: the threads wait for these as for the scores)
+    int32_t tile = first, h = y_head;
+    float l[4], d[4];
+    auto fetch = [&]() {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int32_t q = tile * kTile + k * 32 + lane;
+        const int64_t t = static_cast<int64_t>(h) * p.Tq + at.q0 + q;
+        l[k] = q < at.nq ? p.lse[t] : -CUDART_INF_F;
+        d[k] = q < at.nq ? p.delta[t] : 0.0f;
+      }
+      if (++tile == first + count) {
+        tile = first;
+        ++h;
+      }
+    };
+    if (steps > 0) fetch();
     for (int32_t i = 0; i < steps; ++i) {
       const int b = i & 1;
       if (!warp_wait_all(&stat_empty[b], (i >> 1 & 1) ^ 1, p.err, 66, p.wait_limit_ns)) break;
-      const int32_t q = (first + i % count) * kTile, h = y_head + i / count;
 #pragma unroll
-      for (int k = 0; k < kTile; k += 32) {
+      for (int k = 0; k < 4; ++k) {
         // (a query that is none, or sees no key, has no probabilities)
-        float l = CUDART_INF_F, d = 0.0f;
-        if (q + k + lane < at.nq) {
-          const int64_t t = static_cast<int64_t>(h) * p.Tq + at.q0 + q + k + lane;
-          const float v = p.lse[t];
-          if (v != -CUDART_INF_F) {
-            l = v * kLog2e;
-            d = p.delta[t];
-          }
-        }
-        stat[b * 2 * kTile + k + lane] = l;
-        stat[b * 2 * kTile + kTile + k + lane] = d;
+        const bool none = l[k] == -CUDART_INF_F;
+        stat[b * 2 * kTile + k * 32 + lane] = none ? CUDART_INF_F : l[k] * kLog2e;
+        stat[b * 2 * kTile + kTile + k * 32 + lane] = none ? 0.0f : d[k];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&stat_full[b]);
+      if (i + 1 < steps) fetch();
     }
   } else if (warp >= 4 && at.tiles > 0) {
     // ------------------------------------------------------ probabilities, dS
-    const int half = (warp >> 2) - 1, quarter = warp & 3, row = quarter * 32 + lane;
+    constexpr int kCols = Cfg::kCols, kDims = HD / Cfg::kParts;
+    const int part = (warp >> 2) - 1, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t s_at = tS + lane_base + 64 * half, d_at = tD + lane_base + 64 * half;
+    const uint32_t s_at = tS + lane_base + kCols * part, d_at = tD + lane_base + kCols * part;
     const int32_t x = x0 + row;                           // in the sequence
     const bool valid = x < nx;
     const int64_t token = x_row + static_cast<int64_t>(row);
+    // sum over a row's parts, in order
+    auto over_parts = [&](float v) {
+      stat[part * kTile + row] = v;
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * Cfg::kWarps) : "memory");
+      v = stat[row];
+#pragma unroll
+      for (int i = 1; i < Cfg::kParts; ++i) v += stat[i * kTile + row];
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * Cfg::kWarps) : "memory");
+      return v;
+    };
     float lse = 0.0f, delta = 0.0f, e = 0.0f;             // kDq: of this row; what delta lacks
     if (PASS == kDq) {
       if (valid) {
         lse = p.lse[head * p.Tq + token] * kLog2e;
-        const int32_t c0 = half * (HD / 2);
+        const int32_t c0 = part * kDims;
         delta = dot_row(p.dout.row(token, head) + c0, p.o.row(token, head) + c0,
-                        min(max(p.dim - c0, 0), HD / 2));
+                        min(max(p.dim - c0, 0), kDims));
       }
-      // (the two halves of a row, in order)
-      stat[half * kTile + row] = delta;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      delta = stat[row] + stat[kTile + row];
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      delta = over_parts(delta);
     }
     // kDq: keys that this row sees; kDkv: the first query that sees this row
     const int32_t bound = PASS == kDq ? (p.causal ? min(at.nk, x + off + 1) : at.nk)
@@ -345,26 +357,25 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
     bool ok = true;
     int32_t tile = first;
     for (int32_t i = 0; i < steps; ++i) {
-      const float* st = stat + (i & 1) * 2 * kTile + half * 64;
+      const float* st = stat + (i & 1) * 2 * kTile + part * kCols;
       if (PASS == kDkv) ok = warp_wait_all(&stat_full[i & 1], i >> 1 & 1, p.err, 69, p.wait_limit_ns);
       ok = ok && warp_wait_all(s_bar, i & 1, p.err, 70, p.wait_limit_ns);
       if (!ok) break;
       tc_fence_after();
-      float s[64];
-      tmem_ld_32x32b_x32(s_at, *reinterpret_cast<float(*)[32]>(s));
-      tmem_ld_32x32b_x32(s_at + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+      float s[kCols];
+      tmem_ld_32x32b_x32(s_at, s);
       tmem_ld_wait();
-      const int32_t lim = bound - tile * kTile - 64 * half;   // of this half's columns
+      const int32_t lim = bound - tile * kTile - kCols * part;   // of this part's columns
       if (PASS == kDq) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] = exp2_fast(fmaf(s[c], p.scale_log2, -lse));
-        if (__any_sync(0xffffffffu, lim < 64)) {
+        for (int c = 0; c < kCols; ++c) s[c] = exp2_fast(fmaf(s[c], p.scale_log2, -lse));
+        if (__any_sync(0xffffffffu, lim < kCols)) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) s[c] = c < lim ? s[c] : 0.0f;
+          for (int c = 0; c < kCols; ++c) s[c] = c < lim ? s[c] : 0.0f;
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
+        for (int c = 0; c < kCols; c += 4) {
           const float4 l = *reinterpret_cast<const float4*>(st + c);
           s[c] = exp2_fast(fmaf(s[c], p.scale_log2, -l.x));
           s[c + 1] = exp2_fast(fmaf(s[c + 1], p.scale_log2, -l.y));
@@ -373,13 +384,13 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
         }
         if (__any_sync(0xffffffffu, lim > 0)) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) s[c] = c >= lim ? s[c] : 0.0f;
+          for (int c = 0; c < kCols; ++c) s[c] = c >= lim ? s[c] : 0.0f;
         }
       }
-      uint32_t w[32];
+      uint32_t w[kCols / 2];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
-      tmem_st_32x32b_x32(s_at, w);
+      for (int c = 0; c < kCols / 2; ++c) w[c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
+      tmem_st_32x32b_x16(s_at, w);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -388,21 +399,20 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
       ok = warp_wait_all(d_bar, i & 1, p.err, 71, p.wait_limit_ns);
       if (!ok) break;
       tc_fence_after();
-      float d[64];
-      tmem_ld_32x32b_x32(d_at, *reinterpret_cast<float(*)[32]>(d));
-      tmem_ld_32x32b_x32(d_at + 32, *reinterpret_cast<float(*)[32]>(d + 32));
+      float d[kCols];
+      tmem_ld_32x32b_x32(d_at, d);
       tmem_ld_wait();
       if (PASS == kDq) {
         float sum[4] = {};
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
+        for (int c = 0; c < kCols; ++c) {
           d[c] = s[c] * (d[c] - delta);
           sum[c & 3] += d[c];
         }
         e += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       } else {
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
+        for (int c = 0; c < kCols; c += 4) {
           const float4 l = *reinterpret_cast<const float4*>(st + kTile + c);
           d[c] = s[c] * (d[c] - l.x);
           d[c + 1] = s[c + 1] * (d[c + 1] - l.y);
@@ -411,8 +421,8 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
         }
       }
 #pragma unroll
-      for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(d[2 * c], d[2 * c + 1]);
-      tmem_st_32x32b_x32(d_at, w);
+      for (int c = 0; c < kCols / 2; ++c) w[c] = pack_bf16x2(d[2 * c], d[2 * c + 1]);
+      tmem_st_32x32b_x16(d_at, w);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -425,25 +435,23 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
     if (ok && steps > 0) ok = warp_wait_all(acc_bar, 0, p.err, 72, p.wait_limit_ns);
     tc_fence_after();
     if (PASS == kDq) {
-      stat[half * kTile + row] = e;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      e = stat[row] + stat[kTile + row];
-      if (valid && half == 0) p.delta[head * p.Tq + token] = delta + e;
+      e = over_parts(e);
+      if (valid && part == 0) p.delta[head * p.Tq + token] = delta + e;
     }
     if (ok) {
 #pragma unroll
-      for (int c = half * (HD / 2); c < (half + 1) * (HD / 2); c += 32) {
-        float a1[32], a2[32];
+      for (int c = part * kDims; c < (part + 1) * kDims; c += 16) {
+        float a1[16], a2[16];
         if (steps > 0) {
-          tmem_ld_32x32b_x32(tAcc1 + lane_base + c, a1);
-          tmem_ld_32x32b_x32(tAcc2 + lane_base + c, a2);
+          tmem_ld_32x32b_x16(tAcc1 + lane_base + c, a1);
+          tmem_ld_32x32b_x16(tAcc2 + lane_base + c, a2);
           tmem_ld_wait();
         } else {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) a1[k] = a2[k] = 0.0f;
+          for (int k = 0; k < 16; ++k) a1[k] = a2[k] = 0.0f;
         }
 #pragma unroll
-        for (int k = 0; k < 32; k += 8) {
+        for (int k = 0; k < 16; k += 8) {
           if (valid && c + k < p.dim) {
             float f[8];
 #pragma unroll

@@ -177,17 +177,10 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     // ----------------------------------------------------------- MMA issuer
     const uint32_t id_s = idesc_bf16_f32(kTile, kTile, 0, 0);
     const uint32_t id_o = idesc_bf16_f32(kTile, 16 * ksteps, 0, 1);
-    const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV);
-    const uint64_t dk = desc_k_major(), dmn = desc_mn_major();
-    auto scores = [&](int x, uint32_t k) {               // S_x = Q_x K^T
-      for (int kk = 0; kk < ksteps; ++kk)
-        tc_mma_bf16(tS[x], dk | k_step(q0 + x * Cfg::kTileBytes, kk), dk | k_step(k, kk), id_s, kk > 0);
-    };
-    auto values = [&](int x, uint32_t v, bool more) {    // O_x += P_x V
-#pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk)
-        tc_mma_bf16_ts(tO[x], tS[x] + 8 * kk, dmn | mn_step(v, kk), id_o, more || kk > 0);
-    };
+    const uint64_t q_desc[2] = {desc_k_major(smem_u32(sQ)),
+                                desc_k_major(smem_u32(sQ) + Cfg::kTileBytes)};
+    const uint64_t k_desc = desc_k_major(smem_u32(sKV)), v_desc = desc_mn_major(smem_u32(sKV));
+    constexpr uint32_t kStep = Cfg::kTileBytes >> 4;
     int stage = 0;
     uint32_t phase = 0;
     auto next = [&]() {
@@ -201,9 +194,10 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     if (ok) {
       tc_fence_after();
       if (elect_one()) {
+#pragma unroll
         for (int x = 0; x < 2; ++x)
           if (n[x] > 0) {
-            scores(x, kv0);
+            issue_scores<HD / 16>(tS[x], q_desc[x], k_desc, id_s, ksteps);
             tc_commit(&s_bar[x]);
           }
         tc_commit(&empty_bar[0]);
@@ -228,10 +222,11 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
             break;
           }
           tc_fence_after();
+          const uint64_t vd = v_desc + v_stage * kStep, kd = k_desc + stage * kStep;
           if (elect_one()) {
-            values(x, kv0 + v_stage * Cfg::kTileBytes, j > 0);
+            issue_sums<kTile>(tO[x], tS[x], vd, id_o, j > 0);          // O_x += P_x V
             if (j + 1 < n[x]) {
-              scores(x, kv0 + stage * Cfg::kTileBytes);
+              issue_scores<HD / 16>(tS[x], q_desc[x], kd, id_s, ksteps);
               tc_commit(&s_bar[x]);
             } else {
               tc_commit(&o_bar[x]);

@@ -77,14 +77,39 @@ __device__ __forceinline__ bool warp_wait_all(uint64_t* bar, uint32_t parity, De
 // the next 64 values are the next box.
 constexpr int kBoxBytes = kTile * 128;
 
-__device__ __forceinline__ uint64_t desc_k_major() { return desc_hi_sw128(16u, 1024u); }
-__device__ __forceinline__ uint64_t desc_mn_major() { return desc_hi_sw128(kBoxBytes, 1024u); }
-
-// Start addresses (>> 4) of K step kk of a tile at shared address `base`.
-__device__ __forceinline__ uint32_t k_step(uint32_t base, int kk) {
-  return (base + (kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+//
+// The products' issuers are converged warps that form the descriptors, an elected lane issues:
+// with constant steps behind a base in uniform registers an MMA costs a few instructions. (With
+// the steps' addresses formed in the elected lane's own loop, an MMA of 64 cycles took about 125.)
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t base) {
+  return desc_hi_sw128(16u, 1024u) | ((base >> 4) & 0x3FFFu);
 }
-__device__ __forceinline__ uint32_t mn_step(uint32_t base, int kk) { return (base + kk * 2048) >> 4; }
+__device__ __forceinline__ uint64_t desc_mn_major(uint32_t base) {
+  return desc_hi_sw128(kBoxBytes, 1024u) | ((base >> 4) & 0x3FFFu);
+}
+
+// D = X Y^T over `steps` steps of 16 values (MAX at most), both K-major.
+template <int MAX>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint64_t x, uint64_t y, uint32_t idesc,
+                                             int steps) {
+#pragma unroll
+  for (int kk = 0; kk < MAX; ++kk) {
+    constexpr uint32_t kBox = kBoxBytes >> 4;
+    const uint32_t at = (kk >> 2) * kBox + (kk & 3) * 2;
+    if (kk < steps) tc_mma_bf16(d, x + at, y + at, idesc, kk > 0);
+  }
+}
+
+// D (+)= A Y over the tile's 128 rows, A in TMEM as parts of `COLS` values that lie COLS columns
+// apart, Y MN-major.
+template <int COLS>
+__device__ __forceinline__ void issue_sums(uint32_t d, uint32_t a, uint64_t y, uint32_t idesc,
+                                           bool more) {
+#pragma unroll
+  for (int kk = 0; kk < kTile / 16; ++kk)
+    tc_mma_bf16_ts(d, a + 16 * kk / COLS * COLS + 16 * kk % COLS / 2, y + 128 * kk, idesc,
+                   kk > 0 ? 1u : more);
+}
 
 // Zero rows [from, 128) of a tile of `boxes` boxes that a TMA load has filled, by a whole warp:
 // rows of another sequence may hold NaN, which a probability of 0 would not hide.
