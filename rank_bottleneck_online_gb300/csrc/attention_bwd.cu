@@ -19,7 +19,14 @@
 // gradients of 77 tokens were off by 0.0030, relative to all, with it by the 0.002 of a bf16
 // result and bf16 dS.)
 //
-// Warp 0 loads the tiles through a ring, warp 1 issues the products, warp 2 fetches the second
+// A tile of 128 x 128 products takes 512 cycles of the tensor core, and reads 128 bytes a cycle of
+// shared memory while both operands lie there, which is all that there is: the loads' writes cost
+// time. So with heads of more than 64 values a pair of CTAs works on 256 rows: each has half of
+// the other side's tile, once split along its rows (for S and dP) and once along its values (for
+// the sums), and half the reads. Short sequences, whose rows would leave a CTA of the pair idle,
+// take single CTAs.
+//
+// Warp 0 loads the tiles, each through two buffers, warp 1 issues the products, warp 2 fetches the second
 // pass's lse and delta, sixteen warps are the rows of a tile, four threads a row. The products of
 // one kind run while the threads work on the other's scores: acc1 += P B and the next S during dS,
 // acc2 += dS Y0 and the next dP during P.
@@ -39,7 +46,7 @@ namespace {
 enum Pass : int { kDq = 0, kDkv = 1 };
 
 struct BwdParams {
-  CUtensorMap tmX0, tmX1, tmY0, tmY1;    // boxes of 64 values x 128 rows of one head
+  CUtensorMap tmX0, tmX1, tmY0, tmY1;    // boxes of 64 values x 64 rows of one head
   HeadsIn o, dout;                       // kDq
   HeadsOut g1, g2;                       // kDq: -, dq; kDkv: dv, dk
   const float* lse;                      // [hq, Tq]
@@ -53,13 +60,18 @@ struct BwdParams {
   uint64_t wait_limit_ns;
 };
 
-template <int HD>
+// Tiles of the other side, as first met in a step: Y0 and Y1 as K-major operands, Y1 and Y0 as
+// MN-major ones. A single CTA has both in one.
+enum Kind : int { kY0k = 0, kY1k, kY1m, kY0m, kKinds };
+
+template <int HD, int CG>
 struct BwdCfg {
   static constexpr int kBoxes = HD / 64;
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
-  static constexpr int kStages = HD == 128 ? 4 : 8;      // Y0(0), Y1(0), Y0(1), ...
-  static constexpr int kBars = 2 * kStages + 11;
-  static constexpr int kStatOffset = (2 + kStages) * kTileBytes;
+  static constexpr int kSlotBytes = kTileBytes / CG;     // of a loaded tile
+  static constexpr int kSlotKinds = CG == 2 ? 4 : 2;
+  static constexpr int kBars = 4 * kSlotKinds + 12;
+  static constexpr int kStatOffset = 2 * kTileBytes + 2 * kSlotKinds * kSlotBytes;
   static constexpr int kParts = 4;                       // threads of a row
   static constexpr int kCols = kTile / kParts;           // of its scores, each
   static constexpr int kStatBytes = 4 * 4 * kTile;       // two buffers of lse and delta
@@ -68,6 +80,7 @@ struct BwdCfg {
   static constexpr int kWarps = 4 * kParts;              // that work on the scores
   static constexpr int kThreads = 128 + 32 * kWarps;
   static_assert(kSmemBytes <= 232448, "shared memory");
+  static_assert(CG == 1 || HD == 128, "a half of a tile's values is a box");
 };
 
 // Sum of a row's products over `n` values (a multiple of 8).
@@ -83,19 +96,20 @@ __device__ __forceinline__ float dot_row(const __nv_bfloat16* a, const __nv_bflo
   return s;
 }
 
-template <int HD, int PASS>
-__global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
+template <int HD, int CG, int PASS>
+__global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
     attention_bwd_kernel(const __grid_constant__ BwdParams p) {
-  using Cfg = BwdCfg<HD>;
+  using Cfg = BwdCfg<HD, CG>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sX = smem;                                   // X0, X1
-  uint8_t* sY = smem + 2 * Cfg::kTileBytes;
+  uint8_t* sY = smem + 2 * Cfg::kTileBytes;             // two slots of each kind
   float* stat = reinterpret_cast<float*>(smem + Cfg::kStatOffset);
+  // (full, p and ds: the even CTA's of a pair, for both; the others: each CTA's own)
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOffset);
-  uint64_t* empty_bar = full_bar + Cfg::kStages;
-  uint64_t* x_bar = empty_bar + Cfg::kStages;
+  uint64_t* empty_bar = full_bar + 2 * Cfg::kSlotKinds;
+  uint64_t* x_bar = empty_bar + 2 * Cfg::kSlotKinds;
   uint64_t* s_bar = x_bar + 1;                          // S is complete
   uint64_t* d_bar = s_bar + 1;                          // dP is complete
   uint64_t* p_bar = d_bar + 1;                          // P is written
@@ -103,25 +117,28 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
   uint64_t* acc_bar = ds_bar + 1;                       // the sums are complete
   uint64_t* stat_full = acc_bar + 1;                    // [2]
   uint64_t* stat_empty = stat_full + 2;                 // [2]
-  uint64_t* done_bar = stat_empty + 2;
+  uint64_t* tail_bar = stat_empty + 2;                  // a tile that ends inside
+  uint64_t* done_bar = tail_bar + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? static_cast<int>(cluster_ctarank()) : 0;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < Cfg::kStages; ++s) {
-      mbar_init(&full_bar[s], 1);
+    for (int s = 0; s < 2 * Cfg::kSlotKinds; ++s) {
+      mbar_init(&full_bar[s], CG);
       mbar_init(&empty_bar[s], 1);
     }
-    mbar_init(x_bar, 1);
+    mbar_init(x_bar, CG);
     mbar_init(s_bar, 1);
     mbar_init(d_bar, 1);
-    mbar_init(p_bar, Cfg::kWarps);
-    mbar_init(ds_bar, Cfg::kWarps);
+    mbar_init(p_bar, CG * Cfg::kWarps);
+    mbar_init(ds_bar, CG * Cfg::kWarps);
     mbar_init(acc_bar, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&stat_full[b], 1);
       mbar_init(&stat_empty[b], Cfg::kWarps);
     }
+    mbar_init(tail_bar, 1);
     mbar_init(done_bar, 1);
     fence_barrier_init();
   }
@@ -132,32 +149,43 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
     tma_prefetch_desc(&p.tmY1);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_holder, 512);
-    tmem_relinquish();
+    if constexpr (CG == 2) {
+      tmem_alloc_pair(tmem_holder, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_holder, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (CG == 2) cluster_sync(); else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const uint32_t tS = tmem, tD = tmem + 128, tAcc1 = tmem + 256, tAcc2 = tmem + 256 + HD;
+  // the address of the even CTA's barrier
+  auto lead = [&](uint64_t* bar) {
+    return CG == 2 ? mapa_shared(smem_u32(bar), 0) : smem_u32(bar);
+  };
   griddep_wait();
   griddep_launch_dependents();
 
-  // This CTA's tile of queries (kDq, longest rows first) or keys, and the tiles [first, first +
-  // count) of the other side that its rows see; kDkv has those once for each head of the group.
-  const int32_t head = static_cast<int32_t>(blockIdx.x) % p.heads;
-  Place at = find_tile(p.q_starts, p.k_starts, p.Tq, p.Tk, p.sequences,
-                       static_cast<int32_t>(blockIdx.x) / p.heads, kTile, PASS == kDkv);
+  // This CTA's (pair's) tile of queries (kDq, longest rows first) or keys, and the tiles [first,
+  // first + count) of the other side that its rows see; kDkv has those once for each head of the
+  // group.
+  const int32_t work = static_cast<int32_t>(blockIdx.x) / CG, head = work % p.heads;
+  Place at = find_tile(p.q_starts, p.k_starts, p.Tq, p.Tk, p.sequences, work / p.heads, CG * kTile,
+                       PASS == kDkv);
   const int32_t off = at.nk - at.nq;                     // keys before the first query
-  const int32_t x0 = (PASS == kDq ? at.tiles - 1 - at.tile : at.tile) * kTile;
+  const int32_t pair0 = (PASS == kDq ? at.tiles - 1 - at.tile : at.tile) * (CG * kTile);
+  const int32_t x0 = pair0 + rank * kTile;
   const int32_t nx = PASS == kDq ? at.nq : at.nk, ny = PASS == kDq ? at.nk : at.nq;
   int32_t first = 0, count = 0;
   if (at.tiles > 0) {
     if (PASS == kDq) {
-      const int32_t keys = p.causal ? min(at.nk, min(x0 + kTile, at.nq) + off) : at.nk;
+      const int32_t keys = p.causal ? min(at.nk, min(pair0 + CG * kTile, at.nq) + off) : at.nk;
       count = keys > 0 ? (keys + kTile - 1) / kTile : 0;
     } else {
-      first = p.causal ? max(x0 - off, 0) / kTile : 0;
+      first = p.causal ? max(pair0 - off, 0) / kTile : 0;
       count = max((at.nq + kTile - 1) / kTile - first, 0);
     }
   }
@@ -166,129 +194,207 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
   const int32_t y_row = PASS == kDq ? at.k0 : at.q0;
   const int32_t y_head = PASS == kDq ? head / p.group : head * p.group;
   const int ksteps = (p.dim + 15) / 16;
+  const int32_t width = CG == 2 ? (p.dim + 31) / 32 * 32 : 16 * ksteps;   // columns of the sums
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    uint32_t armed = 0, parities = 0;
+    constexpr int kHalf = kBoxBytes / 2;                 // a box of 64 rows
+    constexpr uint32_t kTailBytes =
+        (PASS == kDq && CG == 2 ? Cfg::kSlotKinds - 1 : Cfg::kSlotKinds) * Cfg::kSlotBytes;
     if (steps > 0) {
       if (elect_one()) {
-        mbar_arrive_expect_tx(x_bar, 2 * Cfg::kTileBytes);
-        for (int b = 0; b < Cfg::kBoxes; ++b) {
-          tma_load_3d(sX + b * kBoxBytes, &p.tmX0, x_bar, 64 * b, head, x_row);
-          tma_load_3d(sX + Cfg::kTileBytes + b * kBoxBytes, &p.tmX1, x_bar, 64 * b, head, x_row);
+        const uint32_t bar = lead(x_bar);
+        if constexpr (CG == 2) mbar_arrive_expect_tx_cluster(bar, 2 * Cfg::kTileBytes);
+        else mbar_arrive_expect_tx(x_bar, 2 * Cfg::kTileBytes);
+        for (int b = 0; b < 2 * Cfg::kBoxes; ++b) {
+          uint8_t* dst = sX + b * kHalf;
+          const int32_t col = 64 * (b >> 1), row = x_row + (b & 1) * (kTile / 2);
+          if constexpr (CG == 2) {
+            tma_load_3d_pair(dst, &p.tmX0, bar, col, head, row);
+            tma_load_3d_pair(dst + Cfg::kTileBytes, &p.tmX1, bar, col, head, row);
+          } else {
+            tma_load_3d(dst, &p.tmX0, x_bar, col, head, row);
+            tma_load_3d(dst + Cfg::kTileBytes, &p.tmX1, x_bar, col, head, row);
+          }
         }
       }
       __syncwarp();
-      int stage = 0;
-      uint32_t phase = 0;
       int32_t tile = first, h = y_head;
-      for (int32_t i = 0; i < 2 * steps; ++i) {
-        if (!warp_wait_all(&empty_bar[stage], phase ^ 1u, p.err, 61, p.wait_limit_ns)) break;
-        armed |= 1u << stage;
-        parities = (parities & ~(1u << stage)) | (phase << stage);
-        if (elect_one()) {
-          mbar_arrive_expect_tx(&full_bar[stage], Cfg::kTileBytes);
-          for (int b = 0; b < Cfg::kBoxes; ++b)
-            tma_load_3d(sY + stage * Cfg::kTileBytes + b * kBoxBytes, i & 1 ? &p.tmY1 : &p.tmY0,
-                        &full_bar[stage], 64 * b, h, y_row + tile * kTile);
+      int32_t last[Cfg::kSlotKinds];                     // step of the last load
+      uint32_t tails = 0;
+      bool ok = true;
+#pragma unroll
+      for (int kind = 0; kind < Cfg::kSlotKinds; ++kind) last[kind] = -1;
+      for (int32_t i = 0; i < steps && ok; ++i) {
+        const int32_t left = ny - tile * kTile, row = y_row + tile * kTile;
+        // a tile in which the sequence ends lands on this CTA's own barrier first
+        const bool tail = left < kTile;
+#pragma unroll
+        for (int kind = 0; kind < Cfg::kSlotKinds; ++kind) {
+          if (PASS == kDq && kind == kY1m) continue;
+          const int s = 2 * kind + (i & 1);
+          ok = ok && warp_wait_all(&empty_bar[s], (i >> 1 & 1) ^ 1, p.err, 61, p.wait_limit_ns);
+          if (!ok) break;
+          last[kind] = i;
+          const CUtensorMap* map = kind == kY0k || kind == kY0m ? &p.tmY0 : &p.tmY1;
+          uint8_t* dst = sY + s * Cfg::kSlotBytes;
+          if (elect_one()) {
+            if constexpr (CG == 2) {
+              const uint32_t bar = tail ? mapa_shared(smem_u32(tail_bar), rank) : lead(&full_bar[s]);
+              const uint32_t bytes = tail ? (kind == 0 ? kTailBytes : 0) : Cfg::kSlotBytes;
+              if (bytes > 0) mbar_arrive_expect_tx_cluster(bar, bytes);
+              for (int b = 0; b < 2; ++b) {
+                if (kind == kY0k || kind == kY1k)        // half of the rows
+                  tma_load_3d_pair(dst + b * kHalf, map, bar, 64 * b, h, row + rank * (kTile / 2));
+                else                                     // half of the values
+                  tma_load_3d_pair(dst + b * kHalf, map, bar, rank * (width / 2), h,
+                                   row + b * (kTile / 2));
+              }
+            } else {
+              uint64_t* bar = tail ? tail_bar : &full_bar[s];
+              const uint32_t bytes = tail ? (kind == 0 ? kTailBytes : 0) : Cfg::kSlotBytes;
+              if (bytes > 0) mbar_arrive_expect_tx(bar, bytes);
+              for (int b = 0; b < 2 * Cfg::kBoxes; ++b)
+                tma_load_3d(dst + b * kHalf, map, bar, 64 * (b >> 1), h,
+                            row + (b & 1) * (kTile / 2));
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        if ((i & 1) && ++tile == first + count) {
+        if (ok && tail) {                                // its rows behind the sequence become 0
+          ok = warp_wait_all(tail_bar, tails++ & 1, p.err, 67, p.wait_limit_ns);
+#pragma unroll
+          for (int kind = 0; kind < Cfg::kSlotKinds; ++kind) {
+            if (PASS == kDq && kind == kY1m) continue;
+            const int s = 2 * kind + (i & 1);
+            uint8_t* dst = sY + s * Cfg::kSlotBytes;
+            if (CG == 2 && (kind == kY0k || kind == kY1k))
+              zero_rows(dst, 2, kTile / 2, min(max(left - rank * (kTile / 2), 0), kTile / 2), lane);
+            else
+              zero_rows(dst, Cfg::kBoxes / CG, kTile, left, lane);
+            if (elect_one()) {
+              if constexpr (CG == 2) mbar_arrive_release(lead(&full_bar[s]));
+              else mbar_arrive(&full_bar[s]);
+            }
+            __syncwarp();
+          }
+        }
+        if (++tile == first + count) {
           tile = first;
           ++h;
         }
-        if (++stage == Cfg::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
-      // the copies started here have landed before the CTA exits
-      for (int s = 0; s < Cfg::kStages; ++s)
-        if (armed >> s & 1u)
-          warp_wait_all(&full_bar[s], parities >> s & 1u, nullptr, 67, p.wait_limit_ns);
-      warp_wait_all(x_bar, 0, nullptr, 67, p.wait_limit_ns);
+      // the copies started here have landed before the CTA (or the pair) exits
+      if (rank == 0) {
+        warp_wait_all(x_bar, 0, nullptr, 67, p.wait_limit_ns);
+#pragma unroll
+        for (int kind = 0; kind < Cfg::kSlotKinds; ++kind)
+          for (int32_t i = max(last[kind] - 1, 0); i <= last[kind]; ++i)
+            warp_wait_all(&full_bar[2 * kind + (i & 1)], i >> 1 & 1, nullptr, 67, p.wait_limit_ns);
+      }
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
-    const uint32_t id_s = idesc_bf16_f32(kTile, kTile, 0, 0);
-    const uint32_t id_acc = idesc_bf16_f32(kTile, 16 * ksteps, 0, 1);
-    const uint64_t x0_desc = desc_k_major(smem_u32(sX));
-    const uint64_t x1_desc = desc_k_major(smem_u32(sX) + Cfg::kTileBytes);
-    const uint64_t yk_desc = desc_k_major(smem_u32(sY)), ymn_desc = desc_mn_major(smem_u32(sY));
-    auto slot = [&](int32_t u) { return u % Cfg::kStages * (Cfg::kTileBytes >> 4); };
-    // Wait for tile `u` of the ring; rows behind the sequence become 0.
-    auto take = [&](int32_t u, int32_t step) {
-      const int s = u % Cfg::kStages;
-      if (!warp_wait_all(&full_bar[s], u / Cfg::kStages & 1, p.err, 63, p.wait_limit_ns))
-        return false;
-      const int32_t left = ny - (first + step % max(count, 1)) * kTile;
-      if (left < kTile) zero_rows(sY + s * Cfg::kTileBytes, Cfg::kBoxes, left, lane);
-      tc_fence_after();
-      return true;
-    };
-    bool ok = steps > 0 && warp_wait_all(x_bar, 0, p.err, 62, p.wait_limit_ns) && take(0, 0);
-    if (ok) {
-      if (elect_one()) {
-        issue_scores<HD / 16>(tS, x0_desc, yk_desc, id_s, ksteps);
-        tc_commit(s_bar);
-      }
-      __syncwarp();
-      ok = take(1, 0);
-    }
-    if (ok) {
-      const uint64_t y = yk_desc + slot(1);
-      if (elect_one()) {
-        issue_scores<HD / 16>(tD, x1_desc, y, id_s, ksteps);
-        tc_commit(d_bar);
-        if (PASS == kDq) tc_commit(&empty_bar[1]);
-      }
-      __syncwarp();
-    }
-    for (int32_t i = 0; i < steps && ok; ++i) {
-      const int32_t y0 = 2 * i, y1 = 2 * i + 1;
-      const bool more = i + 1 < steps;
-      ok = warp_wait_all(p_bar, i & 1, p.err, 64, p.wait_limit_ns);
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t b1 = ymn_desc + slot(PASS == kDq ? y0 : y1), b2 = ymn_desc + slot(y0);
-      const uint64_t next0 = yk_desc + slot(y0 + 2), next1 = yk_desc + slot(y1 + 2);
-      if (elect_one()) {
-        issue_sums<Cfg::kCols>(tAcc1, tS, b1, id_acc, i > 0);
-        if (PASS == kDkv) tc_commit(&empty_bar[y1 % Cfg::kStages]);
-      }
-      __syncwarp();
-      if (more) {
-        ok = take(y0 + 2, i + 1);
-        if (!ok) break;
+    if (rank == 0) {
+      const uint32_t id_s = idesc_bf16_f32(CG * kTile, kTile, 0, 0);
+      const uint32_t id_acc = idesc_bf16_f32(CG * kTile, width, 0, 1);
+      const uint64_t x0_desc = desc_k_major(smem_u32(sX));
+      const uint64_t x1_desc = desc_k_major(smem_u32(sX) + Cfg::kTileBytes);
+      const uint64_t yk_desc = desc_k_major(smem_u32(sY)), ymn_desc = desc_mn_major(smem_u32(sY));
+      constexpr int kYBox = kBoxBytes / CG;
+      constexpr int k1m = CG == 2 ? kY1m : kY1k, k0m = CG == 2 ? kY0m : kY0k;
+      constexpr int kB1 = PASS == kDq ? k0m : k1m;       // of the first sum
+      auto slot = [&](int kind, int32_t i) {
+        return static_cast<uint32_t>(2 * kind + (i & 1)) * (Cfg::kSlotBytes >> 4);
+      };
+      auto take = [&](int kind, int32_t i) {
+        uint64_t* bar = &full_bar[2 * kind + (i & 1)];
+        const uint32_t parity = i >> 1 & 1;
+        const bool there = CG == 2 ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+        if (__all_sync(0xffffffffu, there)) return true;
+        bool ok = warp_wait_all(bar, parity, p.err, 63, p.wait_limit_ns);
+        if (CG == 2) ok = ok && __all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity));
+        return ok;
+      };
+      auto written = [&](uint64_t* bar, int32_t i, uint32_t where) {
+        return warp_wait_all(bar, i & 1, p.err, where, p.wait_limit_ns);
+      };
+      auto commit = [&](uint64_t* bar) {
+        if constexpr (CG == 2) tc_commit_pair_mc(bar, static_cast<uint16_t>(3));
+        else tc_commit(bar);
+      };
+      auto free_slot = [&](int kind, int32_t i) { commit(&empty_bar[2 * kind + (i & 1)]); };
+      bool ok = steps > 0 && warp_wait_all(x_bar, 0, p.err, 62, p.wait_limit_ns) && take(kY0k, 0);
+      if (ok) {
+        tc_fence_after();
         if (elect_one()) {
-          issue_scores<HD / 16>(tS, x0_desc, next0, id_s, ksteps);
-          tc_commit(s_bar);
+          issue_scores<CG, HD / 16, kYBox>(tS, x0_desc, yk_desc + slot(kY0k, 0), id_s, ksteps);
+          commit(s_bar);
+          if (CG == 2) free_slot(kY0k, 0);
+        }
+        __syncwarp();
+        ok = take(kY1k, 0);
+      }
+      if (ok) {
+        tc_fence_after();
+        if (elect_one()) {
+          issue_scores<CG, HD / 16, kYBox>(tD, x1_desc, yk_desc + slot(kY1k, 0), id_s, ksteps);
+          commit(d_bar);
+          if (CG == 2 || PASS == kDq) free_slot(kY1k, 0);
         }
         __syncwarp();
       }
-      ok = warp_wait_all(ds_bar, i & 1, p.err, 65, p.wait_limit_ns);
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one()) {
-        issue_sums<Cfg::kCols>(tAcc2, tD, b2, id_acc, i > 0);
-        tc_commit(more ? &empty_bar[y0 % Cfg::kStages] : acc_bar);
-      }
-      __syncwarp();
-      if (more) {
-        ok = take(y1 + 2, i + 1);
+      for (int32_t i = 0; i < steps && ok; ++i) {
+        const bool more = i + 1 < steps;
+        const uint64_t b1 = ymn_desc + slot(kB1, i), b2 = ymn_desc + slot(k0m, i);
+        const uint64_t next0 = yk_desc + slot(kY0k, i + 1), next1 = yk_desc + slot(kY1k, i + 1);
+        ok = (CG == 1 || take(kB1, i)) && written(p_bar, i, 64);
         if (!ok) break;
+        tc_fence_after();
         if (elect_one()) {
-          issue_scores<HD / 16>(tD, x1_desc, next1, id_s, ksteps);
-          tc_commit(d_bar);
-          if (PASS == kDq) tc_commit(&empty_bar[(y1 + 2) % Cfg::kStages]);
+          issue_sums<CG, Cfg::kCols>(tAcc1, tS, b1, id_acc, i > 0);
+          if (PASS == kDkv) free_slot(k1m, i);
         }
         __syncwarp();
+        if (more) {
+          ok = take(kY0k, i + 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_scores<CG, HD / 16, kYBox>(tS, x0_desc, next0, id_s, ksteps);
+            commit(s_bar);
+            if (CG == 2) free_slot(kY0k, i + 1);
+          }
+          __syncwarp();
+        }
+        ok = (CG == 1 || PASS == kDq || take(k0m, i)) && written(ds_bar, i, 65);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_sums<CG, Cfg::kCols>(tAcc2, tD, b2, id_acc, i > 0);
+          free_slot(k0m, i);
+          if (!more) commit(acc_bar);
+        }
+        __syncwarp();
+        if (more) {
+          ok = take(kY1k, i + 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_scores<CG, HD / 16, kYBox>(tD, x1_desc, next1, id_s, ksteps);
+            commit(d_bar);
+            if (CG == 2 || PASS == kDq) free_slot(kY1k, i + 1);
+          }
+          __syncwarp();
+        }
       }
+      // every MMA issued here is complete before TMEM is released
+      if (elect_one()) {
+        if constexpr (CG == 2) tc_commit_pair(done_bar); else tc_commit(done_bar);
+      }
+      __syncwarp();
+      warp_wait_all(done_bar, 0, nullptr, 68, p.wait_limit_ns);
     }
-    // every MMA issued here is complete before TMEM is released
-    if (elect_one()) tc_commit(done_bar);
-    __syncwarp();
-    warp_wait_all(done_bar, 0, nullptr, 68, p.wait_limit_ns);
   } else if (warp == 2 && PASS == kDkv) {
     // ----------------------------------------------- lse and delta of the queries
     // (loaded a step ahead, all at once: the threads wait for these as for the scores)
@@ -394,7 +500,9 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_bar);
+      if (lane == 0) {
+        if constexpr (CG == 2) mbar_arrive_cluster(lead(p_bar)); else mbar_arrive(p_bar);
+      }
 
       ok = warp_wait_all(d_bar, i & 1, p.err, 71, p.wait_limit_ns);
       if (!ok) break;
@@ -427,7 +535,7 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(ds_bar);
+        if constexpr (CG == 2) mbar_arrive_cluster(lead(ds_bar)); else mbar_arrive(ds_bar);
         if (PASS == kDkv) mbar_arrive(&stat_empty[i & 1]);
       }
       if (++tile == first + count) tile = first;
@@ -469,17 +577,17 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
     }
     tc_fence_before();
   }
-  __syncthreads();
+  if constexpr (CG == 2) cluster_sync(); else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if constexpr (CG == 2) tmem_dealloc_pair(tmem, 512); else tmem_dealloc(tmem, 512);
   }
 }
 
-template <int HD, int PASS>
-cudaError_t launch_pass(const BwdParams& p, int64_t tiles, cudaStream_t stream) {
-  using Cfg = BwdCfg<HD>;
-  const auto kern = attention_bwd_kernel<HD, PASS>;
+template <int HD, int CG, int PASS>
+cudaError_t launch_pass(const BwdParams& p, int64_t T, cudaStream_t stream) {
+  using Cfg = BwdCfg<HD, CG>;
+  const auto kern = attention_bwd_kernel<HD, CG, PASS>;
   static std::atomic<bool> ready[64];    // per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -489,17 +597,30 @@ cudaError_t launch_pass(const BwdParams& p, int64_t tiles, cudaStream_t stream) 
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev].store(true, std::memory_order_release);
   }
+  const int64_t tiles = most_tiles(T, CG * kTile, p.sequences);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.heads), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.heads * CG), 1, 1);
   cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
   cfg.dynamicSmemBytes = Cfg::kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int PASS>
+cudaError_t launch(const BwdParams& p, int64_t T, cudaStream_t stream) {
+  if (p.dim <= 64) return launch_pass<64, 1, PASS>(p, T, stream);
+  // pairs where a sequence has a few tiles' rows
+  if (T / p.sequences >= 512) return launch_pass<128, 2, PASS>(p, T, stream);
+  return launch_pass<128, 1, PASS>(p, T, stream);
 }
 
 }  // namespace
@@ -509,10 +630,10 @@ cudaError_t launch_attention_bwd(const AttentionArgs& a, cudaStream_t stream) {
   BwdParams p;
   std::memset(&p, 0, sizeof(p));
   CUtensorMap q, k, v, dout;
-  if (!heads_map(&q, a.q.at, a.ws, d.Tq, d.hq, d.dim, d.q_ts, d.q_hs, 1, kTile) ||
-      !heads_map(&k, a.k.at, a.ws, d.Tk, d.hk, d.dim, d.k_ts, d.k_hs, 1, kTile) ||
-      !heads_map(&v, a.v.at, a.ws, d.Tk, d.hk, d.dim, d.v_ts, d.v_hs, 1, kTile) ||
-      !heads_map(&dout, a.dout.at, a.ws, d.Tq, d.hq, d.dim, d.do_ts, d.do_hs, 1, kTile))
+  if (!heads_map(&q, a.q.at, a.ws, d.Tq, d.hq, d.dim, d.q_ts, d.q_hs, 1, kTile / 2) ||
+      !heads_map(&k, a.k.at, a.ws, d.Tk, d.hk, d.dim, d.k_ts, d.k_hs, 1, kTile / 2) ||
+      !heads_map(&v, a.v.at, a.ws, d.Tk, d.hk, d.dim, d.v_ts, d.v_hs, 1, kTile / 2) ||
+      !heads_map(&dout, a.dout.at, a.ws, d.Tq, d.hq, d.dim, d.do_ts, d.do_hs, 1, kTile / 2))
     return cudaErrorInvalidValue;
   p.lse = a.lse;
   p.delta = reinterpret_cast<float*>(static_cast<char*>(a.ws) + 256);
@@ -537,9 +658,7 @@ cudaError_t launch_attention_bwd(const AttentionArgs& a, cudaStream_t stream) {
     p.dout = a.dout;
     p.g2 = a.dq;
     p.heads = d.hq;
-    const int64_t tiles = most_tiles(d.Tq, kTile, d.sequences);
-    const cudaError_t e = d.dim <= 64 ? launch_pass<64, kDq>(p, tiles, stream)
-                                      : launch_pass<128, kDq>(p, tiles, stream);
+    const cudaError_t e = launch<kDq>(p, d.Tq, stream);
     if (e != cudaSuccess) return e;
   }
   if (d.Tk == 0) return cudaSuccess;
@@ -550,9 +669,7 @@ cudaError_t launch_attention_bwd(const AttentionArgs& a, cudaStream_t stream) {
   p.g1 = a.dv;
   p.g2 = a.dk;
   p.heads = d.hk;
-  const int64_t tiles = most_tiles(d.Tk, kTile, d.sequences);
-  return d.dim <= 64 ? launch_pass<64, kDkv>(p, tiles, stream)
-                     : launch_pass<128, kDkv>(p, tiles, stream);
+  return launch<kDkv>(p, d.Tk, stream);
 }
 
 }  // namespace boost_gb300

@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           if (n[x] > 0) {
-            issue_scores<HD / 16>(tS[x], q_desc[x], k_desc, id_s, ksteps);
+            issue_scores<1, HD / 16>(tS[x], q_desc[x], k_desc, id_s, ksteps);
             tc_commit(&s_bar[x]);
           }
         tc_commit(&empty_bar[0]);
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
       if (ok && more) ok = warp_wait_all(&full_bar[stage], phase, p.err, 45, p.wait_limit_ns);
       if (!ok) break;
       const int32_t left = at.nk - (first + j) * kTile;
-      if (left < kTile) zero_rows(sKV + v_stage * Cfg::kTileBytes, Cfg::kBoxes, left, lane);
+      if (left < kTile) zero_rows(sKV + v_stage * Cfg::kTileBytes, Cfg::kBoxes, kTile, left, lane);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (j < n[x]) {
@@ -224,9 +224,9 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
           tc_fence_after();
           const uint64_t vd = v_desc + v_stage * kStep, kd = k_desc + stage * kStep;
           if (elect_one()) {
-            issue_sums<kTile>(tO[x], tS[x], vd, id_o, j > 0);          // O_x += P_x V
+            issue_sums<1, kTile>(tO[x], tS[x], vd, id_o, j > 0);          // O_x += P_x V
             if (j + 1 < n[x]) {
-              issue_scores<HD / 16>(tS[x], q_desc[x], kd, id_s, ksteps);
+              issue_scores<1, HD / 16>(tS[x], q_desc[x], kd, id_s, ksteps);
               tc_commit(&s_bar[x]);
             } else {
               tc_commit(&o_bar[x]);

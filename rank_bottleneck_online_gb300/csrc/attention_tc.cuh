@@ -28,6 +28,44 @@ __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem,
       : "memory");
 }
 
+// The same over a CTA pair: 256 rows, 128 of them in each CTA's TMEM, and B split along N.
+__device__ __forceinline__ void tc_mma_bf16_ts_pair(uint32_t d_tmem, uint32_t a_tmem,
+                                                    uint64_t b_desc, uint32_t idesc,
+                                                    uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrive on a barrier of a CTA of the cluster (its cluster address): what this thread has written
+// is seen by a thread of that CTA that has waited with mbar_try_wait_cluster.
+__device__ __forceinline__ void mbar_arrive_release(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Arrive there and expect bytes of copies (which carry their own order: as a release, the arrival
+// would wait about 1100 cycles for this thread's earlier ones).
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
+               "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+
 // Each thread of the warp writes 32 consecutive columns of its TMEM lane.
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -88,35 +126,40 @@ __device__ __forceinline__ uint64_t desc_mn_major(uint32_t base) {
   return desc_hi_sw128(kBoxBytes, 1024u) | ((base >> 4) & 0x3FFFu);
 }
 
-// D = X Y^T over `steps` steps of 16 values (MAX at most), both K-major.
-template <int MAX>
+// D = X Y^T over `steps` steps of 16 values (MAX at most), both K-major, Y's boxes YBOX bytes apart.
+template <int CG, int MAX, int YBOX = kBoxBytes>
 __device__ __forceinline__ void issue_scores(uint32_t d, uint64_t x, uint64_t y, uint32_t idesc,
                                              int steps) {
 #pragma unroll
   for (int kk = 0; kk < MAX; ++kk) {
-    constexpr uint32_t kBox = kBoxBytes >> 4;
-    const uint32_t at = (kk >> 2) * kBox + (kk & 3) * 2;
-    if (kk < steps) tc_mma_bf16(d, x + at, y + at, idesc, kk > 0);
+    const uint64_t xk = x + (kk >> 2) * (kBoxBytes >> 4) + (kk & 3) * 2;
+    const uint64_t yk = y + (kk >> 2) * (YBOX >> 4) + (kk & 3) * 2;
+    if (kk < steps) {
+      if constexpr (CG == 2) tc_mma_bf16_pair(d, xk, yk, idesc, kk > 0);
+      else tc_mma_bf16(d, xk, yk, idesc, kk > 0);
+    }
   }
 }
 
 // D (+)= A Y over the tile's 128 rows, A in TMEM as parts of `COLS` values that lie COLS columns
 // apart, Y MN-major.
-template <int COLS>
+template <int CG, int COLS>
 __device__ __forceinline__ void issue_sums(uint32_t d, uint32_t a, uint64_t y, uint32_t idesc,
                                            bool more) {
 #pragma unroll
-  for (int kk = 0; kk < kTile / 16; ++kk)
-    tc_mma_bf16_ts(d, a + 16 * kk / COLS * COLS + 16 * kk % COLS / 2, y + 128 * kk, idesc,
-                   kk > 0 ? 1u : more);
+  for (int kk = 0; kk < kTile / 16; ++kk) {
+    const uint32_t ak = a + 16 * kk / COLS * COLS + 16 * kk % COLS / 2;
+    if constexpr (CG == 2) tc_mma_bf16_ts_pair(d, ak, y + 128 * kk, idesc, kk > 0 ? 1u : more);
+    else tc_mma_bf16_ts(d, ak, y + 128 * kk, idesc, kk > 0 ? 1u : more);
+  }
 }
 
-// Zero rows [from, 128) of a tile of `boxes` boxes that a TMA load has filled, by a whole warp:
+// Zero rows [from, rows) of `boxes` boxes of 64 values that a TMA load has filled, by a whole warp:
 // rows of another sequence may hold NaN, which a probability of 0 would not hide.
-__device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, int from, int lane) {
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, int rows, int from, int lane) {
   for (int b = 0; b < boxes; ++b)
-    for (int i = from * 8 + lane; i < kTile * 8; i += 32)
-      *reinterpret_cast<uint4*>(tile + b * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+    for (int i = from * 8 + lane; i < rows * 8; i += 32)
+      *reinterpret_cast<uint4*>(tile + b * rows * 128 + i * 16) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   __syncwarp();
 }

@@ -82,6 +82,20 @@ def test_long_sequences():
     Case([(2048, 2048), (1, 5000), (77, 4100)], 2, 1, 128, seed=8).check()
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim", [72, 96, 104, 128])
+@pytest.mark.parametrize("lengths", [[(512, 512)], [(640, 640)], [(1025, 1153)], [(900, 1300), (700, 515)],
+                                     [(1300, 600)], [(1000, 1090), (130, 0), (511, 513)]])
+def test_sequences_of_several_tiles(lengths, dim, causal):
+    Case(lengths, 2, 2, dim, causal=causal, seed=dim, tail=70).check()
+
+
+@pytest.mark.parametrize("hq,hk", [(6, 2), (5, 1)])
+@pytest.mark.parametrize("layout", ["packed", "heads"])
+def test_sequences_of_several_tiles_with_shared_key_heads(hq, hk, layout):
+    Case([(700, 700), (1, 900), (850, 610)], hq, hk, 128, layout=layout, tail=3, seed=hq).check()
+
+
 @pytest.mark.parametrize("nq", [1, 3])
 def test_one_token_over_a_long_context(nq):
     Case([(nq, 30000), (nq, 1), (nq, 129), (nq, 9999)], 5, 1, 128, seed=9).check()
@@ -92,10 +106,19 @@ def test_one_token_over_a_long_context(nq):
 def test_other_sequences_do_not_leak(bad, dim):
     """NaN and infinities in one sequence and behind the last reach no other."""
     lengths = [(100, 190), (130, 70), (60, 60), (129, 140)]
+    _leak(lengths, dim, bad)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_long_sequences_do_not_leak(bad):
+    _leak([(600, 790), (530, 570), (660, 660), (629, 840)], 128, bad)
+
+
+def _leak(lengths, dim, bad):
     c = Case(lengths, 4, 2, dim, tail=150, seed=10)
     want = c.want()
-    q0, k0 = 100, 190
-    for t, at, n in ((c.q, q0, 130), (c.dout, q0, 130), (c.k, k0, 70), (c.v, k0, 70)):
+    (q0, k0), (nq, nk) = lengths[0], lengths[1]
+    for t, at, n in ((c.q, q0, nq), (c.dout, q0, nq), (c.k, k0, nk), (c.v, k0, nk)):
         t[at:at + n] = bad
     for t, which in ((c.q, 0), (c.dout, 0), (c.k, 1), (c.v, 1)):
         t[c.rows(which)[1]] = bad
@@ -103,15 +126,15 @@ def test_other_sequences_do_not_leak(bad, dim):
     grads = c.backward(out, lse)
     keep_q = torch.ones(c.Tq, dtype=torch.bool)
     keep_k = torch.ones(c.Tk, dtype=torch.bool)
-    keep_q[q0:q0 + 130] = keep_k[k0:k0 + 70] = False
+    keep_q[q0:q0 + nq] = keep_k[k0:k0 + nk] = False
     # (the poisoned sequence's own rows stand for themselves)
     for t, name, keep in ((out, "out", keep_q), (grads[0], "dq", keep_q), (grads[1], "dk", keep_k),
                           (grads[2], "dv", keep_k)):
         t[~keep] = 0
         for key in (name, f"{name}_size"):
             want[key][~keep.numpy()] = 0
-    lse[:, q0:q0 + 130] = 0
-    want["lse"][:, q0:q0 + 130] = 0
+    lse[:, q0:q0 + nq] = 0
+    want["lse"][:, q0:q0 + nq] = 0
     c.check_forward(out, lse, want)
     c.check_backward(grads, want)
 
