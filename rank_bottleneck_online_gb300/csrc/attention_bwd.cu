@@ -70,30 +70,81 @@ struct BwdCfg {
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
   static constexpr int kSlotBytes = kTileBytes / CG;     // of a loaded tile
   static constexpr int kSlotKinds = CG == 2 ? 4 : 2;
-  static constexpr int kBars = 4 * kSlotKinds + 12;
+  static constexpr int kBars = 4 * kSlotKinds + 15;
   static constexpr int kStatOffset = 2 * kTileBytes + 2 * kSlotKinds * kSlotBytes;
   static constexpr int kParts = 4;                       // threads of a row
   static constexpr int kCols = kTile / kParts;           // of its scores, each
   static constexpr int kStatBytes = 4 * 4 * kTile;       // two buffers of lse and delta
-  static constexpr int kBarOffset = kStatOffset + kStatBytes;
-  static constexpr int kSmemBytes = 1024 + kBarOffset + 8 * kBars + 16;
   static constexpr int kWarps = 4 * kParts;              // that work on the scores
+  static constexpr int kStageOffset = kStatOffset + kStatBytes;   // 16 rows of 64 bytes a warp
+  static constexpr int kSchedOffset = kStageOffset + kWarps * 1024;
+  static constexpr int kBarOffset = kSchedOffset + 256;
+  static constexpr int kSmemBytes = 1024 + kBarOffset + 8 * kBars + 16;
+  static_assert(sizeof(Schedule) <= 256, "its place");
   static constexpr int kThreads = 128 + 32 * kWarps;
   static_assert(kSmemBytes <= 232448, "shared memory");
   static_assert(CG == 1 || HD == 128, "a half of a tile's values is a box");
 };
 
-// Sum of a row's products over `n` values (a multiple of 8).
-__device__ __forceinline__ float dot_row(const __nv_bfloat16* a, const __nv_bfloat16* b, int n) {
-  float s = 0.0f;
-  for (int e = 0; e < n; e += 8) {
-    float x[8], y[8];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(a + e)), x);
-    unpack8(__ldg(reinterpret_cast<const uint4*>(b + e)), y);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
+// A work's rows of X (queries for kDq, longest rows first; keys for kDkv), and the tiles [first,
+// first + count) of the other side that they see; kDkv has those once for each head of the group.
+template <int CG, int PASS>
+struct Tile {
+  int32_t x0, nx, ny, off;               // first row, rows in the sequence; keys before its queries
+  int32_t x_row, y_row, y_head;          // in the tensors
+  int32_t first, count, steps;
+  __device__ __forceinline__ Tile(const Work& w, const BwdParams& p, int rank) {
+    const Place& at = w.at;
+    off = at.nk - at.nq;
+    const int32_t pair0 = (PASS == kDq ? at.tiles - 1 - at.tile : at.tile) * (CG * kTile);
+    x0 = pair0 + rank * kTile;
+    nx = PASS == kDq ? at.nq : at.nk;
+    ny = PASS == kDq ? at.nk : at.nq;
+    x_row = (PASS == kDq ? at.q0 : at.k0) + x0;
+    y_row = PASS == kDq ? at.k0 : at.q0;
+    y_head = PASS == kDq ? w.head / p.group : w.head * p.group;
+    first = count = 0;
+    if (w.head < 0 || at.tiles < 0) {
+      nx = x0;                           // no rows
+    } else if (PASS == kDq) {
+      const int32_t keys = p.causal ? min(at.nk, min(pair0 + CG * kTile, at.nq) + off) : at.nk;
+      count = keys > 0 ? (keys + kTile - 1) / kTile : 0;
+    } else {
+      first = p.causal ? max(pair0 - off, 0) / kTile : 0;
+      count = max((at.nq + kTile - 1) / kTile - first, 0);
+    }
+    steps = PASS == kDq ? count : count * p.group;
   }
-  return s;
+};
+
+// Store 32 rows of a warp, each lane's DIMS values of its row (from value `col`, of `dim`), rows
+// [row, row + rows) of a head: through 16 rows of shared memory at a time, so that neighbouring
+// lanes store neighbouring bytes (16 bytes of 32 rows a store took about 4000 cycles a tile).
+template <int DIMS>
+__device__ __forceinline__ void store_rows(const HeadsOut& out, int32_t head, int32_t row,
+                                           int32_t rows, int32_t col, int32_t dim,
+                                           const uint32_t (&v)[DIMS / 2], uint8_t* stage, int lane) {
+  constexpr int kPieces = DIMS / 8;      // of 16 bytes a row: 2 or 4
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    __syncwarp();
+    if (lane >> 4 == half) {
+      const int r = lane & 15;
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c)
+        *reinterpret_cast<uint4*>(stage + r * 64 + ((c ^ (r >> 1)) & (kPieces - 1)) * 16) =
+            make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kPieces / 2; ++i) {
+      const int r = i * (32 / kPieces) + lane / kPieces, c = lane % kPieces;
+      const uint4 x =
+          *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ (r >> 1)) & (kPieces - 1)) * 16);
+      if (half * 16 + r < rows && col + c * 8 < dim)
+        *reinterpret_cast<uint4*>(out.row(row + half * 16 + r, head) + col + c * 8) = x;
+    }
+  }
 }
 
 template <int HD, int CG, int PASS>
@@ -106,7 +157,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
   uint8_t* sX = smem;                                   // X0, X1
   uint8_t* sY = smem + 2 * Cfg::kTileBytes;             // two slots of each kind
   float* stat = reinterpret_cast<float*>(smem + Cfg::kStatOffset);
-  // (full, p and ds: the even CTA's of a pair, for both; the others: each CTA's own)
+  // (full, x, p, ds and acc_free: the even CTA's of a pair, for both; the others: each CTA's own)
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOffset);
   uint64_t* empty_bar = full_bar + 2 * Cfg::kSlotKinds;
   uint64_t* x_bar = empty_bar + 2 * Cfg::kSlotKinds;
@@ -118,7 +169,11 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
   uint64_t* stat_full = acc_bar + 1;                    // [2]
   uint64_t* stat_empty = stat_full + 2;                 // [2]
   uint64_t* tail_bar = stat_empty + 2;                  // a tile that ends inside
-  uint64_t* done_bar = tail_bar + 1;
+  uint64_t* x_empty = tail_bar + 1;                     // X0 and X1 are used up
+  uint64_t* acc_free = x_empty + 1;                     // the sums have been read
+  uint64_t* sync_bar = acc_free + 1;
+  uint64_t* done_bar = sync_bar + 1;
+  Schedule* sched = reinterpret_cast<Schedule*>(smem + Cfg::kSchedOffset);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -139,7 +194,11 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
       mbar_init(&stat_empty[b], Cfg::kWarps);
     }
     mbar_init(tail_bar, 1);
+    mbar_init(x_empty, 1);
+    mbar_init(acc_free, CG * Cfg::kWarps);
+    mbar_init(sync_bar, Cfg::kWarps);
     mbar_init(done_bar, 1);
+    schedule_init<CG>(sched, Cfg::kWarps + 1 + (rank == 0) + (PASS == kDkv));
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -169,73 +228,57 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
 
-  // This CTA's (pair's) tile of queries (kDq, longest rows first) or keys, and the tiles [first,
-  // first + count) of the other side that its rows see; kDkv has those once for each head of the
-  // group.
-  const int32_t work = static_cast<int32_t>(blockIdx.x) / CG, head = work % p.heads;
-  Place at = find_tile(p.q_starts, p.k_starts, p.Tq, p.Tk, p.sequences, work / p.heads, CG * kTile,
-                       PASS == kDkv);
-  const int32_t off = at.nk - at.nq;                     // keys before the first query
-  const int32_t pair0 = (PASS == kDq ? at.tiles - 1 - at.tile : at.tile) * (CG * kTile);
-  const int32_t x0 = pair0 + rank * kTile;
-  const int32_t nx = PASS == kDq ? at.nq : at.nk, ny = PASS == kDq ? at.nk : at.nq;
-  int32_t first = 0, count = 0;
-  if (at.tiles > 0) {
-    if (PASS == kDq) {
-      const int32_t keys = p.causal ? min(at.nk, min(pair0 + CG * kTile, at.nq) + off) : at.nk;
-      count = keys > 0 ? (keys + kTile - 1) / kTile : 0;
-    } else {
-      first = p.causal ? max(pair0 - off, 0) / kTile : 0;
-      count = max((at.nq + kTile - 1) / kTile - first, 0);
-    }
-  }
-  const int32_t steps = PASS == kDq ? count : count * p.group;
-  const int32_t x_row = (PASS == kDq ? at.q0 : at.k0) + x0;
-  const int32_t y_row = PASS == kDq ? at.k0 : at.q0;
-  const int32_t y_head = PASS == kDq ? head / p.group : head * p.group;
   const int ksteps = (p.dim + 15) / 16;
   const int32_t width = CG == 2 ? (p.dim + 31) / 32 * 32 : 16 * ksteps;   // columns of the sums
+  uint32_t works = 0;                                    // of this warp so far
+  Work w;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     constexpr int kHalf = kBoxBytes / 2;                 // a box of 64 rows
     constexpr uint32_t kTailBytes =
         (PASS == kDq && CG == 2 ? Cfg::kSlotKinds - 1 : Cfg::kSlotKinds) * Cfg::kSlotBytes;
-    if (steps > 0) {
+    int32_t last[Cfg::kSlotKinds];                       // the last load of each, of all steps
+    uint32_t tails = 0, tiles = 0;                       // tiles that had steps
+    int32_t u = 0;                                       // steps
+    bool ok = true;
+#pragma unroll
+    for (int kind = 0; kind < Cfg::kSlotKinds; ++kind) last[kind] = -1;
+    while (ok && next_work(sched, works, w, p.err, p.wait_limit_ns)) {
+      const Tile<CG, PASS> t(w, p, rank);
+      if (t.steps == 0) continue;
+      ok = warp_wait_all(x_empty, (tiles & 1) ^ 1, p.err, 60, p.wait_limit_ns);
+      if (!ok) break;
+      ++tiles;
       if (elect_one()) {
         const uint32_t bar = lead(x_bar);
         if constexpr (CG == 2) mbar_arrive_expect_tx_cluster(bar, 2 * Cfg::kTileBytes);
         else mbar_arrive_expect_tx(x_bar, 2 * Cfg::kTileBytes);
         for (int b = 0; b < 2 * Cfg::kBoxes; ++b) {
           uint8_t* dst = sX + b * kHalf;
-          const int32_t col = 64 * (b >> 1), row = x_row + (b & 1) * (kTile / 2);
+          const int32_t col = 64 * (b >> 1), row = t.x_row + (b & 1) * (kTile / 2);
           if constexpr (CG == 2) {
-            tma_load_3d_pair(dst, &p.tmX0, bar, col, head, row);
-            tma_load_3d_pair(dst + Cfg::kTileBytes, &p.tmX1, bar, col, head, row);
+            tma_load_3d_pair(dst, &p.tmX0, bar, col, w.head, row);
+            tma_load_3d_pair(dst + Cfg::kTileBytes, &p.tmX1, bar, col, w.head, row);
           } else {
-            tma_load_3d(dst, &p.tmX0, x_bar, col, head, row);
-            tma_load_3d(dst + Cfg::kTileBytes, &p.tmX1, x_bar, col, head, row);
+            tma_load_3d(dst, &p.tmX0, x_bar, col, w.head, row);
+            tma_load_3d(dst + Cfg::kTileBytes, &p.tmX1, x_bar, col, w.head, row);
           }
         }
       }
       __syncwarp();
-      int32_t tile = first, h = y_head;
-      int32_t last[Cfg::kSlotKinds];                     // step of the last load
-      uint32_t tails = 0;
-      bool ok = true;
-#pragma unroll
-      for (int kind = 0; kind < Cfg::kSlotKinds; ++kind) last[kind] = -1;
-      for (int32_t i = 0; i < steps && ok; ++i) {
-        const int32_t left = ny - tile * kTile, row = y_row + tile * kTile;
+      int32_t tile = t.first, h = t.y_head;
+      for (int32_t i = 0; i < t.steps && ok; ++i, ++u) {
+        const int32_t left = t.ny - tile * kTile, row = t.y_row + tile * kTile;
         // a tile in which the sequence ends lands on this CTA's own barrier first
         const bool tail = left < kTile;
 #pragma unroll
         for (int kind = 0; kind < Cfg::kSlotKinds; ++kind) {
           if (PASS == kDq && kind == kY1m) continue;
-          const int s = 2 * kind + (i & 1);
-          ok = ok && warp_wait_all(&empty_bar[s], (i >> 1 & 1) ^ 1, p.err, 61, p.wait_limit_ns);
+          const int s = 2 * kind + (u & 1);
+          ok = ok && warp_wait_all(&empty_bar[s], (u >> 1 & 1) ^ 1, p.err, 61, p.wait_limit_ns);
           if (!ok) break;
-          last[kind] = i;
+          last[kind] = u;
           const CUtensorMap* map = kind == kY0k || kind == kY0m ? &p.tmY0 : &p.tmY1;
           uint8_t* dst = sY + s * Cfg::kSlotBytes;
           if (elect_one()) {
@@ -266,7 +309,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
 #pragma unroll
           for (int kind = 0; kind < Cfg::kSlotKinds; ++kind) {
             if (PASS == kDq && kind == kY1m) continue;
-            const int s = 2 * kind + (i & 1);
+            const int s = 2 * kind + (u & 1);
             uint8_t* dst = sY + s * Cfg::kSlotBytes;
             if (CG == 2 && (kind == kY0k || kind == kY1k))
               zero_rows(dst, 2, kTile / 2, min(max(left - rank * (kTile / 2), 0), kTile / 2), lane);
@@ -279,19 +322,19 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
             __syncwarp();
           }
         }
-        if (++tile == first + count) {
-          tile = first;
+        if (++tile == t.first + t.count) {
+          tile = t.first;
           ++h;
         }
       }
-      // the copies started here have landed before the CTA (or the pair) exits
-      if (rank == 0) {
-        warp_wait_all(x_bar, 0, nullptr, 67, p.wait_limit_ns);
+    }
+    // the copies started here have landed before the CTA (or the pair) exits
+    if (rank == 0) {
+      if (tiles > 0) warp_wait_all(x_bar, (tiles - 1) & 1, nullptr, 67, p.wait_limit_ns);
 #pragma unroll
-        for (int kind = 0; kind < Cfg::kSlotKinds; ++kind)
-          for (int32_t i = max(last[kind] - 1, 0); i <= last[kind]; ++i)
-            warp_wait_all(&full_bar[2 * kind + (i & 1)], i >> 1 & 1, nullptr, 67, p.wait_limit_ns);
-      }
+      for (int kind = 0; kind < Cfg::kSlotKinds; ++kind)
+        for (int32_t i = max(last[kind] - 1, 0); i <= last[kind]; ++i)
+          warp_wait_all(&full_bar[2 * kind + (i & 1)], i >> 1 & 1, nullptr, 67, p.wait_limit_ns);
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer
@@ -324,69 +367,82 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
         else tc_commit(bar);
       };
       auto free_slot = [&](int kind, int32_t i) { commit(&empty_bar[2 * kind + (i & 1)]); };
-      bool ok = steps > 0 && warp_wait_all(x_bar, 0, p.err, 62, p.wait_limit_ns) && take(kY0k, 0);
-      if (ok) {
+      bool ok = true;
+      uint32_t tiles = 0;
+      int32_t u0 = 0;                                    // step that this tile begins with
+      while (ok && next_work(sched, works, w, p.err, p.wait_limit_ns)) {
+        const Tile<CG, PASS> t(w, p, rank);
+        if (t.steps == 0) continue;
+        ok = warp_wait_all(x_bar, tiles & 1, p.err, 62, p.wait_limit_ns) && take(kY0k, u0);
+        if (!ok) break;
         tc_fence_after();
+        const uint64_t y0 = yk_desc + slot(kY0k, u0), y1 = yk_desc + slot(kY1k, u0);
         if (elect_one()) {
-          issue_scores<CG, HD / 16, kYBox>(tS, x0_desc, yk_desc + slot(kY0k, 0), id_s, ksteps);
+          issue_scores<CG, HD / 16, kYBox>(tS, x0_desc, y0, id_s, ksteps);
           commit(s_bar);
-          if (CG == 2) free_slot(kY0k, 0);
+          if (CG == 2) free_slot(kY0k, u0);
         }
         __syncwarp();
-        ok = take(kY1k, 0);
-      }
-      if (ok) {
+        ok = take(kY1k, u0);
+        if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          issue_scores<CG, HD / 16, kYBox>(tD, x1_desc, yk_desc + slot(kY1k, 0), id_s, ksteps);
+          issue_scores<CG, HD / 16, kYBox>(tD, x1_desc, y1, id_s, ksteps);
           commit(d_bar);
-          if (CG == 2 || PASS == kDq) free_slot(kY1k, 0);
+          if (CG == 2 || PASS == kDq) free_slot(kY1k, u0);
+          if (t.steps == 1) commit(x_empty);
         }
         __syncwarp();
-      }
-      for (int32_t i = 0; i < steps && ok; ++i) {
-        const bool more = i + 1 < steps;
-        const uint64_t b1 = ymn_desc + slot(kB1, i), b2 = ymn_desc + slot(k0m, i);
-        const uint64_t next0 = yk_desc + slot(kY0k, i + 1), next1 = yk_desc + slot(kY1k, i + 1);
-        ok = (CG == 1 || take(kB1, i)) && written(p_bar, i, 64);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_sums<CG, Cfg::kCols>(tAcc1, tS, b1, id_acc, i > 0);
-          if (PASS == kDkv) free_slot(k1m, i);
-        }
-        __syncwarp();
-        if (more) {
-          ok = take(kY0k, i + 1);
+        // the last tile's sums have been read
+        ok = warp_wait_all(acc_free, (tiles & 1) ^ 1, p.err, 59, p.wait_limit_ns);
+        ++tiles;
+        for (int32_t i = 0; i < t.steps && ok; ++i) {
+          const int32_t u = u0 + i;
+          const bool more = i + 1 < t.steps;
+          const uint64_t b1 = ymn_desc + slot(kB1, u), b2 = ymn_desc + slot(k0m, u);
+          const uint64_t next0 = yk_desc + slot(kY0k, u + 1), next1 = yk_desc + slot(kY1k, u + 1);
+          ok = (CG == 1 || take(kB1, u)) && written(p_bar, u, 64);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            issue_scores<CG, HD / 16, kYBox>(tS, x0_desc, next0, id_s, ksteps);
-            commit(s_bar);
-            if (CG == 2) free_slot(kY0k, i + 1);
+            issue_sums<CG, Cfg::kCols>(tAcc1, tS, b1, id_acc, i > 0);
+            if (PASS == kDkv) free_slot(k1m, u);
           }
           __syncwarp();
-        }
-        ok = (CG == 1 || PASS == kDq || take(k0m, i)) && written(ds_bar, i, 65);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_sums<CG, Cfg::kCols>(tAcc2, tD, b2, id_acc, i > 0);
-          free_slot(k0m, i);
-          if (!more) commit(acc_bar);
-        }
-        __syncwarp();
-        if (more) {
-          ok = take(kY1k, i + 1);
+          if (more) {
+            ok = take(kY0k, u + 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              issue_scores<CG, HD / 16, kYBox>(tS, x0_desc, next0, id_s, ksteps);
+              commit(s_bar);
+              if (CG == 2) free_slot(kY0k, u + 1);
+            }
+            __syncwarp();
+          }
+          ok = (CG == 1 || PASS == kDq || take(k0m, u)) && written(ds_bar, u, 65);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            issue_scores<CG, HD / 16, kYBox>(tD, x1_desc, next1, id_s, ksteps);
-            commit(d_bar);
-            if (CG == 2 || PASS == kDq) free_slot(kY1k, i + 1);
+            issue_sums<CG, Cfg::kCols>(tAcc2, tD, b2, id_acc, i > 0);
+            free_slot(k0m, u);
+            if (!more) commit(acc_bar);
           }
           __syncwarp();
+          if (more) {
+            ok = take(kY1k, u + 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              issue_scores<CG, HD / 16, kYBox>(tD, x1_desc, next1, id_s, ksteps);
+              commit(d_bar);
+              if (CG == 2 || PASS == kDq) free_slot(kY1k, u + 1);
+              if (i + 2 == t.steps) commit(x_empty);
+            }
+            __syncwarp();
+          }
         }
+        u0 += t.steps;
       }
       // every MMA issued here is complete before TMEM is released
       if (elect_one()) {
@@ -398,184 +454,235 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
   } else if (warp == 2 && PASS == kDkv) {
     // ----------------------------------------------- lse and delta of the queries
     // (loaded a step ahead, all at once: the threads wait for these as for the scores)
-    int32_t tile = first, h = y_head;
-    float l[4], d[4];
-    auto fetch = [&]() {
+    int32_t u = 0;
+    bool ok = true;
+    while (ok && next_work(sched, works, w, p.err, p.wait_limit_ns)) {
+      const Tile<CG, PASS> t(w, p, rank);
+      int32_t tile = t.first, h = t.y_head;
+      float l[4], d[4];
+      auto fetch = [&]() {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int32_t q = tile * kTile + k * 32 + lane;
-        const int64_t t = static_cast<int64_t>(h) * p.Tq + at.q0 + q;
-        l[k] = q < at.nq ? p.lse[t] : -CUDART_INF_F;
-        d[k] = q < at.nq ? p.delta[t] : 0.0f;
-      }
-      if (++tile == first + count) {
-        tile = first;
-        ++h;
-      }
-    };
-    if (steps > 0) fetch();
-    for (int32_t i = 0; i < steps; ++i) {
-      const int b = i & 1;
-      if (!warp_wait_all(&stat_empty[b], (i >> 1 & 1) ^ 1, p.err, 66, p.wait_limit_ns)) break;
+        for (int k = 0; k < 4; ++k) {
+          const int32_t q = tile * kTile + k * 32 + lane;
+          const int64_t at = static_cast<int64_t>(h) * p.Tq + w.at.q0 + q;
+          l[k] = q < w.at.nq ? p.lse[at] : -CUDART_INF_F;
+          d[k] = q < w.at.nq ? p.delta[at] : 0.0f;
+        }
+        if (++tile == t.first + t.count) {
+          tile = t.first;
+          ++h;
+        }
+      };
+      if (t.steps > 0) fetch();
+      for (int32_t i = 0; i < t.steps; ++i, ++u) {
+        const int b = u & 1;
+        ok = warp_wait_all(&stat_empty[b], (u >> 1 & 1) ^ 1, p.err, 66, p.wait_limit_ns);
+        if (!ok) break;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        // (a query that is none, or sees no key, has no probabilities)
-        const bool none = l[k] == -CUDART_INF_F;
-        stat[b * 2 * kTile + k * 32 + lane] = none ? CUDART_INF_F : l[k] * kLog2e;
-        stat[b * 2 * kTile + kTile + k * 32 + lane] = none ? 0.0f : d[k];
+        for (int k = 0; k < 4; ++k) {
+          // (a query that is none, or sees no key, has no probabilities)
+          const bool none = l[k] == -CUDART_INF_F;
+          stat[b * 2 * kTile + k * 32 + lane] = none ? CUDART_INF_F : l[k] * kLog2e;
+          stat[b * 2 * kTile + kTile + k * 32 + lane] = none ? 0.0f : d[k];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&stat_full[b]);
+        if (i + 1 < t.steps) fetch();
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&stat_full[b]);
-      if (i + 1 < steps) fetch();
     }
-  } else if (warp >= 4 && at.tiles > 0) {
+  } else if (warp == 3) {
+    schedule<CG>(sched, p.q_starts, p.k_starts, p.Tq, p.Tk, p.sequences, p.heads, CG * kTile,
+                 PASS == kDkv, rank, p.err, p.wait_limit_ns);
+  } else if (warp >= 4) {
     // ------------------------------------------------------ probabilities, dS
     constexpr int kCols = Cfg::kCols, kDims = HD / Cfg::kParts;
     const int part = (warp >> 2) - 1, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_at = tS + lane_base + kCols * part, d_at = tD + lane_base + kCols * part;
-    const int32_t x = x0 + row;                           // in the sequence
-    const bool valid = x < nx;
-    const int64_t token = x_row + static_cast<int64_t>(row);
-    // sum over a row's parts, in order
-    auto over_parts = [&](float v) {
-      stat[part * kTile + row] = v;
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * Cfg::kWarps) : "memory");
-      v = stat[row];
+    uint8_t* stage = smem + Cfg::kStageOffset + (warp - 4) * 1024;
+    // kDq: this warp's rows of out and dout, 16 lanes a row, for their products' sums; and lse
+    uint4 ro[4], rd[4];
+    float lse = 0.0f;
+    auto fetch = [&](const Tile<CG, PASS>& t) {
+      if (PASS != kDq) return;
 #pragma unroll
-      for (int i = 1; i < Cfg::kParts; ++i) v += stat[i * kTile + row];
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * Cfg::kWarps) : "memory");
-      return v;
+      for (int j = 0; j < 4; ++j) {
+        const int r = (warp - 4) * 8 + 2 * j + (lane >> 4), c = (lane & 15) * 8;
+        ro[j] = rd[j] = make_uint4(0, 0, 0, 0);
+        if (t.x0 + r < t.nx && c < p.dim) {
+          ro[j] = *reinterpret_cast<const uint4*>(p.o.row(t.x_row + r, w.head) + c);
+          rd[j] = *reinterpret_cast<const uint4*>(p.dout.row(t.x_row + r, w.head) + c);
+        }
+      }
+      lse = t.x0 + row < t.nx ? p.lse[w.head * p.Tq + t.x_row + row] * kLog2e : 0.0f;
     };
-    float lse = 0.0f, delta = 0.0f, e = 0.0f;             // kDq: of this row; what delta lacks
-    if (PASS == kDq) {
-      if (valid) {
-        lse = p.lse[head * p.Tq + token] * kLog2e;
-        const int32_t c0 = part * kDims;
-        delta = dot_row(p.dout.row(token, head) + c0, p.o.row(token, head) + c0,
-                        min(max(p.dim - c0, 0), kDims));
-      }
-      delta = over_parts(delta);
-    }
-    // kDq: keys that this row sees; kDkv: the first query that sees this row
-    const int32_t bound = PASS == kDq ? (p.causal ? min(at.nk, x + off + 1) : at.nk)
-                                      : (p.causal ? x - off : 0);
+    int32_t u = 0;
+    uint32_t tiles = 0, syncs = 0;
     bool ok = true;
-    int32_t tile = first;
-    for (int32_t i = 0; i < steps; ++i) {
-      const float* st = stat + (i & 1) * 2 * kTile + part * kCols;
-      if (PASS == kDkv) ok = warp_wait_all(&stat_full[i & 1], i >> 1 & 1, p.err, 69, p.wait_limit_ns);
-      ok = ok && warp_wait_all(s_bar, i & 1, p.err, 70, p.wait_limit_ns);
-      if (!ok) break;
-      tc_fence_after();
-      float s[kCols];
-      tmem_ld_32x32b_x32(s_at, s);
-      tmem_ld_wait();
-      const int32_t lim = bound - tile * kTile - kCols * part;   // of this part's columns
+    auto threads_sync = [&]() {                           // of the warps that work on the scores
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sync_bar);
+      ok = ok && warp_wait_all(sync_bar, syncs++ & 1, p.err, 73, p.wait_limit_ns);
+    };
+    bool have = next_work(sched, works, w, p.err, p.wait_limit_ns);
+    Tile<CG, PASS> t(w, p, rank);
+    if (have) fetch(t);
+    while (have) {
+      const int32_t x = t.x0 + row;                       // in the sequence
+      const bool valid = x < t.nx;
+      float delta = 0.0f, e = 0.0f;                       // kDq: of this row; what delta lacks
       if (PASS == kDq) {
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) s[c] = exp2_fast(fmaf(s[c], p.scale_log2, -lse));
-        if (__any_sync(0xffffffffu, lim < kCols)) {
+        for (int j = 0; j < 4; ++j) {
+          float a[8], b[8], s = 0.0f;
+          unpack8(ro[j], a);
+          unpack8(rd[j], b);
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) s[c] = c < lim ? s[c] : 0.0f;
-        }
-      } else {
+          for (int k = 0; k < 8; ++k) s = fmaf(a[k], b[k], s);
 #pragma unroll
-        for (int c = 0; c < kCols; c += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(st + c);
-          s[c] = exp2_fast(fmaf(s[c], p.scale_log2, -l.x));
-          s[c + 1] = exp2_fast(fmaf(s[c + 1], p.scale_log2, -l.y));
-          s[c + 2] = exp2_fast(fmaf(s[c + 2], p.scale_log2, -l.z));
-          s[c + 3] = exp2_fast(fmaf(s[c + 3], p.scale_log2, -l.w));
+          for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          if ((lane & 15) == 0) stat[(warp - 4) * 8 + 2 * j + (lane >> 4)] = s;
         }
-        if (__any_sync(0xffffffffu, lim > 0)) {
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) s[c] = c >= lim ? s[c] : 0.0f;
-        }
+        threads_sync();
+        delta = stat[row];
+        threads_sync();
       }
-      uint32_t w[kCols / 2];
+      // kDq: keys that this row sees; kDkv: the first query that sees this row
+      const int32_t bound = PASS == kDq ? (p.causal ? min(w.at.nk, x + t.off + 1) : w.at.nk)
+                                        : (p.causal ? x - t.off : 0);
+      int32_t tile = t.first;
+      for (int32_t i = 0; i < t.steps; ++i, ++u) {
+        const float* st = stat + (u & 1) * 2 * kTile + part * kCols;
+        if (PASS == kDkv)
+          ok = ok && warp_wait_all(&stat_full[u & 1], u >> 1 & 1, p.err, 69, p.wait_limit_ns);
+        ok = ok && warp_wait_all(s_bar, u & 1, p.err, 70, p.wait_limit_ns);
+        if (!ok) break;
+        tc_fence_after();
+        float s[kCols];
+        tmem_ld_32x32b_x32(s_at, s);
+        tmem_ld_wait();
+        const int32_t lim = bound - tile * kTile - kCols * part;   // of this part's columns
+        if (PASS == kDq) {
 #pragma unroll
-      for (int c = 0; c < kCols / 2; ++c) w[c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
-      tmem_st_32x32b_x16(s_at, w);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (CG == 2) mbar_arrive_cluster(lead(p_bar)); else mbar_arrive(p_bar);
-      }
+          for (int c = 0; c < kCols; ++c) s[c] = exp2_fast(fmaf(s[c], p.scale_log2, -lse));
+          if (__any_sync(0xffffffffu, lim < kCols)) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) s[c] = c < lim ? s[c] : 0.0f;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(st + c);
+            s[c] = exp2_fast(fmaf(s[c], p.scale_log2, -l.x));
+            s[c + 1] = exp2_fast(fmaf(s[c + 1], p.scale_log2, -l.y));
+            s[c + 2] = exp2_fast(fmaf(s[c + 2], p.scale_log2, -l.z));
+            s[c + 3] = exp2_fast(fmaf(s[c + 3], p.scale_log2, -l.w));
+          }
+          if (__any_sync(0xffffffffu, lim > 0)) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) s[c] = c >= lim ? s[c] : 0.0f;
+          }
+        }
+        uint32_t pk[kCols / 2];
+#pragma unroll
+        for (int c = 0; c < kCols / 2; ++c) pk[c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
+        tmem_st_32x32b_x16(s_at, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2) mbar_arrive_cluster(lead(p_bar)); else mbar_arrive(p_bar);
+        }
 
-      ok = warp_wait_all(d_bar, i & 1, p.err, 71, p.wait_limit_ns);
-      if (!ok) break;
+        ok = warp_wait_all(d_bar, u & 1, p.err, 71, p.wait_limit_ns);
+        if (!ok) break;
+        tc_fence_after();
+        float d[kCols];
+        tmem_ld_32x32b_x32(d_at, d);
+        tmem_ld_wait();
+        if (PASS == kDq) {
+          float sum[4] = {};
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            d[c] = s[c] * (d[c] - delta);
+            sum[c & 3] += d[c];
+          }
+          e += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(st + kTile + c);
+            d[c] = s[c] * (d[c] - l.x);
+            d[c + 1] = s[c + 1] * (d[c + 1] - l.y);
+            d[c + 2] = s[c + 2] * (d[c + 2] - l.z);
+            d[c + 3] = s[c + 3] * (d[c + 3] - l.w);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < kCols / 2; ++c) pk[c] = pack_bf16x2(d[2 * c], d[2 * c + 1]);
+        tmem_st_32x32b_x16(d_at, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2) mbar_arrive_cluster(lead(ds_bar)); else mbar_arrive(ds_bar);
+          if (PASS == kDkv) mbar_arrive(&stat_empty[u & 1]);
+        }
+        if (++tile == t.first + t.count) tile = t.first;
+      }
+      if (PASS == kDq) {                                  // e over the row's parts, in order
+        stat[part * kTile + row] = e;
+        threads_sync();
+        e = stat[row];
+#pragma unroll
+        for (int i = 1; i < Cfg::kParts; ++i) e += stat[i * kTile + row];
+        threads_sync();
+        if (valid && part == 0) p.delta[w.head * p.Tq + t.x_row + row] = delta + e;
+      }
+      // the next tile's rows are on their way while this one's sums are stored
+      const Tile<CG, PASS> done = t;
+      const int32_t head = w.head;
+      have = ok && next_work(sched, works, w, p.err, p.wait_limit_ns);
+      t = Tile<CG, PASS>(w, p, rank);
+      if (have) fetch(t);
+      if (done.steps > 0) {
+        ok = ok && warp_wait_all(acc_bar, tiles++ & 1, p.err, 72, p.wait_limit_ns);
+        if (!ok) break;
+      }
       tc_fence_after();
-      float d[kCols];
-      tmem_ld_32x32b_x32(d_at, d);
-      tmem_ld_wait();
-      if (PASS == kDq) {
-        float sum[4] = {};
+      uint32_t g1[kDims / 2], g2[kDims / 2];
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          d[c] = s[c] * (d[c] - delta);
-          sum[c & 3] += d[c];
-        }
-        e += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < kCols; c += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(st + kTile + c);
-          d[c] = s[c] * (d[c] - l.x);
-          d[c + 1] = s[c + 1] * (d[c + 1] - l.y);
-          d[c + 2] = s[c + 2] * (d[c + 2] - l.z);
-          d[c + 3] = s[c + 3] * (d[c + 3] - l.w);
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < kCols / 2; ++c) w[c] = pack_bf16x2(d[2 * c], d[2 * c + 1]);
-      tmem_st_32x32b_x16(d_at, w);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (CG == 2) mbar_arrive_cluster(lead(ds_bar)); else mbar_arrive(ds_bar);
-        if (PASS == kDkv) mbar_arrive(&stat_empty[i & 1]);
-      }
-      if (++tile == first + count) tile = first;
-    }
-    if (ok && steps > 0) ok = warp_wait_all(acc_bar, 0, p.err, 72, p.wait_limit_ns);
-    tc_fence_after();
-    if (PASS == kDq) {
-      e = over_parts(e);
-      if (valid && part == 0) p.delta[head * p.Tq + token] = delta + e;
-    }
-    if (ok) {
-#pragma unroll
-      for (int c = part * kDims; c < (part + 1) * kDims; c += 16) {
+      for (int c = 0; c < kDims; c += 16) {
         float a1[16], a2[16];
-        if (steps > 0) {
-          tmem_ld_32x32b_x16(tAcc1 + lane_base + c, a1);
-          tmem_ld_32x32b_x16(tAcc2 + lane_base + c, a2);
+        if (done.steps > 0) {
+          tmem_ld_32x32b_x16(tAcc1 + lane_base + part * kDims + c, a1);
+          tmem_ld_32x32b_x16(tAcc2 + lane_base + part * kDims + c, a2);
           tmem_ld_wait();
         } else {
 #pragma unroll
           for (int k = 0; k < 16; ++k) a1[k] = a2[k] = 0.0f;
         }
 #pragma unroll
-        for (int k = 0; k < 16; k += 8) {
-          if (valid && c + k < p.dim) {
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              f[j] = p.scale * (PASS == kDq ? fmaf(-e, a1[k + j], a2[k + j]) : a2[k + j]);
-            *reinterpret_cast<uint4*>(p.g2.row(token, head) + c + k) = pack8(f);
-            if (PASS == kDkv) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) f[j] = a1[k + j];
-              *reinterpret_cast<uint4*>(p.g1.row(token, head) + c + k) = pack8(f);
-            }
+        for (int k = 0; k < 16; k += 2) {
+          if (PASS == kDq) {
+            a2[k] = fmaf(-e, a1[k], a2[k]);
+            a2[k + 1] = fmaf(-e, a1[k + 1], a2[k + 1]);
           }
+          g2[(c + k) / 2] = pack_bf16x2(p.scale * a2[k], p.scale * a2[k + 1]);
+          if (PASS == kDkv) g1[(c + k) / 2] = pack_bf16x2(a1[k], a1[k + 1]);
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && done.steps > 0) {
+        if constexpr (CG == 2) mbar_arrive_cluster(lead(acc_free)); else mbar_arrive(acc_free);
+      }
+      store_rows<kDims>(p.g2, head, done.x_row + quarter * 32, done.nx - done.x0 - quarter * 32,
+                        part * kDims, p.dim, g2, stage, lane);
+      if (PASS == kDkv)
+        store_rows<kDims>(p.g1, head, done.x_row + quarter * 32, done.nx - done.x0 - quarter * 32,
+                          part * kDims, p.dim, g1, stage, lane);
     }
-    tc_fence_before();
   }
   if constexpr (CG == 2) cluster_sync(); else __syncthreads();
   if (warp == 1) {

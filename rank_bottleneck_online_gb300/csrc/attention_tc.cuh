@@ -206,6 +206,128 @@ __device__ __forceinline__ Place find_tile(const int32_t* q_starts, const int32_
   return f;
 }
 
+// ----------------------------------------------------------------- work after work
+// A CTA (or a pair) that is done takes the place of one that has not begun yet
+// (clusterlaunchcontrol): tiles go out in the grid's order to whoever is free, and what a launch
+// costs each (barriers, TMEM, the search for its sequence, the first loads) is paid once or hidden.
+// One warp asks, looks the tile up and leaves it for the others a tile ahead.
+
+// Ask for a CTA (cluster) to cancel: 16 bytes at the same place in every CTA of the cluster, which
+// complete on each one's `bar`.
+template <int CG>
+__device__ __forceinline__ void clc_try_cancel(void* response, uint64_t* bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+        ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(smem_u32(response)),
+        "r"(smem_u32(bar))
+        : "memory");
+  else
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+        ".b128 [%0], [%1];" ::"r"(smem_u32(response)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+
+// The first CTA of the cancelled cluster (x), or -1 if there was none.
+__device__ __forceinline__ int32_t clc_answer(const void* response) {
+  uint32_t canceled, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(canceled), "=r"(x)
+      : "r"(smem_u32(response))
+      : "memory");
+  return canceled != 0u ? static_cast<int32_t>(x) : -1;
+}
+
+struct Work {
+  Place at;
+  int32_t head;                          // < 0: no more
+};
+
+struct Schedule {
+  uint4 response;
+  uint64_t clc_bar, clc_free;            // an answer is there; both CTAs have read it (the even's)
+  uint64_t full[2], empty[2];
+  Work work[2];
+};
+
+// Barriers of a schedule that `readers` warps of this CTA follow; by one thread.
+template <int CG>
+__device__ __forceinline__ void schedule_init(Schedule* s, int readers) {
+  mbar_init(&s->clc_bar, 1);
+  mbar_init(&s->clc_free, CG);
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&s->full[i], 1);
+    mbar_init(&s->empty[i], readers);
+  }
+}
+
+// The warp that asks: work after work, `per` rows a tile, `heads` of them side by side in the grid.
+template <int CG>
+__device__ __forceinline__ void schedule(Schedule* s, const int32_t* q_starts,
+                                         const int32_t* k_starts, int64_t Tq, int64_t Tk,
+                                         int sequences, int32_t heads, int32_t per, bool keys,
+                                         int rank, DeviceError* err, uint64_t limit_ns) {
+  const int lane = threadIdx.x & 31;
+  int32_t cta = static_cast<int32_t>(blockIdx.x);
+  for (uint32_t n = 0;; ++n) {
+    const int i = n & 1;
+    Work w;
+    w.head = -1;
+    if (cta >= 0) {
+      const int32_t work = cta / CG;
+      w.head = work % heads;
+      w.at = find_tile(q_starts, k_starts, Tq, Tk, sequences, work / heads, per, keys);
+    }
+    if (!warp_wait_all(&s->empty[i], (n >> 1 & 1) ^ 1, err, 31, limit_ns)) return;
+    if (lane == 0) {
+      s->work[i] = w;
+      mbar_arrive(&s->full[i]);
+    }
+    __syncwarp();
+    if (cta < 0) return;
+    // (the answer's place is free: both CTAs have read the last one)
+    if (rank == 0 && n > 0 && !warp_wait_all(&s->clc_free, (n - 1) & 1, err, 32, limit_ns)) return;
+    if (elect_one()) {
+      mbar_arrive_expect_tx(&s->clc_bar, 16);
+      if (rank == 0) clc_try_cancel<CG>(&s->response, &s->clc_bar);
+    }
+    __syncwarp();
+    // (not given up for another wait's sake: the answer must not land behind this CTA)
+    if (!warp_wait_all(&s->clc_bar, n & 1, nullptr, 0, limit_ns)) {
+      record_error(err, kErrTimeout, 33);
+      return;
+    }
+    cta = clc_answer(&s->response);
+    fence_proxy_async_smem();            // (read before the next answer is written)
+    __syncwarp();
+    if (elect_one()) {
+      if constexpr (CG == 2) mbar_arrive_release(mapa_shared(smem_u32(&s->clc_free), 0));
+      else mbar_arrive(&s->clc_free);
+    }
+    __syncwarp();
+  }
+}
+
+// A reader's next work, the n-th; false after the last.
+__device__ __forceinline__ bool next_work(Schedule* s, uint32_t& n, Work& w, DeviceError* err,
+                                          uint64_t limit_ns) {
+  const int i = n & 1;
+  if (!warp_wait_all(&s->full[i], n >> 1 & 1, err, 34, limit_ns)) return false;
+  w = s->work[i];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&s->empty[i]);
+  ++n;
+  return w.head >= 0;
+}
+
 // Most tiles that sequences of T rows in all can have.
 inline int64_t most_tiles(int64_t T, int64_t per, int64_t sequences) {
   const int64_t n = T / per + (sequences < T ? sequences : T);
