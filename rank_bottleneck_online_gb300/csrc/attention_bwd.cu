@@ -53,7 +53,8 @@ struct BwdParams {
   float* delta;                          // [hq, Tq]: written by kDq, read by kDkv
   const int32_t *q_starts, *k_starts;
   int64_t Tq, Tk;
-  int32_t heads, group;                  // of the tiles' side; query heads of a key head
+  Order order;                           // of the tiles' side
+  int32_t group;                         // query heads of a key head
   int32_t dim, sequences, causal;
   float scale, scale_log2;
   DeviceError* err;
@@ -246,7 +247,10 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
     for (int kind = 0; kind < Cfg::kSlotKinds; ++kind) last[kind] = -1;
     while (ok && next_work(sched, works, w, p.err, p.wait_limit_ns)) {
       const Tile<CG, PASS> t(w, p, rank);
-      if (t.steps == 0) continue;
+      if (t.steps == 0) {
+        if (rank == 0) want_work(sched);
+        continue;
+      }
       ok = warp_wait_all(x_empty, (tiles & 1) ^ 1, p.err, 60, p.wait_limit_ns);
       if (!ok) break;
       ++tiles;
@@ -327,6 +331,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
           ++h;
         }
       }
+      if (rank == 0) want_work(sched);
     }
     // the copies started here have landed before the CTA (or the pair) exits
     if (rank == 0) {
@@ -491,7 +496,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
       }
     }
   } else if (warp == 3) {
-    schedule<CG>(sched, p.q_starts, p.k_starts, p.Tq, p.Tk, p.sequences, p.heads, CG * kTile,
+    schedule<CG>(sched, p.q_starts, p.k_starts, p.Tq, p.Tk, p.sequences, p.order, CG * kTile,
                  PASS == kDkv, rank, p.err, p.wait_limit_ns);
   } else if (warp >= 4) {
     // ------------------------------------------------------ probabilities, dS
@@ -692,9 +697,13 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
 }
 
 template <int HD, int CG, int PASS>
-cudaError_t launch_pass(const BwdParams& p, int64_t T, cudaStream_t stream) {
+cudaError_t launch_pass(BwdParams p, int64_t T, cudaStream_t stream) {
   using Cfg = BwdCfg<HD, CG>;
   const auto kern = attention_bwd_kernel<HD, CG, PASS>;
+  // the other side: k and v of a key head, or q and dout of its query heads
+  const double bytes = 4.0 * p.dim * (PASS == kDq ? static_cast<double>(p.Tk) / p.group
+                                                  : static_cast<double>(p.Tq) * p.group);
+  p.order = grid_order(p.order.heads, most_tiles(T, CG * kTile, p.sequences), bytes, p.causal != 0);
   static std::atomic<bool> ready[64];    // per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -704,9 +713,8 @@ cudaError_t launch_pass(const BwdParams& p, int64_t T, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev].store(true, std::memory_order_release);
   }
-  const int64_t tiles = most_tiles(T, CG * kTile, p.sequences);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.heads * CG), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.order.tiles * p.order.heads * CG), 1, 1);
   cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
   cfg.dynamicSmemBytes = Cfg::kSmemBytes;
   cfg.stream = stream;
@@ -764,7 +772,7 @@ cudaError_t launch_attention_bwd(const AttentionArgs& a, cudaStream_t stream) {
     p.o = a.o;
     p.dout = a.dout;
     p.g2 = a.dq;
-    p.heads = d.hq;
+    p.order.heads = d.hq;
     const cudaError_t e = launch<kDq>(p, d.Tq, stream);
     if (e != cudaSuccess) return e;
   }
@@ -775,7 +783,7 @@ cudaError_t launch_attention_bwd(const AttentionArgs& a, cudaStream_t stream) {
   p.tmY1 = dout;
   p.g1 = a.dv;
   p.g2 = a.dk;
-  p.heads = d.hk;
+  p.order.heads = d.hk;
   return launch<kDkv>(p, d.Tk, stream);
 }
 

@@ -38,7 +38,8 @@ struct FwdParams {
   int64_t Tq, Tk;
   int32_t hq, dim, sequences, causal;
   int32_t pack, tok;                     // heads and tokens of a tile
-  int32_t heads, group;                  // hq / pack; of those that share a key head
+  Order order;                           // of hq / pack heads
+  int32_t group;                         // of them that share a key head
   int32_t splits;
   float scale_log2;
   DeviceError* err;
@@ -110,9 +111,11 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
   griddep_launch_dependents();
 
   // This CTA's pair of tiles, longest rows first.
-  const int32_t head = static_cast<int32_t>(blockIdx.x) % p.heads;
-  Place at = find_tile(p.q_starts, p.k_starts, p.Tq, p.Tk, p.sequences,
-                       static_cast<int32_t>(blockIdx.x) / p.heads, 2 * p.tok, false);
+  const int32_t span = p.order.set * p.order.tiles;
+  const int32_t first_head = static_cast<int32_t>(blockIdx.x) / span * p.order.set;
+  const int32_t set = min(p.order.set, p.order.heads - first_head);
+  const int32_t in_set = static_cast<int32_t>(blockIdx.x) % span, head = first_head + in_set % set;
+  Place at = find_tile(p.q_starts, p.k_starts, p.Tq, p.Tk, p.sequences, in_set / set, 2 * p.tok, false);
   const int32_t t0 = (at.tiles - 1 - at.tile) * 2 * p.tok;       // first token in the sequence
   const int32_t off = at.nk - at.nq;                              // keys before the first query
   // key tiles [first, first + n) of each, and of this split alone
@@ -429,7 +432,7 @@ int key_splits(const boost_attention_desc& d) {
 }
 
 template <int HD>
-cudaError_t launch_fwd(const FwdParams& p, int64_t pairs, cudaStream_t stream) {
+cudaError_t launch_fwd(const FwdParams& p, cudaStream_t stream) {
   using Cfg = FwdCfg<HD>;
   const auto kern = attention_fwd_kernel<HD>;
   static std::atomic<bool> ready[64];    // per device
@@ -442,7 +445,7 @@ cudaError_t launch_fwd(const FwdParams& p, int64_t pairs, cudaStream_t stream) {
     if (dev < 64) ready[dev].store(true, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pairs * p.heads), p.splits, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.order.tiles * p.order.heads), p.splits, 1);
   cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
   cfg.dynamicSmemBytes = Cfg::kSmemBytes;
   cfg.stream = stream;
@@ -468,8 +471,8 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream) {
   std::memset(&p, 0, sizeof(p));
   p.pack = packed_heads(d);
   p.tok = kTile / p.pack;
-  p.heads = d.hq / p.pack;
-  p.group = p.heads / d.hk;
+  p.group = d.hq / p.pack / d.hk;
+  p.order = grid_order(d.hq / p.pack, tile_pairs(d), 4.0 * d.dim * d.Tk / p.group, d.causal != 0);
   if (!heads_map(&p.tmQ, a.q.at, a.ws, d.Tq, d.hq, d.dim, d.q_ts, d.q_hs, p.pack, p.tok) ||
       !heads_map(&p.tmK, a.k.at, a.ws, d.Tk, d.hk, d.dim, d.k_ts, d.k_hs, 1, kTile) ||
       !heads_map(&p.tmV, a.v.at, a.ws, d.Tk, d.hk, d.dim, d.v_ts, d.v_hs, 1, kTile))
@@ -491,8 +494,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream) {
   const int64_t rows = d.Tq * d.hq;
   p.part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + 256);
   p.part_lse = p.part + p.splits * rows * d.dim;
-  const int64_t pairs = tile_pairs(d);
-  cudaError_t e = d.dim <= 64 ? launch_fwd<64>(p, pairs, stream) : launch_fwd<128>(p, pairs, stream);
+  cudaError_t e = d.dim <= 64 ? launch_fwd<64>(p, stream) : launch_fwd<128>(p, stream);
   if (e != cudaSuccess || p.splits == 1) return e;
   return launch_k(attention_join_kernel, (rows + kThreads / 32 - 1) / (kThreads / 32), stream, p);
 }

@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -164,18 +165,22 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int boxes, int rows, in
   __syncwarp();
 }
 
-// A sequence's bounds, and the number of one of its tiles.
+// A sequence's bounds, and one of its tiles: `tile` of `tiles`, as the grid counts them.
 struct Place {
   int32_t tile, tiles;                   // tiles < 0: none
   int32_t q0, nq, k0, nk;
 };
 
 // Where tile `index` of all sequences lies, sequence s having ceil(rows / per) tiles; by a whole
-// warp, each lane with a sequence of its own at a time. `keys`: the tiles are of the keys.
+// warp, each lane with a sequence of its own at a time. `keys`: the tiles are of the keys. Up to
+// 32 sequences take turns (the first tile of each, the second of each that has one, ...), so that
+// with a causal mask the tiles with most work, which the kernels count first, go out first; more
+// sequences follow one another.
 __device__ __forceinline__ Place find_tile(const int32_t* q_starts, const int32_t* k_starts,
                                            int64_t Tq, int64_t Tk, int sequences, int32_t index,
                                            int32_t per, bool keys) {
   const int lane = threadIdx.x & 31;
+  constexpr uint32_t kAll = 0xffffffffu;
   Place f{0, -1, 0, 0, 0, 0};
   for (int s0 = 0; s0 < sequences; s0 += 32) {
     Place mine{0, 0, 0, 0, 0, 0};
@@ -184,24 +189,45 @@ __device__ __forceinline__ Place find_tile(const int32_t* q_starts, const int32_
       sequence_bounds(k_starts, Tk, s0 + lane, mine.k0, mine.nk);
       mine.tiles = ((keys ? mine.nk : mine.nq) + per - 1) / per;
     }
-    int32_t sum = mine.tiles;            // up to and with this lane's
+    int src = -1;
+    if (sequences <= 32) {
+      // the last turn that begins at or before `index`: sum min(tiles, turn) <= index
+      int32_t lo = 0, hi = static_cast<int32_t>(__reduce_max_sync(kAll, mine.tiles));
+      const int32_t all = static_cast<int32_t>(__reduce_add_sync(kAll, mine.tiles));
+      if (index >= all) return f;
+      while (hi - lo > 1) {
+        const int32_t mid = (lo + hi) / 2;
+        if (static_cast<int32_t>(__reduce_add_sync(kAll, min(mine.tiles, mid))) <= index) lo = mid;
+        else hi = mid;
+      }
+      const int32_t rest = index - static_cast<int32_t>(__reduce_add_sync(kAll, min(mine.tiles, lo)));
+      const uint32_t has = __ballot_sync(kAll, mine.tiles > lo);
+      const uint32_t before = has & ((1u << lane) - 1u);
+      src = __ffs(__ballot_sync(kAll, mine.tiles > lo && __popc(before) == rest)) - 1;
+      f.tile = lo;
+    } else {
+      int32_t sum = mine.tiles;          // up to and with this lane's
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t below = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += below;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t below = __shfl_up_sync(kAll, sum, o);
+        if (lane >= o) sum += below;
+      }
+      const uint32_t has = __ballot_sync(kAll, index < sum);
+      if (has != 0) {
+        src = __ffs(has) - 1;
+        f.tile = index - __shfl_sync(kAll, sum - mine.tiles, src);
+      } else {
+        index -= __shfl_sync(kAll, sum, 31);
+      }
     }
-    const uint32_t has = __ballot_sync(0xffffffffu, index < sum);
-    if (has != 0) {
-      const int src = __ffs(has) - 1;
-      f.tile = index - __shfl_sync(0xffffffffu, sum - mine.tiles, src);
-      f.tiles = __shfl_sync(0xffffffffu, mine.tiles, src);
-      f.q0 = __shfl_sync(0xffffffffu, mine.q0, src);
-      f.nq = __shfl_sync(0xffffffffu, mine.nq, src);
-      f.k0 = __shfl_sync(0xffffffffu, mine.k0, src);
-      f.nk = __shfl_sync(0xffffffffu, mine.nk, src);
+    if (src >= 0) {
+      f.tiles = __shfl_sync(kAll, mine.tiles, src);
+      f.q0 = __shfl_sync(kAll, mine.q0, src);
+      f.nq = __shfl_sync(kAll, mine.nq, src);
+      f.k0 = __shfl_sync(kAll, mine.k0, src);
+      f.nk = __shfl_sync(kAll, mine.nk, src);
       return f;
     }
-    index -= __shfl_sync(0xffffffffu, sum, 31);
   }
   return f;
 }
@@ -210,7 +236,8 @@ __device__ __forceinline__ Place find_tile(const int32_t* q_starts, const int32_
 // A CTA (or a pair) that is done takes the place of one that has not begun yet
 // (clusterlaunchcontrol): tiles go out in the grid's order to whoever is free, and what a launch
 // costs each (barriers, TMEM, the search for its sequence, the first loads) is paid once or hidden.
-// One warp asks, looks the tile up and leaves it for the others a tile ahead.
+// One warp asks, looks the tile up and leaves it for the others, once the loading warp has begun
+// its last loads of the tile before: no CTA holds work that an idle one could have.
 
 // Ask for a CTA (cluster) to cancel: 16 bytes at the same place in every CTA of the cluster, which
 // complete on each one's `bar`.
@@ -246,6 +273,21 @@ __device__ __forceinline__ int32_t clc_answer(const void* response) {
   return canceled != 0u ? static_cast<int32_t>(x) : -1;
 }
 
+// The grid's order: heads in sets of `set` whose other side (what the tiles stream through) stays
+// in L2, within a set tile by tile, the set's heads side by side.
+struct Order {
+  int32_t heads, set, tiles;             // tiles: the most that there can be
+};
+
+inline Order grid_order(int64_t heads, int64_t tiles, double bytes_per_head, bool causal) {
+  // (a causal grid whose heads all fit is one set: its heavy tiles all go out first)
+  const double whole = causal ? 70e6 : 0.0, set_bytes = 32e6;
+  int64_t set = heads;
+  if (heads * bytes_per_head > whole)
+    set = std::max<int64_t>(1, std::min<int64_t>(heads, static_cast<int64_t>(set_bytes / std::max(bytes_per_head, 1.0))));
+  return {static_cast<int32_t>(heads), static_cast<int32_t>(set), static_cast<int32_t>(tiles)};
+}
+
 struct Work {
   Place at;
   int32_t head;                          // < 0: no more
@@ -254,6 +296,7 @@ struct Work {
 struct Schedule {
   uint4 response;
   uint64_t clc_bar, clc_free;            // an answer is there; both CTAs have read it (the even's)
+  uint64_t want;                         // the loading warp wants more (the even's)
   uint64_t full[2], empty[2];
   Work work[2];
 };
@@ -263,17 +306,18 @@ template <int CG>
 __device__ __forceinline__ void schedule_init(Schedule* s, int readers) {
   mbar_init(&s->clc_bar, 1);
   mbar_init(&s->clc_free, CG);
+  mbar_init(&s->want, 1);
   for (int i = 0; i < 2; ++i) {
     mbar_init(&s->full[i], 1);
     mbar_init(&s->empty[i], readers);
   }
 }
 
-// The warp that asks: work after work, `per` rows a tile, `heads` of them side by side in the grid.
+// The warp that asks: work after work, `per` rows a tile.
 template <int CG>
 __device__ __forceinline__ void schedule(Schedule* s, const int32_t* q_starts,
                                          const int32_t* k_starts, int64_t Tq, int64_t Tk,
-                                         int sequences, int32_t heads, int32_t per, bool keys,
+                                         int sequences, const Order& order, int32_t per, bool keys,
                                          int rank, DeviceError* err, uint64_t limit_ns) {
   const int lane = threadIdx.x & 31;
   int32_t cta = static_cast<int32_t>(blockIdx.x);
@@ -282,9 +326,10 @@ __device__ __forceinline__ void schedule(Schedule* s, const int32_t* q_starts,
     Work w;
     w.head = -1;
     if (cta >= 0) {
-      const int32_t work = cta / CG;
-      w.head = work % heads;
-      w.at = find_tile(q_starts, k_starts, Tq, Tk, sequences, work / heads, per, keys);
+      const int32_t work = cta / CG, span = order.set * order.tiles, first = work / span * order.set;
+      const int32_t set = min(order.set, order.heads - first), at = work % span;
+      w.head = first + at % set;
+      w.at = find_tile(q_starts, k_starts, Tq, Tk, sequences, at / set, per, keys);
     }
     if (!warp_wait_all(&s->empty[i], (n >> 1 & 1) ^ 1, err, 31, limit_ns)) return;
     if (lane == 0) {
@@ -295,6 +340,7 @@ __device__ __forceinline__ void schedule(Schedule* s, const int32_t* q_starts,
     if (cta < 0) return;
     // (the answer's place is free: both CTAs have read the last one)
     if (rank == 0 && n > 0 && !warp_wait_all(&s->clc_free, (n - 1) & 1, err, 32, limit_ns)) return;
+    if (rank == 0 && !warp_wait_all(&s->want, n & 1, err, 35, limit_ns)) return;
     if (elect_one()) {
       mbar_arrive_expect_tx(&s->clc_bar, 16);
       if (rank == 0) clc_try_cancel<CG>(&s->response, &s->clc_bar);
@@ -314,6 +360,12 @@ __device__ __forceinline__ void schedule(Schedule* s, const int32_t* q_starts,
     }
     __syncwarp();
   }
+}
+
+// The even CTA's loading warp asks for the work behind its n-th.
+__device__ __forceinline__ void want_work(Schedule* s) {
+  if (elect_one()) mbar_arrive(&s->want);
+  __syncwarp();
 }
 
 // A reader's next work, the n-th; false after the last.
