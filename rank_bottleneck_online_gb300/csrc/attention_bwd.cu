@@ -703,7 +703,7 @@ cudaError_t launch_pass(BwdParams p, int64_t T, cudaStream_t stream) {
   // the other side: k and v of a key head, or q and dout of its query heads
   const double bytes = 4.0 * p.dim * (PASS == kDq ? static_cast<double>(p.Tk) / p.group
                                                   : static_cast<double>(p.Tq) * p.group);
-  p.order = grid_order(p.order.heads, most_tiles(T, CG * kTile, p.sequences), bytes, p.causal != 0);
+  p.order = grid_order(p.order.heads, most_tiles(T, CG * kTile, p.sequences), bytes);
   static std::atomic<bool> ready[64];    // per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

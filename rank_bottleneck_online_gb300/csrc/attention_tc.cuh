@@ -279,12 +279,10 @@ struct Order {
   int32_t heads, set, tiles;             // tiles: the most that there can be
 };
 
-inline Order grid_order(int64_t heads, int64_t tiles, double bytes_per_head, bool causal) {
-  // (a causal grid whose heads all fit is one set: its heavy tiles all go out first)
-  const double whole = causal ? 70e6 : 0.0, set_bytes = 32e6;
-  int64_t set = heads;
-  if (heads * bytes_per_head > whole)
-    set = std::max<int64_t>(1, std::min<int64_t>(heads, static_cast<int64_t>(set_bytes / std::max(bytes_per_head, 1.0))));
+inline Order grid_order(int64_t heads, int64_t tiles, double bytes_per_head) {
+  constexpr double kSet = 32e6;          // of 129 MB of L2
+  const double fit = kSet / std::max(bytes_per_head, 1.0);
+  const int64_t set = std::max<int64_t>(1, std::min<int64_t>(heads, static_cast<int64_t>(fit)));
   return {static_cast<int32_t>(heads), static_cast<int32_t>(set), static_cast<int32_t>(tiles)};
 }
 

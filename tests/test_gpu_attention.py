@@ -101,6 +101,21 @@ def test_one_token_over_a_long_context(nq):
     Case([(nq, 30000), (nq, 1), (nq, 129), (nq, 9999)], 5, 1, 128, seed=9).check()
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hk,dim", [(4, 4, 64), (6, 2, 128), (32, 1, 72), (40, 1, 128)])
+@pytest.mark.parametrize("lengths", [[(1, 1100)], [(2, 1500), (0, 700), (1, 0), (3, 2049), (1, 640)],
+                                     [(4, 900)] * 5 + [(1, 1)], [(12, 3000), (1, 5)]])
+def test_parts_of_the_keys(lengths, hq, hk, dim, causal):
+    """Few queries over many keys: the keys go in parts, joined at the end."""
+    Case(lengths, hq, hk, dim, causal=causal, tail=2, seed=dim).check()
+
+
+def test_equal_parts_of_the_keys():
+    """More queries than a tile's, but too few tiles for the SMs."""
+    Case([(300, 6000), (200, 3000)], 2, 2, 128, seed=20).check()
+    Case([(400, 5000)], 1, 1, 64, causal=False, seed=21).check()
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("dim", [64, 128])
 def test_other_sequences_do_not_leak(bad, dim):
