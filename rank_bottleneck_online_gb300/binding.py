@@ -910,19 +910,28 @@ def grad_clip(grads, max_norm, ws: Workspace, *, outs=None, norm=None, stream=No
         raise ValueError(f"{len(outs)} outs for {len(grads)} gradients")
     if norm is None:
         norm = torch.empty((1,), dtype=torch.float32, device=ws.buf.device)
-    table = (Grad * len(grads))()
-    bf, wide = torch.bfloat16, torch.float32
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        dtype, shape = g.dtype, g.shape
-        if dtype is not bf and dtype is not wide:
-            raise TypeError(f"gradient {i} must be bfloat16 or float32, got {dtype}")
-        at = _take(g, f"gradient {i}", dtype, shape, device)
-        to = None
-        if max_norm is not None:
-            to = at if o is g else _take(o, f"out {i}", dtype, shape, device)
-        table[i] = (at, to, g.numel(), dtype is wide)
+    # (a model has hundreds: whole lists at a time, and the words for what is wrong afterwards)
+    n, bf, wide = len(grads), torch.bfloat16, torch.float32
+    types, sizes = [g.dtype for g in grads], [g.numel() for g in grads]
+    fine = (all(d is bf or d is wide for d in types)
+            and all(g.is_contiguous() and g.get_device() == device for g in grads))
+    if outs is not grads:
+        fine = fine and all(o.dtype is d and o.shape == g.shape and o.is_contiguous()
+                            and o.get_device() == device for o, g, d in zip(outs, grads, types))
+    if not fine:
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if g.dtype is not bf and g.dtype is not wide:
+                raise TypeError(f"gradient {i} must be bfloat16 or float32, got {g.dtype}")
+            _take(g, f"gradient {i}", g.dtype, g.shape, device)
+            _take(o, f"out {i}", g.dtype, g.shape, device)
+    at = [g.data_ptr() for g in grads]
+    to = [0] * n if max_norm is None else at if outs is grads else [o.data_ptr() for o in outs]
+    # the table of Grad entries: four words each
+    words = [0] * (4 * n)
+    words[0::4], words[1::4], words[2::4], words[3::4] = at, to, sizes, [d is wide for d in types]
+    table = (ctypes.c_int64 * (4 * n))(*words)
     _check(lib().boost_grad_clip(
-        len(grads), table, float("inf") if max_norm is None else max_norm,
+        n, ctypes.cast(table, ctypes.POINTER(Grad)), float("inf") if max_norm is None else max_norm,
         _take(norm, "norm", wide, (1,), device), _on(ws.buf, "ws", torch.uint8, device), ws.nbytes,
         _raw_stream(stream, device)), "boost_grad_clip")
     return norm

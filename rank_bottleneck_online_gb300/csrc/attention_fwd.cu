@@ -13,8 +13,11 @@
 // before that.
 //
 // Query heads that share a key head share a tile: its rows are `pack` heads of 128 / pack tokens.
-// Where the tiles leave SMs idle, a tile's keys are split over several CTAs, whose parts (fp32,
-// with their own sums) a second kernel joins in order.
+// Where the tiles leave SMs idle, a tile's keys are split, and the parts (fp32, with their own
+// sums) joined in order by a second kernel: into equal parts, or, where all queries are a
+// single tile's (a decoding step), into parts of a fixed number of key tiles, so that long and
+// short sequences fill the SMs alike. There A and B are the same queries, A with the even and B
+// with the odd tiles of a part: two steps of a chain of load, product, softmax, product at a time.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -40,7 +43,7 @@ struct FwdParams {
   int32_t pack, tok;                     // heads and tokens of a tile
   Order order;                           // of hq / pack heads
   int32_t group;                         // of them that share a key head
-  int32_t splits;
+  int32_t splits, chunk;                 // equal parts of a tile's keys; or key tiles of a part (or 0)
   float scale_log2;
   DeviceError* err;
   uint64_t wait_limit_ns;
@@ -60,7 +63,7 @@ struct FwdCfg {
 
 constexpr float kSlack = 8.0f;           // log2 of the largest P
 
-template <int HD>
+template <int HD, bool OWN>
 __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     attention_fwd_kernel(const __grid_constant__ FwdParams p) {
   using Cfg = FwdCfg<HD>;
@@ -115,25 +118,33 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
   const int32_t first_head = static_cast<int32_t>(blockIdx.x) / span * p.order.set;
   const int32_t set = min(p.order.set, p.order.heads - first_head);
   const int32_t in_set = static_cast<int32_t>(blockIdx.x) % span, head = first_head + in_set % set;
-  Place at = find_tile(p.q_starts, p.k_starts, p.Tq, p.Tk, p.sequences, in_set / set, 2 * p.tok, false);
-  const int32_t t0 = (at.tiles - 1 - at.tile) * 2 * p.tok;       // first token in the sequence
+  constexpr bool own = OWN;                                       // A and B have keys of their own
+  Place at = find_tile(p.q_starts, p.k_starts, p.Tq, p.Tk, p.sequences, in_set / set,
+                       own ? p.chunk * kTile : 2 * p.tok, own);
+  const int32_t t0 = own ? 0 : (at.tiles - 1 - at.tile) * 2 * p.tok;   // first token in the sequence
+  const int32_t apart = own ? 0 : p.tok;                          // from A's to B's
   const int32_t off = at.nk - at.nq;                              // keys before the first query
   // key tiles [first, first + n) of each, and of this split alone
   int32_t n[2], first = 0;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    const int32_t begin = t0 + x * p.tok, last = min(begin + p.tok, at.nq) - 1;
+    const int32_t begin = t0 + x * apart, last = min(begin + p.tok, at.nq) - 1;
     int32_t keys = 0;
     if (at.tiles > 0 && last >= begin) keys = p.causal ? min(at.nk, last + off + 1) : at.nk;
     n[x] = keys > 0 ? (keys + kTile - 1) / kTile : 0;
   }
-  if (p.splits > 1) {
+  if (own) {
+    first = at.tile * p.chunk;
+    const int32_t all = max(min(n[0] - first, p.chunk), 0);
+    n[0] = (all + 1) / 2;
+    n[1] = all / 2;
+  } else if (p.splits > 1) {
     const int32_t most = max(n[0], n[1]), each = (most + p.splits - 1) / p.splits;
     first = static_cast<int32_t>(blockIdx.y) * each;
     n[0] = max(min(n[0] - first, each), 0);
     n[1] = max(min(n[1] - first, each), 0);
   }
-  const int32_t steps = max(n[0], n[1]);
+  const int32_t steps = own ? n[0] + n[1] : max(n[0], n[1]);      // key tiles
   const int ksteps = (p.dim + 15) / 16;
 
   if (warp == 0) {
@@ -149,20 +160,29 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
           if (n[x] > 0)
             for (int b = 0; b < Cfg::kBoxes; ++b)
               tma_load_3d(sQ + x * Cfg::kTileBytes + b * kBoxBytes, &p.tmQ, q_bar, 64 * b,
-                          head * p.pack, at.q0 + t0 + x * p.tok);
+                          head * p.pack, at.q0 + t0 + x * apart);
       }
       __syncwarp();
       int stage = 0;
       uint32_t phase = 0;
+      // K of the first step (of A's and B's); then V and the K that comes next
+      const int32_t ahead = own ? min(2, steps) : 1;
       for (int32_t i = 0; i < 2 * steps; ++i) {
+        int32_t tile = i;
+        bool v = false;
+        if (i >= ahead) {
+          const int32_t r = i - ahead, whole = 2 * (steps - ahead);
+          v = r >= whole || !(r & 1);
+          tile = r >= whole ? steps - ahead + r - whole : (r >> 1) + (v ? 0 : ahead);
+        }
         if (!warp_wait_all(&empty_bar[stage], phase ^ 1u, p.err, 41, p.wait_limit_ns)) break;
         armed |= 1u << stage;
         parities = (parities & ~(1u << stage)) | (phase << stage);
         if (elect_one()) {
           mbar_arrive_expect_tx(&full_bar[stage], Cfg::kTileBytes);
           for (int b = 0; b < Cfg::kBoxes; ++b)
-            tma_load_3d(sKV + stage * Cfg::kTileBytes + b * kBoxBytes, i & 1 ? &p.tmV : &p.tmK,
-                        &full_bar[stage], 64 * b, kh, at.k0 + (first + (i >> 1)) * kTile);
+            tma_load_3d(sKV + stage * Cfg::kTileBytes + b * kBoxBytes, v ? &p.tmV : &p.tmK,
+                        &full_bar[stage], 64 * b, kh, at.k0 + (first + tile) * kTile);
         }
         __syncwarp();
         if (++stage == Cfg::kStages) {
@@ -194,7 +214,42 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     };
     bool ok = steps > 0 && warp_wait_all(q_bar, 0, p.err, 42, p.wait_limit_ns) &&
               warp_wait_all(&full_bar[0], 0, p.err, 43, p.wait_limit_ns);
-    if (ok) {
+    // tiles of their own: tile i is A's or B's in turn
+    for (int32_t i = -2; own && ok && i < steps; ++i) {
+      const int x = i & 1;
+      const uint32_t s_tm = tS[0] + kTile * x;
+      if (i >= 0) {                                      // O_x += P_x V
+        const int32_t left = at.nk - (first + i) * kTile;
+        ok = warp_wait_all(&full_bar[stage], phase, p.err, 44, p.wait_limit_ns);
+        if (ok && left < kTile)
+          zero_rows(sKV + stage * Cfg::kTileBytes, Cfg::kBoxes, kTile, left, lane);
+        ok = ok && warp_wait_all(&p_bar[x], i >> 1 & 1, p.err, 46, p.wait_limit_ns);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = v_desc + stage * kStep;
+        if (elect_one()) {
+          issue_sums<1, kTile>(tO[0] + HD * x, s_tm, vd, id_o, i > 1);
+          tc_commit(&empty_bar[stage]);
+          if (i + 2 >= steps) tc_commit(&o_bar[x]);
+        }
+        __syncwarp();
+        next();
+      }
+      if (i + 2 < steps) {                               // S_x = Q K^T
+        ok = warp_wait_all(&full_bar[stage], phase, p.err, 45, p.wait_limit_ns);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t kd = k_desc + stage * kStep;
+        if (elect_one()) {
+          issue_scores<1, HD / 16>(s_tm, q_desc[0], kd, id_s, ksteps);
+          tc_commit(&s_bar[x]);
+          tc_commit(&empty_bar[stage]);
+        }
+        __syncwarp();
+        next();
+      }
+    }
+    if (ok && !own) {
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -208,7 +263,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
       __syncwarp();
       next();
     }
-    for (int32_t j = 0; j < steps && ok; ++j) {
+    for (int32_t j = 0; j < steps && ok && !own; ++j) {
       const int v_stage = stage;
       ok = warp_wait_all(&full_bar[stage], phase, p.err, 44, p.wait_limit_ns);
       next();
@@ -255,10 +310,12 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     const int x = (warp >> 2) - 1, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_at = tS[x] + lane_base, o_at = tO[x] + lane_base;
-    const int32_t tq = t0 + x * p.tok + row / p.pack;     // token in the sequence
+    const int32_t tq = t0 + x * apart + row / p.pack;     // token in the sequence
     const bool valid = row < p.pack * p.tok && tq < at.nq;
-    // keys that this row sees, from this CTA's first
-    const int32_t sees = (p.causal ? min(at.nk, tq + off + 1) : at.nk) - first * kTile;
+    // keys that this row sees, from its first tile, and how far its tiles are apart
+    const int32_t sees =
+        (p.causal ? min(at.nk, tq + off + 1) : at.nk) - (first + (own ? x : 0)) * kTile;
+    const int32_t step = own ? 2 * kTile : kTile;
     float m = -CUDART_INF_F, l = 0.0f;                    // reference in S's units, sum of P
     bool ok = true;
     for (int32_t j = 0; j < n[x]; ++j) {
@@ -272,7 +329,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
       for (int c = 0; c < 4; ++c)
         tmem_ld_32x32b_x32(s_at + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
       tmem_ld_wait();
-      const int32_t lim = sees - j * kTile;
+      const int32_t lim = sees - j * step;
       if (__any_sync(0xffffffffu, lim < kTile)) {
 #pragma unroll
         for (int c = 0; c < 128; ++c) s[c] = c < lim ? s[c] : -CUDART_INF_F;
@@ -333,10 +390,12 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
       const int64_t token = at.q0 + static_cast<int64_t>(tq);
       const int32_t h = head * p.pack + row % p.pack;
       __nv_bfloat16* dst = p.out.row(token, h);
-      const int64_t item = (static_cast<int64_t>(blockIdx.y) * p.Tq + token) * p.hq + h;
+      const bool parts = own || p.splits > 1;
+      const int32_t part_index = own ? 2 * at.tile + x : static_cast<int32_t>(blockIdx.y);
+      const int64_t item = (static_cast<int64_t>(part_index) * p.Tq + token) * p.hq + h;
       float* part = p.part + item * p.dim;
       if (valid) {
-        if (p.splits > 1)
+        if (parts)
           p.part_lse[item] = lse2;
         else if (p.lse != nullptr)
           p.lse[h * p.Tq + token] = lse2 * kLn2;
@@ -357,7 +416,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = inv == 0.0f ? 0.0f : o[i + e] * inv;
-            if (p.splits > 1) {
+            if (parts) {
               *reinterpret_cast<float4*>(part + c + i) = make_float4(f[0], f[1], f[2], f[3]);
               *reinterpret_cast<float4*>(part + c + i + 4) = make_float4(f[4], f[5], f[6], f[7]);
             } else {
@@ -376,31 +435,78 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
   }
 }
 
-// Joins the splits of a row's keys: a warp a row of one head.
+// Joins the parts of a row's keys: a block a row of one head, its warps take parts in turn, and
+// the warps' sums are added in their order. (A warp alone a row took 22 us for the 100 parts of the
+// longest of eight rows of 40 heads, one load after another; a block 4.)
 __global__ void __launch_bounds__(kThreads) attention_join_kernel(const FwdParams p) {
   pdl_enter();
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int64_t rows = p.Tq * p.hq;
-  if (item >= rows) return;
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float4 sums[kWarps][32];
+  __shared__ float tops[kWarps], totals[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t item = blockIdx.x, rows = p.Tq * p.hq;
   const int32_t token = static_cast<int32_t>(item / p.hq), h = static_cast<int32_t>(item % p.hq);
-  bool in = false;                                       // rows of no sequence stay
+  int32_t keys = -1;                                     // rows of no sequence stay
   for (int s = lane; s < p.sequences; s += 32) {
-    int32_t q0, nq;
+    int32_t q0, nq, k0, nk;
     sequence_bounds(p.q_starts, p.Tq, s, q0, nq);
-    in |= token >= q0 && token < q0 + nq;
+    sequence_bounds(p.k_starts, p.Tk, s, k0, nk);
+    if (token >= q0 && token < q0 + nq) keys = nk;
   }
-  if (!__any_sync(0xffffffffu, in)) return;
-  float top = -CUDART_INF_F;
-  for (int i = 0; i < p.splits; ++i) top = fmaxf(top, p.part_lse[i * rows + item]);
-  const float base = top == -CUDART_INF_F ? 0.0f : top;
-  float sum = 0.0f, o[4] = {};
+  keys = __reduce_max_sync(0xffffffffu, keys);
+  if (keys < 0) return;                                  // (the whole block)
+  // (a sequence has two parts for each `chunk` tiles of its keys)
+  const int32_t step = p.chunk * kTile, parts = step > 0 ? 2 * ((keys + step - 1) / step) : p.splits;
+  float top = -CUDART_INF_F, sum = 0.0f, o[4] = {};
   const int c = lane * 4;
-  for (int i = 0; i < p.splits; ++i) {
-    const float w = exp2_fast(p.part_lse[i * rows + item] - base);
-    sum += w;
-    if (c < p.dim && w != 0.0f) {
-      const float4 v = *reinterpret_cast<const float4*>(p.part + (i * rows + item) * p.dim + c);
+  for (int i0 = warp; i0 < parts; i0 += 4 * kWarps) {
+    float l[4];
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * kWarps;
+      l[k] = -CUDART_INF_F;
+      v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i < parts) {
+        l[k] = p.part_lse[i * rows + item];
+        if (c < p.dim) v[k] = *reinterpret_cast<const float4*>(p.part + (i * rows + item) * p.dim + c);
+      }
+    }
+    float next = top;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) next = fmaxf(next, l[k]);
+    const float base = next == -CUDART_INF_F ? 0.0f : next, f = exp2_fast(top - base);
+    sum *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] *= f;
+    top = next;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float w = exp2_fast(l[k] - base);
+      sum += w;
+      if (w != 0.0f) {                                   // (a part of no keys counts nothing)
+        o[0] = fmaf(w, v[k].x, o[0]); o[1] = fmaf(w, v[k].y, o[1]);
+        o[2] = fmaf(w, v[k].z, o[2]); o[3] = fmaf(w, v[k].w, o[3]);
+      }
+    }
+  }
+  sums[warp][lane] = make_float4(o[0], o[1], o[2], o[3]);
+  if (lane == 0) {
+    tops[warp] = top;
+    totals[warp] = sum;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int i = 1; i < kWarps; ++i) top = fmaxf(top, tops[i]);
+  const float base = top == -CUDART_INF_F ? 0.0f : top;
+  sum = o[0] = o[1] = o[2] = o[3] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    const float w = exp2_fast(tops[i] - base);
+    const float4 v = sums[i][lane];
+    sum = fmaf(w, totals[i], sum);
+    if (w != 0.0f) {
       o[0] = fmaf(w, v.x, o[0]); o[1] = fmaf(w, v.y, o[1]);
       o[2] = fmaf(w, v.z, o[2]); o[3] = fmaf(w, v.w, o[3]);
     }
@@ -418,23 +524,44 @@ int packed_heads(const boost_attention_desc& d) {
   return group <= 32 ? group : 1;        // (128 / 33 tokens would leave a fifth of the rows idle)
 }
 
-int64_t tile_pairs(const boost_attention_desc& d) {
-  return most_tiles(d.Tq, 2 * (kTile / packed_heads(d)), d.sequences);
+// How a call's work is cut.
+struct FwdPlan {
+  int pack, tok, splits, chunk, parts;
+  int64_t tiles;                         // of a head: pairs of tiles of queries, or parts of keys
+};
+
+FwdPlan plan(const boost_attention_desc& d) {
+  FwdPlan f{};
+  f.pack = packed_heads(d);
+  f.tok = kTile / f.pack;
+  f.splits = f.parts = 1;
+  const int64_t heads = d.hq / f.pack, keys = (d.Tk + kTile - 1) / kTile;
+  // All queries are a tile's: parts of the keys of a fixed length, three for each SM, but long
+  // enough that the parts' own traffic stays below half of the keys' and values'.
+  if (d.Tq <= f.tok) {
+    const int64_t rows = d.Tq / d.sequences * f.pack;
+    const int64_t chunk = std::max<int64_t>({4, rows / 16, (keys * heads + 455) / 456});
+    if (keys > chunk) {
+      f.chunk = static_cast<int>(std::min<int64_t>(chunk, 1 << 20));
+      f.parts = static_cast<int>(2 * ((keys + f.chunk - 1) / f.chunk));
+      f.tiles = most_tiles(d.Tk, static_cast<int64_t>(f.chunk) * kTile, d.sequences);
+      return f;
+    }
+  }
+  // Else as many equal parts as fill the SMs, each with four tiles of an average sequence's keys.
+  f.tiles = most_tiles(d.Tq, 2 * f.tok, d.sequences);
+  const int64_t ctas = f.tiles * heads;
+  if (ctas > 0)
+    f.splits = static_cast<int>(
+        std::max<int64_t>(1, std::min<int64_t>({304 / ctas, d.Tk / d.sequences / kTile / 4, 64})));
+  f.parts = f.splits;
+  return f;
 }
 
-// CTAs that share a tile's keys: as many as fill the SMs, each with four tiles of an average
-// sequence's keys at least.
-int key_splits(const boost_attention_desc& d) {
-  const int64_t ctas = tile_pairs(d) * (d.hq / packed_heads(d));
-  const int64_t tiles = d.Tk / d.sequences / kTile;
-  if (ctas == 0) return 1;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({304 / ctas, tiles / 4, 64})));
-}
-
-template <int HD>
+template <int HD, bool OWN>
 cudaError_t launch_fwd(const FwdParams& p, cudaStream_t stream) {
   using Cfg = FwdCfg<HD>;
-  const auto kern = attention_fwd_kernel<HD>;
+  const auto kern = attention_fwd_kernel<HD, OWN>;
   static std::atomic<bool> ready[64];    // per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -460,8 +587,9 @@ cudaError_t launch_fwd(const FwdParams& p, cudaStream_t stream) {
 }  // namespace
 
 size_t attention_workspace(const boost_attention_desc& d) {
-  const size_t rows = static_cast<size_t>(d.hq) * d.Tq, splits = key_splits(d);
-  const size_t fwd = splits > 1 ? 4 * splits * rows * (d.dim + 1) : 0;
+  const FwdPlan f = plan(d);
+  const size_t rows = static_cast<size_t>(d.hq) * d.Tq;
+  const size_t fwd = f.parts > 1 ? 4 * f.parts * rows * (d.dim + 1) : 0;
   return 256 + std::max(fwd, 4 * rows);                  // (the backward keeps a value a row)
 }
 
@@ -469,13 +597,14 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream) {
   const boost_attention_desc& d = a.d;
   FwdParams p;
   std::memset(&p, 0, sizeof(p));
-  p.pack = packed_heads(d);
-  p.tok = kTile / p.pack;
+  const FwdPlan f = plan(d);
+  p.pack = f.pack;
+  p.tok = f.tok;
   p.group = d.hq / p.pack / d.hk;
   // (With a causal mask all heads are one set: the tiles with most work, of every head, go out
   // first. 16384 tokens in four sequences, 16 heads: 225 us, in sets of three heads 254; without the
   // mask, where all have as much, 418 and 402.)
-  p.order = grid_order(d.hq / p.pack, tile_pairs(d), d.causal ? 0.0 : 4.0 * d.dim * d.Tk / p.group);
+  p.order = grid_order(d.hq / p.pack, f.tiles, d.causal ? 0.0 : 4.0 * d.dim * d.Tk / p.group);
   if (!heads_map(&p.tmQ, a.q.at, a.ws, d.Tq, d.hq, d.dim, d.q_ts, d.q_hs, p.pack, p.tok) ||
       !heads_map(&p.tmK, a.k.at, a.ws, d.Tk, d.hk, d.dim, d.k_ts, d.k_hs, 1, kTile) ||
       !heads_map(&p.tmV, a.v.at, a.ws, d.Tk, d.hk, d.dim, d.v_ts, d.v_hs, 1, kTile))
@@ -490,16 +619,21 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream) {
   p.dim = d.dim;
   p.sequences = d.sequences;
   p.causal = d.causal;
-  p.splits = key_splits(d);
+  p.splits = f.splits;
+  p.chunk = f.chunk;
   p.scale_log2 = d.scale * kLog2e;
   p.err = static_cast<DeviceError*>(a.ws);
   p.wait_limit_ns = wait_limit_ns();
   const int64_t rows = d.Tq * d.hq;
   p.part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + 256);
-  p.part_lse = p.part + p.splits * rows * d.dim;
-  cudaError_t e = d.dim <= 64 ? launch_fwd<64>(p, stream) : launch_fwd<128>(p, stream);
-  if (e != cudaSuccess || p.splits == 1) return e;
-  return launch_k(attention_join_kernel, (rows + kThreads / 32 - 1) / (kThreads / 32), stream, p);
+  p.part_lse = p.part + f.parts * rows * d.dim;
+  cudaError_t e = cudaSuccess;
+  if (f.tiles > 0 && f.chunk > 0)
+    e = d.dim <= 64 ? launch_fwd<64, true>(p, stream) : launch_fwd<128, true>(p, stream);
+  else if (f.tiles > 0)
+    e = d.dim <= 64 ? launch_fwd<64, false>(p, stream) : launch_fwd<128, false>(p, stream);
+  if (e != cudaSuccess || f.parts == 1) return e;
+  return launch_k(attention_join_kernel, rows, stream, p);
 }
 
 }  // namespace boost_gb300

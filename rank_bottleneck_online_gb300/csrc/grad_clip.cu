@@ -23,10 +23,14 @@ namespace boost_gb300 {
 
 namespace {
 
-constexpr int kTensors = 120;            // of one launch: 24 bytes each in 4 KB of parameters
-constexpr int kBlocks = 608;             // four an SM, and as many sums in the workspace
+constexpr int kBlocks = 1216;            // eight an SM, and as many sums in the workspace
 constexpr int kChunk = 8192;             // elements of one block's step
 
+// The tensors of one launch: 28 bytes each, in the 4 KB of parameters that any launch may have, or,
+// for more of them, in the 32 KB of a large one.
+constexpr int kFew = 120, kMany = 1100;
+
+template <int kTensors>
 struct ClipParams {
   const void* g[kTensors];
   void* out[kTensors];
@@ -38,9 +42,11 @@ struct ClipParams {
   float* norm;                           // of the last scaling launch, or NULL
   double max_norm;
 };
+static_assert(sizeof(ClipParams<kFew>) <= 4096 && sizeof(ClipParams<kMany>) <= 32764, "parameters");
 
 // The tensor of a chunk, and the chunk's place in it.
-__device__ __forceinline__ int tensor_of(const ClipParams& p, uint32_t chunk, int64_t& at) {
+template <int N>
+__device__ __forceinline__ int tensor_of(const ClipParams<N>& p, uint32_t chunk, int64_t& at) {
   int lo = 0, hi = p.tensors - 1;
   while (lo < hi) {
     const int mid = (lo + hi) / 2;
@@ -50,7 +56,8 @@ __device__ __forceinline__ int tensor_of(const ClipParams& p, uint32_t chunk, in
   return lo;
 }
 
-__device__ __forceinline__ bool is_wide(const ClipParams& p, int t) {
+template <int N>
+__device__ __forceinline__ bool is_wide(const ClipParams<N>& p, int t) {
   return p.wide[t >> 5] >> (t & 31) & 1u;
 }
 
@@ -66,7 +73,8 @@ __device__ __forceinline__ double block_sum(double v, double* shared) {
   return v;
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ ClipParams p) {
+template <int N>
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ ClipParams<N> p) {
   pdl_enter();
   __shared__ double shared[kThreads / 32];
   double sum = 0.0;
@@ -121,7 +129,8 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
   if (threadIdx.x == 0) p.sums[blockIdx.x] = (p.first ? 0.0 : p.sums[blockIdx.x]) + sum;
 }
 
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ ClipParams p) {
+template <int N>
+__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ ClipParams<N> p) {
   pdl_enter();
   __shared__ double shared[kThreads / 32];
   double sum = 0.0;
@@ -147,8 +156,8 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
           v[i] = *(reinterpret_cast<const float4*>(g) + i * kThreads + threadIdx.x);
 #pragma unroll
         for (int i = 0; i < kChunk / 4 / kThreads; ++i)
-          *(reinterpret_cast<float4*>(out) + i * kThreads + threadIdx.x) =
-              make_float4(v[i].x * f, v[i].y * f, v[i].z * f, v[i].w * f);
+          __stcs(reinterpret_cast<float4*>(out) + i * kThreads + threadIdx.x,
+                 make_float4(v[i].x * f, v[i].y * f, v[i].z * f, v[i].w * f));
       } else {
         for (int i = threadIdx.x; i < n; i += kThreads) out[i] = g[i] * f;
       }
@@ -166,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
           unpack8(v[i], x);
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] *= f;
-          *(reinterpret_cast<uint4*>(out) + i * kThreads + threadIdx.x) = pack8(x);
+          __stcs(reinterpret_cast<uint4*>(out) + i * kThreads + threadIdx.x, pack8(x));
         }
       } else {
         for (int i = threadIdx.x; i < n; i += kThreads)
@@ -201,6 +210,52 @@ bool outputs_meet(const boost_grad* grads, int64_t count) {
     if (s.output) written = std::max(written, s.end);
   }
   return false;
+}
+
+// The two passes over the tensors, N of them a launch.
+template <int N>
+cudaError_t launch(int64_t count, const boost_grad* grads, double max_norm, float* norm, double* sums,
+                   cudaStream_t s) {
+  std::vector<ClipParams<N>> launches;
+  for (int64_t i = 0; i < count; ++i) {
+    if (grads[i].n == 0) continue;
+    if (launches.empty() || launches.back().tensors == N) {
+      launches.emplace_back();
+      ClipParams<N>& p = launches.back();
+      std::fill(std::begin(p.wide), std::end(p.wide), 0u);
+      p.tensors = 0;
+      p.sums = sums;
+      p.max_norm = max_norm;
+      p.norm = nullptr;
+      p.first = launches.size() == 1;
+    }
+    ClipParams<N>& p = launches.back();
+    const int t = p.tensors++;
+    p.g[t] = grads[i].g;
+    p.out[t] = grads[i].out;
+    p.n[t] = grads[i].n;
+    p.end[t] = (t == 0 ? 0 : p.end[t - 1]) +
+               static_cast<uint32_t>((grads[i].n + kChunk - 1) / kChunk);
+    if (grads[i].wide) p.wide[t >> 5] |= 1u << (t & 31);
+  }
+  if (launches.empty()) return cudaMemsetAsync(norm, 0, 4, s);
+  // (every launch of the first pass has all blocks: each leaves its sum)
+  for (const ClipParams<N>& p : launches) {
+    const cudaError_t e = launch_k(grad_norm_kernel<N>, kBlocks, s, p);
+    if (e != cudaSuccess) return e;
+  }
+  launches.front().norm = norm;            // the last of the second pass
+  for (size_t i = launches.size(); i-- > 0;) {
+    ClipParams<N>& p = launches[i];
+    const bool writes = std::any_of(p.out, p.out + p.tensors, [](void* q) { return q != nullptr; });
+    if (!writes && i > 0) continue;
+    if (!writes) p.tensors = 0;
+    const int64_t grid = p.tensors == 0 ? 1 : std::min<int64_t>(p.end[p.tensors - 1], kBlocks);
+    const cudaError_t e = launch_k(grad_scale_kernel<N>, grid, s, p);
+    if (e != cudaSuccess) return e;
+  }
+  prof_note_kernels(static_cast<int>(2 * launches.size()) - 1);
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -247,43 +302,10 @@ boost_status boost_grad_clip(int64_t count, const boost_grad* grads, double max_
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ProfScope ps(s, K_GRAD_CLIP, 3.0 * values, bytes);
-  // the tensors in launches of kTensors
-  std::vector<ClipParams> launches;
-  for (int64_t i = 0; i < count; ++i) {
-    if (grads[i].n == 0) continue;
-    if (launches.empty() || launches.back().tensors == kTensors) {
-      launches.emplace_back();
-      ClipParams& p = launches.back();
-      std::fill(std::begin(p.wide), std::end(p.wide), 0u);
-      p.tensors = 0;
-      p.sums = reinterpret_cast<double*>(static_cast<char*>(ws) + 256);
-      p.max_norm = max_norm;
-      p.norm = nullptr;
-      p.first = launches.size() == 1;
-    }
-    ClipParams& p = launches.back();
-    const int t = p.tensors++;
-    p.g[t] = grads[i].g;
-    p.out[t] = grads[i].out;
-    p.n[t] = grads[i].n;
-    p.end[t] = (t == 0 ? 0 : p.end[t - 1]) +
-               static_cast<uint32_t>((grads[i].n + kChunk - 1) / kChunk);
-    if (grads[i].wide) p.wide[t >> 5] |= 1u << (t & 31);
-  }
-  if (launches.empty()) return cudaMemsetAsync(norm, 0, 4, s) == cudaSuccess ? BOOST_OK : BOOST_ERR_CUDA;
-  // (every launch of the first pass has all blocks: each leaves its sum)
-  for (const ClipParams& p : launches)
-    if (launch_k(grad_norm_kernel, kBlocks, s, p) != cudaSuccess) return BOOST_ERR_CUDA;
-  launches.front().norm = norm;            // the last of the second pass
-  for (size_t i = launches.size(); i-- > 0;) {
-    ClipParams& p = launches[i];
-    const bool writes = std::any_of(p.out, p.out + p.tensors, [](void* q) { return q != nullptr; });
-    if (!writes && i > 0) continue;
-    if (!writes) p.tensors = 0;
-    const int64_t grid = p.tensors == 0 ? 1 : std::min<int64_t>(p.end[p.tensors - 1], kBlocks);
-    if (launch_k(grad_scale_kernel, grid, s, p) != cudaSuccess) return BOOST_ERR_CUDA;
-  }
-  return BOOST_OK;
+  double* sums = reinterpret_cast<double*>(static_cast<char*>(ws) + 256);
+  const cudaError_t e = count <= kFew ? launch<kFew>(count, grads, max_norm, norm, sums, s)
+                                      : launch<kMany>(count, grads, max_norm, norm, sums, s);
+  return e == cudaSuccess ? BOOST_OK : BOOST_ERR_CUDA;
 } catch (...) {
   return BOOST_ERR_CUDA;                   // (host memory for the tables)
 }

@@ -183,7 +183,12 @@ extern "C" boost_status boost_norm_quantize(int64_t T, int64_t d, int32_t fmt, f
   p.T = T;
   p.d = d;
   p.eps = eps;
+  // Warps of a row: eight (or all that it has work for) where rows are few; else those whose turns
+  // over the row's tiles leave the fewest idle (8191 x 5120, ten tiles: 43 us with 8, 27 with 2).
   p.warps = p.kt >= 8 ? 8 : p.kt >= 4 ? 4 : p.kt >= 2 ? 2 : 1;
+  if (T >= 2048)
+    for (int w = p.warps / 2; w >= 1; w /= 2)
+      if ((p.kt + w - 1) / w * w < (p.kt + p.warps - 1) / p.warps * p.warps) p.warps = w;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const double n = static_cast<double>(T) * d;
   ProfScope ps(s, K_NORM_QUANT, 0.0,
