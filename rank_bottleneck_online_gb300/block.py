@@ -1,6 +1,6 @@
 """Workloads composed from the C-ABI calls: one block, the LLaMA MLP, the full
-layer without its attention core, and the SVD-style pair; a block whose forward
-multiplies in 8 bits; rotary positions and dropout in the layer.
+layer with or without its attention core, and the SVD-style pair; a block whose forward
+multiplies in 8 bits; rotary positions and dropout in the layer; clipping of their gradients.
 
 Each workload owns its device tensors (weights, saved activations, gradients
 and one workspace) so that a training step is a fixed sequence of library
@@ -57,15 +57,24 @@ class Block:
                            dgamma=self.dgamma, dA=self.dA, dB=self.dB, stream=stream,
                            dx_residual=dx_residual)
 
+    def weight_grads(self):
+        """The gradients of the weights."""
+        return [self.dA, self.dB] + ([self.dgamma] if self.dgamma is not None else [])
+
 
 class Fp8Block(Block):
     """A block whose forward multiplies in 8 bits: e4m3 weights quantised once, with gamma
     folded into A, in square blocks of 128; activations quantised row by row on the way. The
     1/rms scale and the activation stay in the down-projection's epilogue. The backward is the
-    bf16 block's on the bf16 weights, which this block keeps (straight-through)."""
+    bf16 block's on the bf16 weights, which this block keeps (straight-through).
 
-    def __init__(self, T, d, r, k, n, **kw):
+    fused_norm: the norm's statistics and the quantiser from one reading of x, together with the
+    addition of a residual to x where one is to be (``add``). The row scales' sums are taken in
+    another order than without it."""
+
+    def __init__(self, T, d, r, k, n, *, fused_norm=False, **kw):
         super().__init__(T, d, r, k, n, **kw)
+        self.fused_norm = fused_norm and bool(self.desc.has_norm)
         D = self.desc
         f8, bf, dev = torch.float8_e4m3fn, torch.bfloat16, self.device
 
@@ -94,13 +103,20 @@ class Fp8Block(Block):
                        stream=stream)
         B.fp8_quantize(self.B, way="columns", block_rows=128, cols_out=self.B8, stream=stream)
 
-    def forward(self, x, stream=None, residual=None):
+    def forward(self, x, stream=None, residual=None, add=None):
+        """add [T, d] (with ``fused_norm``): x is replaced by x + add, in place, first."""
         D = self.desc
         if residual is not None and D.k != 1:
             raise ValueError("a residual needs one output group")
-        if D.has_norm:
-            B.rmsnorm_stats(D, x, self.ssq, self.rstd, stream)
-        B.fp8_quantize(x, rows_out=self.x8, stream=stream)
+        if add is not None and not self.fused_norm:
+            raise ValueError("the addition in front belongs to the fused norm")
+        if self.fused_norm:
+            B.norm_quantize(x, residual=add, h=None if add is None else x, eps=D.eps,
+                            rstd=self.rstd, rows_out=self.x8, stream=stream)
+        else:
+            if D.has_norm:
+                B.rmsnorm_stats(D, x, self.ssq, self.rstd, stream)
+            B.fp8_quantize(x, rows_out=self.x8, stream=stream)
         B.fp8_matmul(*self.x8, *self.A8, D.d, self.ws8, row_scale=self.rstd, act=self.act,
                      out=self.a, stream=stream)
         groups = self.a.view(D.T, D.k, D.r).transpose(0, 1)
@@ -141,11 +157,44 @@ class Rotary:
                      for x, given, t in zip((q, k), (q_out, k_out), turned))
 
 
+class Attention:
+    """The layer's attention core: ``heads`` heads of ``dim`` values, causal unless told otherwise,
+    over packed sequences (``binding.attention``), with what its backward keeps."""
+
+    def __init__(self, T, heads, dim, *, causal=True, scale=None, sequences=1, device="cuda"):
+        """sequences: the most that a call has."""
+        self.T, self.heads, self.dim, self.causal, self.scale = T, heads, dim, causal, scale
+        self.out = torch.empty(T, heads * dim, dtype=torch.bfloat16, device=device)
+        self.lse = torch.empty(heads, T, dtype=torch.float32, device=device)
+        # (of fewer sequences, too: they may be cut in more parts)
+        self.workspace_bytes = max(B.attention_workspace_bytes(T, T, heads, heads, dim, s)
+                                   for s in range(1, sequences + 1))
+
+    def _split(self, t):
+        return t.view(self.T, self.heads, self.dim)
+
+    def forward(self, q, k, v, ws, starts=None, stream=None):
+        """out [T, heads * dim] of q, k, v of that shape; starts: int32 [sequences + 1]."""
+        B.attention(self._split(q), self._split(k), self._split(v), ws, causal=self.causal,
+                    scale=self.scale, q_starts=starts, k_starts=starts, out=self._split(self.out),
+                    lse=self.lse, stream=stream)
+        return self.out
+
+    def backward(self, q, k, v, dout, ws, dq, dk, dv, starts=None, stream=None):
+        """The last forward's gradients, into dq, dk and dv."""
+        s = self._split
+        B.attention_bwd(s(q), s(k), s(v), s(self.out), self.lse, s(dout), ws, causal=self.causal,
+                        scale=self.scale, q_starts=starts, k_starts=starts, dq=s(dq), dk=s(dk),
+                        dv=s(dv), stream=stream)
+        return dq, dk, dv
+
+
 class MLP:
     """LLaMA MLP of two bottlenecks: gate/up (normed, k=2) -> SwiGLU -> down (k=1)."""
 
     def __init__(self, T, d, r, ffn, *, S=1, eps=1e-5, act="silu", weights=None,
-                 device="cuda", ws=None, fused_glu=True, checkpoint="input", fp8=False):
+                 device="cuda", ws=None, fused_glu=True, checkpoint="input", fp8=False,
+                 fused_norm=False):
         w = weights or {}
         self.T, self.d, self.r, self.ffn = T, d, r, ffn
         # SwiGLU forward in the gate/up up-projection's epilogue, and its backward in the
@@ -165,10 +214,12 @@ class MLP:
         if fp8 and checkpoint != "input":
             raise ValueError("the bottleneck cut regenerates the bf16 block's activations")
         self.fp8 = fp8
+        if fused_norm and not fp8:
+            raise ValueError("the fused norm gives 8-bit values")
         block = Fp8Block if fp8 else Block
         self.gu = block(T, d, r, 2, ffn, S=S, eps=eps, act=act, has_norm=True,
                         weights={"gamma": w.get("gamma"), "A": w.get("A1"), "B": w.get("B1")},
-                        device=device, ws=ws)
+                        device=device, ws=ws, **({"fused_norm": fused_norm} if fp8 else {}))
         self.dn = block(T, ffn, r, 1, d, S=1, eps=eps, act=act, has_norm=False,
                         weights={"A": w.get("A2"), "B": w.get("B2")}, device=device,
                         ws=self.gu.ws if checkpoint == "input" else None)
@@ -184,14 +235,18 @@ class MLP:
     def out(self):
         return self.dn.y[0]
 
-    def forward(self, x, stream=None, residual=None):
-        """residual [T, d]: out = residual + MLP(x), added in the down block's epilogue."""
+    def forward(self, x, stream=None, residual=None, add=None):
+        """residual [T, d]: out = residual + MLP(x), added in the down block's epilogue. add
+        [T, d] (with ``fused_norm``): x is replaced by x + add, in place, first (so that residual
+        may be x itself)."""
+        if add is not None and not self.fp8:
+            raise ValueError("the addition in front belongs to the fused norm")
         if self.fused_glu and not self.fp8:
             gu = self.gu
             B.block_fwd_swiglu(gu.desc, x, gu.gamma, gu.A, gu.B, gu.ws, y=gu.y, h=self.h,
                                rstd=gu.rstd, stream=stream)
         else:
-            y1 = self.gu.forward(x, stream)
+            y1 = self.gu.forward(x, stream, **({} if add is None else {"add": add}))
             B.swiglu_fwd(y1[0], y1[1], self.h, stream=stream)
         return self.dn.forward(self.h, stream, residual=residual)[0]
 
@@ -225,9 +280,16 @@ class MLP:
         return {"dx": self.gu.dx, "dgamma": self.gu.dgamma, "dA1": self.gu.dA, "dB1": self.gu.dB,
                 "dA2": self.dn.dA, "dB2": self.dn.dB}
 
+    def weight_grads(self):
+        """The gradients of the weights."""
+        return self.gu.weight_grads() + self.dn.weight_grads()
+
 
 class Layer:
     """QKV (normed, k=3) -> O (k=1) on V -> residual -> MLP -> residual.
+
+    attention (an ``Attention``): O works on the attention of q, k and v, and the backward forms
+    their gradients; without it O works on V, and the gradients of q and k are given.
 
     Both residual adds run in GEMM epilogues: x1 = x + O(v) in the O block's
     up-projection, out = x1 + MLP(x1) in the MLP's down up-projection; in the backward,
@@ -239,29 +301,39 @@ class Layer:
     upstream gradient. dropout (p > 0): x1 = x + dropout(O(v)), out = x1 + dropout(MLP(x1)),
     with the masks of (``seed``, ``mask`` of the call) and none stored. Give the layers of a
     model different seeds, any ones: branches share a mask only where seed, mask and branch are
-    the same. fp8: the blocks' forward in 8 bits (``Fp8Block``)."""
+    the same. fp8: the blocks' forward in 8 bits (``Fp8Block``); fused_norm: theirs."""
 
     def __init__(self, T, d, r, ffn, *, S=1, eps=1e-5, act="silu", weights=None, device="cuda",
-                 rotary=None, dropout=0.0, seed=0, fp8=False):
+                 rotary=None, dropout=0.0, seed=0, fp8=False, attention=None, fused_norm=False):
         p = weights or {}
         self.T, self.d = T, d
         self.rotary, self.dropout, self.seed = rotary, dropout, seed
+        self.attention, self.fused_norm = attention, fused_norm
+        if attention is not None and (attention.T, attention.heads * attention.dim) != (T, d):
+            raise ValueError(f"the attention core is of {attention.T} tokens and {attention.heads} "
+                             f"heads of {attention.dim}, the layer of {T} x {d}")
+        if fused_norm and not fp8:
+            raise ValueError("the fused norm gives 8-bit values")
         block = Fp8Block if fp8 else Block
         self.qkv = block(T, d, r, 3, d, S=S, eps=eps, act=act, has_norm=True,
                          weights={"gamma": p.get("gamma1"), "A": p.get("A_qkv"),
-                                  "B": p.get("B_qkv")}, device=device)
+                                  "B": p.get("B_qkv")}, device=device,
+                         **({"fused_norm": fused_norm} if fp8 else {}))
         ws = self.qkv.ws
         self.o = block(T, d, r, 1, d, S=1, eps=eps, act=act, has_norm=False,
                        weights={"A": p.get("A_o"), "B": p.get("B_o")}, device=device, ws=ws)
         self.mlp = MLP(T, d, r, ffn, S=S, eps=eps, act=act,
                        weights={"gamma": p.get("gamma2"), "A1": p.get("A_gu"), "B1": p.get("B_gu"),
                                 "A2": p.get("A_dn"), "B2": p.get("B_dn")}, device=device, ws=ws,
-                       fp8=fp8)
+                       fp8=fp8, fused_norm=fused_norm)
         ws = self.mlp.gu.ws
         for blk in (self.qkv, self.o):
             blk.ws = ws
         dev = self.qkv.device
         self.dqkv = torch.empty(3, T, d, dtype=torch.bfloat16, device=dev)
+        if attention is not None:
+            ws.ensure(attention.workspace_bytes)
+            self.dattention = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
         # gradient of a branch behind its dropout
         self.dbranch = torch.empty(T, d, dtype=torch.bfloat16, device=dev) if dropout else None
 
@@ -305,27 +377,51 @@ class Layer:
         return B.dropout_bwd(grad, self.dropout, *self._words(which, mask), dx=self.dbranch,
                              counter=counter, stream=stream)
 
-    def forward(self, x, stream=None, positions=None, mask=0, counter=None):
+    def forward(self, x, stream=None, positions=None, mask=0, counter=None, starts=None):
         """positions ([T] or [axes, T]): those of the tokens, with ``rotary``. mask: which
         dropout masks (plus ``counter``, a device value, as in ``binding.dropout_add``), below
-        2^63 together."""
+        2^63 together. starts: where the packed sequences begin (int32 [sequences + 1], on the
+        device; from 0 to T, so that every row has an output), with ``attention``."""
+        if starts is not None and self.attention is None:
+            raise ValueError("sequences without an attention core")
         qkv = self.qkv.forward(x, stream)
         if self.rotary is not None:
             self.rotary(qkv[0], qkv[1], positions, q_out=qkv[0], k_out=qkv[1], stream=stream)
+        v = qkv[2]
+        if self.attention is not None:
+            v = self.attention.forward(qkv[0], qkv[1], v, self.qkv.ws, starts, stream)
         if not self.dropout:
-            x1 = self.o.forward(qkv[2], stream, residual=x)[0]
+            if self.fused_norm:
+                x1 = self.o.forward(v, stream)[0]
+                return self.mlp.forward(x1, stream, residual=x1, add=x)
+            x1 = self.o.forward(v, stream, residual=x)[0]
             return self.mlp.forward(x1, stream, residual=x1)
-        x1 = self._join(self.o.forward(qkv[2], stream)[0], x, 0, mask, counter, stream)
+        x1 = self._join(self.o.forward(v, stream)[0], x, 0, mask, counter, stream)
         return self._join(self.mlp.forward(x1, stream), x1, 1, mask, counter, stream)
 
-    def backward(self, x, dout, dq, dk, stream=None, positions=None, mask=0, counter=None):
-        """dq, dk: the attention core's gradients of q and k (the turned ones, with
+    def backward(self, x, dout, dq=None, dk=None, stream=None, positions=None, mask=0,
+                 counter=None, starts=None):
+        """With ``attention`` its gradients of q, k and v are formed here (starts: the forward's).
+        Else dq, dk: the attention core's gradients of q and k (the turned ones, with
         ``rotary``). The QKV block's upstream gradient is the stacked [dq, dk, dv]; dq and
         dk are turned back or copied into it (copied unless they are already its first two
         planes, `dqkv[0]`, `dqkv[1]`), and the O block writes dv straight into the third.
         positions, mask, counter: those of the forward."""
         dm = self._split(dout, 1, mask, counter, stream)
         dx1 = self.mlp.backward(self.x1, dm, stream, dx_residual=dout)[0]
+        if self.attention is not None:
+            if dq is not None or dk is not None:
+                raise ValueError("the attention core forms the gradients of q and k")
+            do = self._split(dx1, 0, mask, counter, stream)
+            att, (dq, dk, dv) = self.attention, self.dqkv
+            self.o.backward(att.out, do.view(1, self.T, self.d), stream, dx=self.dattention)
+            att.backward(*self.qkv.y, self.dattention, self.qkv.ws, dq, dk, dv, starts, stream)
+            if self.rotary is not None:
+                self.rotary(dq, dk, positions, inverse=True, q_out=dq, k_out=dk, stream=stream)
+            return self.qkv.backward(x, self.dqkv, stream, dx_residual=dx1)[0]
+        if dq is None or dk is None or starts is not None:
+            raise ValueError("without an attention core its gradients of q and k are needed, and "
+                             "there are no sequences")
         if self.rotary is not None:
             self.rotary(dq, dk, positions, inverse=True, q_out=self.dqkv[0], k_out=self.dqkv[1],
                         stream=stream)
@@ -338,6 +434,10 @@ class Layer:
         do = self._split(dx1, 0, mask, counter, stream)
         self.o.backward(self.qkv.y[2], do.view(1, self.T, self.d), stream, dx=self.dqkv[2])
         return self.qkv.backward(x, self.dqkv, stream, dx_residual=dx1)[0]
+
+    def weight_grads(self):
+        """The gradients of the weights."""
+        return self.qkv.weight_grads() + self.o.weight_grads() + self.mlp.weight_grads()
 
 
 class SVDPair:
@@ -366,6 +466,19 @@ class SVDPair:
     def backward(self, x, dy_qkv, dy_gu, stream=None):
         dxq = self.qkv.backward(x, dy_qkv, stream)[0]
         return self.gu.backward(x, dy_gu, stream, dx_residual=dxq)[0]
+
+    def weight_grads(self):
+        """The gradients of the weights."""
+        return self.qkv.weight_grads() + self.gu.weight_grads()
+
+
+def clip_gradients(workloads, max_norm, ws, *, norm=None, stream=None):
+    """The weight gradients of these blocks, MLPs, layers or pairs scaled in place to a norm over
+    all of them of ``max_norm`` at most (None: left as they are). Returns the norm (float32 [1], on
+    the device). ws: a workspace of ``binding.grad_clip_workspace_bytes()``, a block's own for
+    instance."""
+    return B.grad_clip([g for w in workloads for g in w.weight_grads()], max_norm, ws, norm=norm,
+                       stream=stream)
 
 
 def build_workload(name, tensors, device="cuda", T=None):
