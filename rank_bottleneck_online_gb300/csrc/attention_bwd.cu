@@ -26,10 +26,11 @@
 // the sums), and half the reads. Short sequences, whose rows would leave a CTA of the pair idle,
 // take single CTAs.
 //
-// Warp 0 loads the tiles, each through two buffers, warp 1 issues the products, warp 2 fetches the second
-// pass's lse and delta, sixteen warps are the rows of a tile, four threads a row. The products of
-// one kind run while the threads work on the other's scores: acc1 += P B and the next S during dS,
-// acc2 += dS Y0 and the next dP during P.
+// Warp 0 loads the tiles, each through two buffers, warp 1 issues the products, warp 2 fetches lse
+// and delta (the first pass's a work ahead, the second's a step), warp 3 the next work, sixteen
+// warps are the rows of a tile, four threads a row. The products of one kind run while the threads
+// work on the other's scores: acc1 += P B and the next S during dS, acc2 += dS Y0 and the next dP
+// during P.
 #include <math_constants.h>
 
 #include <atomic>
@@ -75,7 +76,8 @@ struct BwdCfg {
   static constexpr int kStatOffset = 2 * kTileBytes + 2 * kSlotKinds * kSlotBytes;
   static constexpr int kParts = 4;                       // threads of a row
   static constexpr int kCols = kTile / kParts;           // of its scores, each
-  static constexpr int kStatBytes = 4 * 4 * kTile;       // two buffers of lse and delta
+  // two buffers of lse and delta; kDq: and two of the parts of e
+  static constexpr int kStatBytes = (4 + 2 * kParts) * 4 * kTile;
   static constexpr int kWarps = 4 * kParts;              // that work on the scores
   static constexpr int kStageOffset = kStatOffset + kStatBytes;   // 16 rows of 64 bytes a warp
   static constexpr int kSchedOffset = kStageOffset + kWarps * 1024;
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
     mbar_init(acc_free, CG * Cfg::kWarps);
     mbar_init(sync_bar, Cfg::kWarps);
     mbar_init(done_bar, 1);
-    schedule_init<CG>(sched, Cfg::kWarps + 1 + (rank == 0) + (PASS == kDkv));
+    schedule_init<CG>(sched, Cfg::kWarps + 2 + (rank == 0));
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
@@ -273,6 +275,8 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
       __syncwarp();
       int32_t tile = t.first, h = t.y_head;
       for (int32_t i = 0; i < t.steps && ok; ++i, ++u) {
+        // (the next work's row sums take warp 2 about as long as eight steps)
+        if (rank == 0 && i == max(t.steps - 8, 0)) want_work(sched);
         const int32_t left = t.ny - tile * kTile, row = t.y_row + tile * kTile;
         // a tile in which the sequence ends lands on this CTA's own barrier first
         const bool tail = left < kTile;
@@ -331,7 +335,6 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
           ++h;
         }
       }
-      if (rank == 0) want_work(sched);
     }
     // the copies started here have landed before the CTA (or the pair) exits
     if (rank == 0) {
@@ -456,7 +459,48 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
       __syncwarp();
       warp_wait_all(done_bar, 0, nullptr, 68, p.wait_limit_ns);
     }
-  } else if (warp == 2 && PASS == kDkv) {
+  } else if (warp == 2 && PASS == kDq) {
+    // ------------------------- lse of the tile's rows, and delta from out: a work ahead
+    bool ok = true;
+    for (uint32_t n = 0; ok && next_work(sched, works, w, p.err, p.wait_limit_ns); ++n) {
+      const Tile<CG, PASS> t(w, p, rank);
+      float* to = stat + (n & 1) * 2 * kTile;
+      ok = warp_wait_all(&stat_empty[n & 1], (n >> 1 & 1) ^ 1, p.err, 66, p.wait_limit_ns);
+      if (!ok) break;
+#pragma unroll
+      for (int k = 0; k < kTile; k += 32)
+        to[k + lane] = t.x0 + k + lane < t.nx
+                           ? p.lse[w.head * p.Tq + t.x_row + k + lane] * kLog2e : 0.0f;
+      // 16 lanes a row, 8 rows at a time
+      const int c = (lane & 15) * 8;
+#pragma unroll 1
+      for (int r0 = lane >> 4; r0 < kTile; r0 += 16) {
+        uint4 a[8], b[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = r0 + 2 * k;
+          a[k] = b[k] = make_uint4(0, 0, 0, 0);
+          if (t.x0 + r < t.nx && c < p.dim) {
+            a[k] = *reinterpret_cast<const uint4*>(p.o.row(t.x_row + r, w.head) + c);
+            b[k] = *reinterpret_cast<const uint4*>(p.dout.row(t.x_row + r, w.head) + c);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float x[8], y[8], s = 0.0f;
+          unpack8(a[k], x);
+          unpack8(b[k], y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s = fmaf(x[e], y[e], s);
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          if ((lane & 15) == 0) to[kTile + r0 + 2 * k] = s;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&stat_full[n & 1]);
+    }
+  } else if (warp == 2) {
     // ----------------------------------------------- lse and delta of the queries
     // (loaded a step ahead, all at once: the threads wait for these as for the scores)
     int32_t u = 0;
@@ -505,52 +549,22 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_at = tS + lane_base + kCols * part, d_at = tD + lane_base + kCols * part;
     uint8_t* stage = smem + Cfg::kStageOffset + (warp - 4) * 1024;
-    // kDq: this warp's rows of out and dout, 16 lanes a row, for their products' sums; and lse
-    uint4 ro[4], rd[4];
-    float lse = 0.0f;
-    auto fetch = [&](const Tile<CG, PASS>& t) {
-      if (PASS != kDq) return;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = (warp - 4) * 8 + 2 * j + (lane >> 4), c = (lane & 15) * 8;
-        ro[j] = rd[j] = make_uint4(0, 0, 0, 0);
-        if (t.x0 + r < t.nx && c < p.dim) {
-          ro[j] = *reinterpret_cast<const uint4*>(p.o.row(t.x_row + r, w.head) + c);
-          rd[j] = *reinterpret_cast<const uint4*>(p.dout.row(t.x_row + r, w.head) + c);
-        }
-      }
-      lse = t.x0 + row < t.nx ? p.lse[w.head * p.Tq + t.x_row + row] * kLog2e : 0.0f;
-    };
     int32_t u = 0;
-    uint32_t tiles = 0, syncs = 0;
+    uint32_t tiles = 0, stats = 0;                        // works with steps; works
     bool ok = true;
-    auto threads_sync = [&]() {                           // of the warps that work on the scores
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sync_bar);
-      ok = ok && warp_wait_all(sync_bar, syncs++ & 1, p.err, 73, p.wait_limit_ns);
-    };
     bool have = next_work(sched, works, w, p.err, p.wait_limit_ns);
     Tile<CG, PASS> t(w, p, rank);
-    if (have) fetch(t);
     while (have) {
       const int32_t x = t.x0 + row;                       // in the sequence
       const bool valid = x < t.nx;
-      float delta = 0.0f, e = 0.0f;                       // kDq: of this row; what delta lacks
+      float lse = 0.0f, delta = 0.0f, e = 0.0f;           // kDq: of this row; what delta lacks
       if (PASS == kDq) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float a[8], b[8], s = 0.0f;
-          unpack8(ro[j], a);
-          unpack8(rd[j], b);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) s = fmaf(a[k], b[k], s);
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if ((lane & 15) == 0) stat[(warp - 4) * 8 + 2 * j + (lane >> 4)] = s;
-        }
-        threads_sync();
-        delta = stat[row];
-        threads_sync();
+        const float* st = stat + (stats & 1) * 2 * kTile;
+        ok = warp_wait_all(&stat_full[stats & 1], stats >> 1 & 1, p.err, 69, p.wait_limit_ns);
+        lse = st[row];
+        delta = st[kTile + row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&stat_empty[stats & 1]);
       }
       // kDq: keys that this row sees; kDkv: the first query that sees this row
       const int32_t bound = PASS == kDq ? (p.causal ? min(w.at.nk, x + t.off + 1) : w.at.nk)
@@ -636,20 +650,21 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
         if (++tile == t.first + t.count) tile = t.first;
       }
       if (PASS == kDq) {                                  // e over the row's parts, in order
-        stat[part * kTile + row] = e;
-        threads_sync();
-        e = stat[row];
+        float* parts = stat + 4 * kTile + (stats & 1) * Cfg::kParts * kTile;
+        parts[part * kTile + row] = e;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sync_bar);
+        ok = ok && warp_wait_all(sync_bar, stats & 1, p.err, 73, p.wait_limit_ns);
+        e = parts[row];
 #pragma unroll
-        for (int i = 1; i < Cfg::kParts; ++i) e += stat[i * kTile + row];
-        threads_sync();
-        if (valid && part == 0) p.delta[w.head * p.Tq + t.x_row + row] = delta + e;
+        for (int i = 1; i < Cfg::kParts; ++i) e += parts[i * kTile + row];
+        if (ok && valid && part == 0) p.delta[w.head * p.Tq + t.x_row + row] = delta + e;
+        ++stats;
       }
-      // the next tile's rows are on their way while this one's sums are stored
       const Tile<CG, PASS> done = t;
       const int32_t head = w.head;
       have = ok && next_work(sched, works, w, p.err, p.wait_limit_ns);
       t = Tile<CG, PASS>(w, p, rank);
-      if (have) fetch(t);
       if (done.steps > 0) {
         ok = ok && warp_wait_all(acc_bar, tiles++ & 1, p.err, 72, p.wait_limit_ns);
         if (!ok) break;

@@ -236,8 +236,8 @@ __device__ __forceinline__ Place find_tile(const int32_t* q_starts, const int32_
 // A CTA (or a pair) that is done takes the place of one that has not begun yet
 // (clusterlaunchcontrol): tiles go out in the grid's order to whoever is free, and what a launch
 // costs each (barriers, TMEM, the search for its sequence, the first loads) is paid once or hidden.
-// One warp asks, looks the tile up and leaves it for the others, once the loading warp has begun
-// its last loads of the tile before: no CTA holds work that an idle one could have.
+// One warp asks, looks the tile up and leaves it for the others, once the loading warp is near the
+// end of the tile before: no CTA holds work for long that an idle one could have.
 
 // Ask for a CTA (cluster) to cancel: 16 bytes at the same place in every CTA of the cluster, which
 // complete on each one's `bar`.
