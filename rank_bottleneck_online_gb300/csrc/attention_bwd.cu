@@ -72,7 +72,7 @@ struct BwdCfg {
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
   static constexpr int kSlotBytes = kTileBytes / CG;     // of a loaded tile
   static constexpr int kSlotKinds = CG == 2 ? 4 : 2;
-  static constexpr int kBars = 4 * kSlotKinds + 15;
+  static constexpr int kBars = 4 * kSlotKinds + 16;
   static constexpr int kStatOffset = 2 * kTileBytes + 2 * kSlotKinds * kSlotBytes;
   static constexpr int kParts = 4;                       // threads of a row
   static constexpr int kCols = kTile / kParts;           // of its scores, each
@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
   uint64_t* x_bar = empty_bar + 2 * Cfg::kSlotKinds;
   uint64_t* s_bar = x_bar + 1;                          // S is complete
   uint64_t* d_bar = s_bar + 1;                          // dP is complete
-  uint64_t* p_bar = d_bar + 1;                          // P is written
-  uint64_t* ds_bar = p_bar + 1;                         // dS is written
+  uint64_t* p_bar = d_bar + 1;                          // [2] P is written, half by half
+  uint64_t* ds_bar = p_bar + 2;                         // dS is written
   uint64_t* acc_bar = ds_bar + 1;                       // the sums are complete
   uint64_t* stat_full = acc_bar + 1;                    // [2]
   uint64_t* stat_empty = stat_full + 2;                 // [2]
@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
     mbar_init(x_bar, CG);
     mbar_init(s_bar, 1);
     mbar_init(d_bar, 1);
-    mbar_init(p_bar, CG * Cfg::kWarps);
+    mbar_init(&p_bar[0], CG * Cfg::kWarps);
+    mbar_init(&p_bar[1], CG * Cfg::kWarps);
     mbar_init(ds_bar, CG * Cfg::kWarps);
     mbar_init(acc_bar, 1);
     for (int b = 0; b < 2; ++b) {
@@ -409,11 +410,17 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
           const bool more = i + 1 < t.steps;
           const uint64_t b1 = ymn_desc + slot(kB1, u), b2 = ymn_desc + slot(k0m, u);
           const uint64_t next0 = yk_desc + slot(kY0k, u + 1), next1 = yk_desc + slot(kY1k, u + 1);
-          ok = (CG == 1 || take(kB1, u)) && written(p_bar, u, 64);
+          // (the first half's products run while the threads work on the second's P)
+          ok = (CG == 1 || take(kB1, u)) && written(&p_bar[0], u, 64);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) issue_sums<CG, Cfg::kCols, 0, 2>(tAcc1, tS, b1, id_acc, i > 0);
+          __syncwarp();
+          ok = written(&p_bar[1], u, 64);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            issue_sums<CG, Cfg::kCols>(tAcc1, tS, b1, id_acc, i > 0);
+            issue_sums<CG, Cfg::kCols, 1, 2>(tAcc1, tS, b1, id_acc, true);
             if (PASS == kDkv) free_slot(k1m, u);
           }
           __syncwarp();
@@ -581,36 +588,36 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
         tmem_ld_32x32b_x32(s_at, s);
         tmem_ld_wait();
         const int32_t lim = bound - tile * kTile - kCols * part;   // of this part's columns
-        if (PASS == kDq) {
+        const bool cut = __any_sync(0xffffffffu, PASS == kDq ? lim < kCols : lim > 0);
+        uint32_t pk[kCols / 2];
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) s[c] = exp2_fast(fmaf(s[c], p.scale_log2, -lse));
-          if (__any_sync(0xffffffffu, lim < kCols)) {
+        for (int half = 0; half < 2; ++half) {
+          constexpr int kHalf = kCols / 2;
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) s[c] = c < lim ? s[c] : 0.0f;
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < kCols; c += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(st + c);
+          for (int c = half * kHalf; c < (half + 1) * kHalf; c += 4) {
+            float4 l = make_float4(lse, lse, lse, lse);
+            if (PASS == kDkv) l = *reinterpret_cast<const float4*>(st + c);
             s[c] = exp2_fast(fmaf(s[c], p.scale_log2, -l.x));
             s[c + 1] = exp2_fast(fmaf(s[c + 1], p.scale_log2, -l.y));
             s[c + 2] = exp2_fast(fmaf(s[c + 2], p.scale_log2, -l.z));
             s[c + 3] = exp2_fast(fmaf(s[c + 3], p.scale_log2, -l.w));
           }
-          if (__any_sync(0xffffffffu, lim > 0)) {
+          if (cut) {
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) s[c] = c >= lim ? s[c] : 0.0f;
+            for (int c = half * kHalf; c < (half + 1) * kHalf; ++c)
+              s[c] = (PASS == kDq ? c < lim : c >= lim) ? s[c] : 0.0f;
           }
-        }
-        uint32_t pk[kCols / 2];
 #pragma unroll
-        for (int c = 0; c < kCols / 2; ++c) pk[c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
-        tmem_st_32x32b_x16(s_at, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (CG == 2) mbar_arrive_cluster(lead(p_bar)); else mbar_arrive(p_bar);
+          for (int c = half * kHalf / 2; c < (half + 1) * kHalf / 2; ++c)
+            pk[c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
+          tmem_st_32x32b_x8(s_at + half * (kHalf / 2), pk + half * (kHalf / 2));
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (CG == 2) mbar_arrive_cluster(lead(&p_bar[half]));
+            else mbar_arrive(&p_bar[half]);
+          }
         }
 
         ok = warp_wait_all(d_bar, u & 1, p.err, 71, p.wait_limit_ns);

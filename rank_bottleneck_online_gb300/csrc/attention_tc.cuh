@@ -82,6 +82,14 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
       : "memory");
 }
 
+// Each thread of the warp writes 8 consecutive columns of its TMEM lane.
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 // Each thread of the warp writes 16 consecutive columns of its TMEM lane.
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -142,16 +150,16 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint64_t x, uint64_t y,
   }
 }
 
-// D (+)= A Y over the tile's 128 rows, A in TMEM as parts of `COLS` values that lie COLS columns
-// apart, Y MN-major.
-template <int CG, int COLS>
+// D (+)= A Y over the tile's 128 rows, or over every STEP-th 16 of them from the FROM-th, A in TMEM
+// as parts of `COLS` values that lie COLS columns apart, Y MN-major.
+template <int CG, int COLS, int FROM = 0, int STEP = 1>
 __device__ __forceinline__ void issue_sums(uint32_t d, uint32_t a, uint64_t y, uint32_t idesc,
                                            bool more) {
 #pragma unroll
-  for (int kk = 0; kk < kTile / 16; ++kk) {
+  for (int kk = FROM; kk < kTile / 16; kk += STEP) {
     const uint32_t ak = a + 16 * kk / COLS * COLS + 16 * kk % COLS / 2;
-    if constexpr (CG == 2) tc_mma_bf16_ts_pair(d, ak, y + 128 * kk, idesc, kk > 0 ? 1u : more);
-    else tc_mma_bf16_ts(d, ak, y + 128 * kk, idesc, kk > 0 ? 1u : more);
+    if constexpr (CG == 2) tc_mma_bf16_ts_pair(d, ak, y + 128 * kk, idesc, kk > FROM ? 1u : more);
+    else tc_mma_bf16_ts(d, ak, y + 128 * kk, idesc, kk > FROM ? 1u : more);
   }
 }
 
