@@ -54,7 +54,7 @@ struct FwdCfg {
   static constexpr int kBoxes = HD / 64;
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
   static constexpr int kStages = HD == 128 ? 5 : 8;
-  static constexpr int kBars = 2 * kStages + 8;
+  static constexpr int kBars = 2 * kStages + 10;
   static constexpr int kBarOffset = (2 + kStages) * kTileBytes;
   static constexpr int kSmemBytes = 1024 + kBarOffset + 8 * kBars + 16;
   static constexpr int kThreads = 384;
@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
   uint64_t* empty_bar = full_bar + Cfg::kStages;
   uint64_t* q_bar = empty_bar + Cfg::kStages;
   uint64_t* s_bar = q_bar + 1;                          // [2] scores are complete
-  uint64_t* p_bar = s_bar + 2;                          // [2] probabilities are written
-  uint64_t* o_bar = p_bar + 2;                          // [2] the last product is complete
+  uint64_t* p_bar = s_bar + 2;                          // [2][2] a half of P is written
+  uint64_t* o_bar = p_bar + 4;                          // [2] the last product is complete
   uint64_t* done_bar = o_bar + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done_bar + 1);
 
@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     mbar_init(q_bar, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_bar[x], 1);
-      mbar_init(&p_bar[x], 4);
+      mbar_init(&p_bar[2 * x], 4);
+      mbar_init(&p_bar[2 * x + 1], 4);
       mbar_init(&o_bar[x], 1);
     }
     mbar_init(done_bar, 1);
@@ -223,7 +224,8 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
         ok = warp_wait_all(&full_bar[stage], phase, p.err, 44, p.wait_limit_ns);
         if (ok && left < kTile)
           zero_rows(sKV + stage * Cfg::kTileBytes, Cfg::kBoxes, kTile, left, lane);
-        ok = ok && warp_wait_all(&p_bar[x], i >> 1 & 1, p.err, 46, p.wait_limit_ns);
+        ok = ok && warp_wait_all(&p_bar[2 * x], i >> 1 & 1, p.err, 46, p.wait_limit_ns) &&
+             warp_wait_all(&p_bar[2 * x + 1], i >> 1 & 1, p.err, 46, p.wait_limit_ns);
         if (!ok) break;
         tc_fence_after();
         const uint64_t vd = v_desc + stage * kStep;
@@ -275,14 +277,18 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (j < n[x]) {
-          if (!warp_wait_all(&p_bar[x], j & 1, p.err, 46, p.wait_limit_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+          // O_x += P_x V; the first half's products run while the threads work on the second
           const uint64_t vd = v_desc + v_stage * kStep, kd = k_desc + stage * kStep;
+          ok = warp_wait_all(&p_bar[2 * x], j & 1, p.err, 46, p.wait_limit_ns);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) issue_sums<1, kTile, 0, 1, 4>(tO[x], tS[x], vd, id_o, j > 0);
+          __syncwarp();
+          ok = warp_wait_all(&p_bar[2 * x + 1], j & 1, p.err, 46, p.wait_limit_ns);
+          if (!ok) break;
+          tc_fence_after();
           if (elect_one()) {
-            issue_sums<1, kTile>(tO[x], tS[x], vd, id_o, j > 0);          // O_x += P_x V
+            issue_sums<1, kTile, 4>(tO[x], tS[x], vd, id_o, true);
             if (j + 1 < n[x]) {
               issue_scores<1, HD / 16>(tS[x], q_desc[x], kd, id_s, ksteps);
               tc_commit(&s_bar[x]);
@@ -362,24 +368,27 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
       // (a row that sees nothing yet: all its scores are -inf, and so are their exponents)
       const float shift = m == -CUDART_INF_F ? 0.0f : -m * p.scale_log2;
       float sum[4] = {};
-      uint32_t w[64];
 #pragma unroll
-      for (int c = 0; c < 128; c += 4) {
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[c + i] = exp2_fast(fmaf(s[c + i], p.scale_log2, shift));
-          sum[i] += s[c + i];
+        for (int k = 0; k < 64; k += 4) {
+          const int c = 64 * half + k;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[c + i] = exp2_fast(fmaf(s[c + i], p.scale_log2, shift));
+            sum[i] += s[c + i];
+          }
+          w[k / 2] = pack_bf16x2(s[c], s[c + 1]);
+          w[k / 2 + 1] = pack_bf16x2(s[c + 2], s[c + 3]);
         }
-        w[c / 2] = pack_bf16x2(s[c], s[c + 1]);
-        w[c / 2 + 1] = pack_bf16x2(s[c + 2], s[c + 3]);
+        tmem_st_32x32b_x32(s_at + 32 * half, w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_bar[2 * x + half]);
       }
-      tmem_st_32x32b_x32(s_at, w);
-      tmem_st_32x32b_x32(s_at + 32, w + 32);
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_bar[x]);
     }
     // O / l, and the logarithm of the sum
     if (ok && n[x] > 0) ok = warp_wait_all(&o_bar[x], 0, p.err, 50, p.wait_limit_ns);

@@ -150,13 +150,13 @@ __device__ __forceinline__ void issue_scores(uint32_t d, uint64_t x, uint64_t y,
   }
 }
 
-// D (+)= A Y over the tile's 128 rows, or over every STEP-th 16 of them from the FROM-th, A in TMEM
-// as parts of `COLS` values that lie COLS columns apart, Y MN-major.
-template <int CG, int COLS, int FROM = 0, int STEP = 1>
+// D (+)= A Y over the tile's 128 rows, or over every STEP-th 16 of them from the FROM-th up to the
+// TO-th, A in TMEM as parts of `COLS` values that lie COLS columns apart, Y MN-major.
+template <int CG, int COLS, int FROM = 0, int STEP = 1, int TO = kTile / 16>
 __device__ __forceinline__ void issue_sums(uint32_t d, uint32_t a, uint64_t y, uint32_t idesc,
                                            bool more) {
 #pragma unroll
-  for (int kk = FROM; kk < kTile / 16; kk += STEP) {
+  for (int kk = FROM; kk < TO; kk += STEP) {
     const uint32_t ak = a + 16 * kk / COLS * COLS + 16 * kk % COLS / 2;
     if constexpr (CG == 2) tc_mma_bf16_ts_pair(d, ak, y + 128 * kk, idesc, kk > FROM ? 1u : more);
     else tc_mma_bf16_ts(d, ak, y + 128 * kk, idesc, kk > FROM ? 1u : more);
