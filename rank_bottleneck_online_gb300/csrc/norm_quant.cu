@@ -26,14 +26,30 @@ struct NormQuantParams {
   float* rstd;
   uint8_t *q, *sf;
   int64_t T, d, pitch, kt;
-  int32_t warps;                         // of a row: 1, 2, 4 or 8
+  int32_t warps;                         // of a row
   float eps;
 };
 
 constexpr int kRows = 2;                 // of a warp
+// Warps of a block at most. (A residual's values take registers: 80 a thread in three blocks of
+// eight warps an SM, 16384 x 4096 in 71 us; 64 in blocks of up to sixteen, 75 us, and 128, 85 us.)
+constexpr int most_warps(bool residual) { return residual ? 8 : 16; }
 
 __device__ __forceinline__ void words_of(const uint4& v, uint32_t* w) {
   w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+}
+
+// Squares of two values added to two sums, in one instruction.
+__device__ __forceinline__ float2 square_sum2(float a, float b, float2 s) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\t"
+      "mov.b64 y, {%4, %5};\n\t"
+      "fma.rn.f32x2 y, x, x, y;\n\t"
+      "mov.b64 {%0, %1}, y;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a), "f"(b), "f"(s.x), "f"(s.y));
+  return r;
 }
 
 // x + residual of 8 values, rounded once.
@@ -46,54 +62,65 @@ __device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b) {
   return pack8(x);
 }
 
-__device__ __forceinline__ uint4 mul8(const uint4& a, const uint4& b) {
-  float x[8], y[8];
-  unpack8(a, x);
-  unpack8(b, y);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] *= y[e];
-  return pack8(x);
+// gamma h of 8 values, rounded once (a product of two bf16 values is exact before that).
+__device__ __forceinline__ uint32_t mul2_bf16(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(kThreads) norm_quant_kernel(const NormQuantParams p) {
+__device__ __forceinline__ uint4 mul8(const uint4& a, const uint4& b) {
+  return make_uint4(mul2_bf16(a.x, b.x), mul2_bf16(a.y, b.y), mul2_bf16(a.z, b.z),
+                    mul2_bf16(a.w, b.w));
+}
+
+template <int FMT, bool RES>
+__global__ void __launch_bounds__(32 * most_warps(RES), RES ? 3 : 2) norm_quant_kernel(const NormQuantParams p) {
   pdl_enter();
-  __shared__ float sums[kThreads / 32][kRows];
+  __shared__ float sums[most_warps(RES)][kRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int part = warp % p.warps, lines = kThreads / 32 / p.warps;
+  const int part = warp % p.warps, lines = blockDim.x / 32 / p.warps;
   const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * lines + warp / p.warps) * kRows;
-  float sum[kRows] = {};
+  const int rows = static_cast<int>(min(max(p.T - row0, static_cast<int64_t>(0)),
+                                        static_cast<int64_t>(kRows)));
+  float2 sum[kRows] = {};
   const int64_t tiles = p.kt;                          // of 512 columns
+  const int64_t first_at = row0 * p.d + lane * 16;
   for (int64_t tile = part; tile < tiles; tile += p.warps) {
     const int64_t col = tile * 512 + lane * 16;
-    uint4 v[kRows][2], r[kRows][2];
+    // (d is a multiple of 8: a lane's second vector may lie behind the columns, or both)
+    const bool in[2] = {col < p.d, col + 8 < p.d};
+    const int64_t at = first_at + tile * 512;
+    uint4 v[kRows][2], r[RES ? kRows : 1][2];
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        v[i][k] = r[i][k] = make_uint4(0, 0, 0, 0);
-        if (row0 + i < p.T && col + 8 * k < p.d) {
-          const int64_t at = (row0 + i) * p.d + col + 8 * k;
-          v[i][k] = *reinterpret_cast<const uint4*>(p.x + at);
-          if (p.res != nullptr) r[i][k] = *reinterpret_cast<const uint4*>(p.res + at);
+        v[i][k] = make_uint4(0, 0, 0, 0);
+        if (RES) r[i][k] = v[i][k];
+        if (i < rows && in[k]) {
+          v[i][k] = *reinterpret_cast<const uint4*>(p.x + at + i * p.d + 8 * k);
+          if (RES) r[i][k] = *reinterpret_cast<const uint4*>(p.res + at + i * p.d + 8 * k);
         }
       }
+    uint4 g[2] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (p.gamma != nullptr && in[k])
+        g[k] = __ldg(reinterpret_cast<const uint4*>(p.gamma + col + 8 * k));
     uint32_t w[kRows][8];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const bool in = row0 + i < p.T && col + 8 * k < p.d;
-        if (p.res != nullptr) v[i][k] = add8(v[i][k], r[i][k]);
-        float f[8];
-        unpack8(v[i][k], f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[i] = fmaf(f[e], f[e], sum[i]);
-        if (in && p.h != nullptr)
-          *reinterpret_cast<uint4*>(p.h + (row0 + i) * p.d + col + 8 * k) = v[i][k];
-        if (in && p.gamma != nullptr)
-          v[i][k] = mul8(v[i][k], __ldg(reinterpret_cast<const uint4*>(p.gamma + col + 8 * k)));
+        if (RES) v[i][k] = add8(v[i][k], r[i][k]);
         words_of(v[i][k], w[i] + 4 * k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sum[i] = square_sum2(bf16_lo(w[i][4 * k + e]), bf16_hi(w[i][4 * k + e]), sum[i]);
+        if (p.h != nullptr && i < rows && in[k])
+          *reinterpret_cast<uint4*>(p.h + at + i * p.d + 8 * k) = v[i][k];
+        if (p.gamma != nullptr) words_of(mul8(v[i][k], g[k]), w[i] + 4 * k);
       }
     }
     uint32_t top[kRows];
@@ -102,26 +129,25 @@ __global__ void __launch_bounds__(kThreads) norm_quant_kernel(const NormQuantPar
     const bool in_cols = first + (lane >> 3) < (p.d + 127) / 128;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int64_t row = row0 + i;
       const uint32_t byte = scale_byte<FMT>(top[i]);
-      if (row < p.T && col < p.pitch) {
+      if (i < rows && col < p.pitch) {
         const float inv = scale_inverse(byte);
         const uint2 a = quant8<FMT>(w[i], inv, mend), b = quant8<FMT>(w[i] + 4, inv, mend);
-        *reinterpret_cast<uint4*>(p.q + row * p.pitch + col) = make_uint4(a.x, a.y, b.x, b.y);
+        *reinterpret_cast<uint4*>(p.q + (row0 + i) * p.pitch + col) = make_uint4(a.x, a.y, b.x, b.y);
       }
-      uint32_t word = static_cast<uint32_t>(stored_byte(byte, top[i], in_cols && row < p.T))
+      uint32_t word = static_cast<uint32_t>(stored_byte(byte, top[i], in_cols && i < rows))
                       << (lane & 24);
       word |= __shfl_xor_sync(0xffffffffu, word, 8);
       word |= __shfl_xor_sync(0xffffffffu, word, 16);
       // (the scales of rows behind the last, up to a whole row tile, are 127)
-      if (lane == 0 && row < (p.T + 127) / 128 * 128)
-        *reinterpret_cast<uint32_t*>(p.sf + scale_at(row, first, p.kt)) = word;
+      if (lane == 0 && row0 + i < (p.T + 127) / 128 * 128)
+        *reinterpret_cast<uint32_t*>(p.sf + scale_at(row0 + i, first, p.kt)) = word;
     }
   }
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    sum[i] = warp_sum(sum[i]);
-    if (lane == 0) sums[warp][i] = sum[i];
+    const float all = warp_sum(sum[i].x + sum[i].y);
+    if (lane == 0) sums[warp][i] = all;
   }
   __syncthreads();
   if (part == 0 && lane < kRows && row0 + lane < p.T) {
@@ -183,20 +209,23 @@ extern "C" boost_status boost_norm_quantize(int64_t T, int64_t d, int32_t fmt, f
   p.T = T;
   p.d = d;
   p.eps = eps;
-  // Warps of a row: eight (or all that it has work for) where rows are few; else those whose turns
-  // over the row's tiles leave the fewest idle (8191 x 5120, ten tiles: 43 us with 8, 27 with 2).
-  p.warps = p.kt >= 8 ? 8 : p.kt >= 4 ? 4 : p.kt >= 2 ? 2 : 1;
-  if (T >= 2048)
-    for (int w = p.warps / 2; w >= 1; w /= 2)
-      if ((p.kt + w - 1) / w * w < (p.kt + p.warps - 1) / p.warps * p.warps) p.warps = w;
+  // A warp for each of a row's tiles, if a block can have as many: then nobody waits for a turn's
+  // loads after another's; else as few turns as that takes, shared evenly. Blocks of eight warps
+  // where rows are short. (8191 x 5120, ten tiles: eight warps in two turns took 43 us.)
+  const bool res = residual != nullptr;
+  const int64_t turns = (p.kt + most_warps(res) - 1) / most_warps(res);
+  p.warps = static_cast<int32_t>((p.kt + turns - 1) / turns);
+  const int lines = p.warps >= 8 ? 1 : 8 / p.warps;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const double n = static_cast<double>(T) * d;
   ProfScope ps(s, K_NORM_QUANT, 0.0,
                n * (2.0 + (residual ? 2.0 : 0.0) + (h ? 2.0 : 0.0) + 129.0 / 128.0));
-  const int64_t block_rows = kThreads / 32 / p.warps * kRows;
+  const auto kern = fmt == BOOST_E4M3
+      ? (res ? norm_quant_kernel<BOOST_E4M3, true> : norm_quant_kernel<BOOST_E4M3, false>)
+      : (res ? norm_quant_kernel<BOOST_E5M2, true> : norm_quant_kernel<BOOST_E5M2, false>);
+  const int64_t block_rows = lines * kRows;
   const int64_t grid = ((T + 127) / 128 * 128 + block_rows - 1) / block_rows;
-  const cudaError_t e =
-      launch_k(fmt == BOOST_E4M3 ? norm_quant_kernel<BOOST_E4M3> : norm_quant_kernel<BOOST_E5M2>,
-               grid, s, p);
+  const cudaError_t e = launch_blocks(kern, dim3(static_cast<unsigned>(grid), 1, 1),
+                                      dim3(32 * p.warps * lines, 1, 1), s, p);
   return e == cudaSuccess ? BOOST_OK : BOOST_ERR_CUDA;
 }

@@ -40,13 +40,14 @@ __device__ __forceinline__ void pdl_enter() {
   griddep_launch_dependents();
 }
 
-// Launch `kern` on `stream` with a grid of `grid` and blocks of kThreads, with the
+// Launch `kern` on `stream` with a grid of `grid` and blocks of `block`, with the
 // programmatic-stream-serialisation attribute when enabled.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_grid(void (*kern)(KArgs...), dim3 grid, cudaStream_t stream, Args&&... args) {
+cudaError_t launch_blocks(void (*kern)(KArgs...), dim3 grid, dim3 block, cudaStream_t stream,
+                          Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = block;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -54,6 +55,12 @@ cudaError_t launch_grid(void (*kern)(KArgs...), dim3 grid, cudaStream_t stream, 
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// The same with blocks of kThreads.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_grid(void (*kern)(KArgs...), dim3 grid, cudaStream_t stream, Args&&... args) {
+  return launch_blocks(kern, grid, dim3(kThreads, 1, 1), stream, std::forward<Args>(args)...);
 }
 
 template <typename... KArgs, typename... Args>
