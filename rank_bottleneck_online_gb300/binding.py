@@ -9,8 +9,10 @@ library is missing, ``lib()`` raises.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -148,7 +150,7 @@ def lib():
     L.boost_norm_quantize.argtypes = [i64, i64, ctypes.c_int32, ctypes.c_float] + [vp] * 8
     L.boost_grad_clip_workspace_bytes.argtypes = []
     L.boost_grad_clip_workspace_bytes.restype = sz
-    L.boost_grad_clip.argtypes = [i64, ctypes.POINTER(Grad), ctypes.c_double, vp, vp, sz, vp]
+    L.boost_grad_clip.argtypes = [i64, vp, ctypes.c_double, vp, vp, sz, vp]
     L.boost_status_string.argtypes = [ctypes.c_int]
     L.boost_status_string.restype = ctypes.c_char_p
     L.boost_swiglu_fwd.argtypes = [i64, i64, vp, vp, vp, vp]
@@ -895,14 +897,18 @@ def norm_quantize(x, *, residual=None, gamma=None, eps=1e-5, fmt="e4m3", h=None,
 
 
 # ------------------------------------------------------------- gradient clipping
+_dtype_of = operator.attrgetter("dtype")
+
+
 def grad_clip_workspace_bytes() -> int:
     return int(lib().boost_grad_clip_workspace_bytes())
 
 
 def grad_clip(grads, max_norm, ws: Workspace, *, outs=None, norm=None, stream=None):
     """The norm over all gradients (float32 [1], on the device), and each scaled in place by
-    min(1, max_norm / (norm + 1e-6)), or into ``outs``. max_norm None: the norm alone. Gradients
-    are contiguous, bfloat16 or float32, of any number, sizes and shapes."""
+    min(1, max_norm / (norm + 1e-6)), or into ``outs``, each of its gradient's type and number of
+    values. max_norm None: the norm alone. Gradients are contiguous, bfloat16 or float32, of any
+    number, sizes and shapes."""
     device = _device()
     grads = list(grads)
     outs = grads if outs is None else list(outs)
@@ -911,27 +917,28 @@ def grad_clip(grads, max_norm, ws: Workspace, *, outs=None, norm=None, stream=No
     if norm is None:
         norm = torch.empty((1,), dtype=torch.float32, device=ws.buf.device)
     # (a model has hundreds: whole lists at a time, and the words for what is wrong afterwards)
-    n, bf, wide = len(grads), torch.bfloat16, torch.float32
-    types, sizes = [g.dtype for g in grads], [g.numel() for g in grads]
-    fine = (all(d is bf or d is wide for d in types)
-            and all(g.is_contiguous() and g.get_device() == device for g in grads))
+    n, bf, wide, T = len(grads), torch.bfloat16, torch.float32, torch.Tensor
+    types, sizes = list(map(_dtype_of, grads)), list(map(T.numel, grads))
+    fine = ({bf, wide}.issuperset(types) and all(map(T.is_contiguous, grads))
+            and {device}.issuperset(map(T.get_device, grads)))
     if outs is not grads:
-        fine = fine and all(o.dtype is d and o.shape == g.shape and o.is_contiguous()
-                            and o.get_device() == device for o, g, d in zip(outs, grads, types))
+        fine = (fine and list(map(_dtype_of, outs)) == types and list(map(T.numel, outs)) == sizes
+                and all(map(T.is_contiguous, outs))
+                and {device}.issuperset(map(T.get_device, outs)))
     if not fine:
         for i, (g, o) in enumerate(zip(grads, outs)):
             if g.dtype is not bf and g.dtype is not wide:
                 raise TypeError(f"gradient {i} must be bfloat16 or float32, got {g.dtype}")
             _take(g, f"gradient {i}", g.dtype, g.shape, device)
             _take(o, f"out {i}", g.dtype, g.shape, device)
-    at = [g.data_ptr() for g in grads]
-    to = [0] * n if max_norm is None else at if outs is grads else [o.data_ptr() for o in outs]
+    at = list(map(T.data_ptr, grads))
+    to = [0] * n if max_norm is None else at if outs is grads else list(map(T.data_ptr, outs))
     # the table of Grad entries: four words each
     words = [0] * (4 * n)
     words[0::4], words[1::4], words[2::4], words[3::4] = at, to, sizes, [d is wide for d in types]
-    table = (ctypes.c_int64 * (4 * n))(*words)
+    table = array.array("q", words)
     _check(lib().boost_grad_clip(
-        n, ctypes.cast(table, ctypes.POINTER(Grad)), float("inf") if max_norm is None else max_norm,
+        n, table.buffer_info()[0], float("inf") if max_norm is None else max_norm,
         _take(norm, "norm", wide, (1,), device), _on(ws.buf, "ws", torch.uint8, device), ws.nbytes,
         _raw_stream(stream, device)), "boost_grad_clip")
     return norm

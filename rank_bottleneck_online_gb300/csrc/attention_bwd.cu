@@ -38,6 +38,7 @@
 
 #include "attention.cuh"
 #include "attention_tc.cuh"
+#include "profile.h"
 #include "simple.cuh"
 
 namespace boost_gb300 {
@@ -726,6 +727,9 @@ cudaError_t launch_pass(BwdParams p, int64_t T, cudaStream_t stream) {
   const double bytes = 4.0 * p.dim * (PASS == kDq ? static_cast<double>(p.Tk) / p.group
                                                   : static_cast<double>(p.Tq) * p.group);
   p.order = grid_order(p.order.heads, most_tiles(T, CG * kTile, p.sequences), bytes);
+  // (some waits last as long as a tile's work: 4 us a step at most, on top of the limit)
+  const int64_t steps = PASS == kDq ? p.Tk / kTile + 1 : (p.Tq / kTile + 1) * p.group;
+  p.wait_limit_ns += 4000 * static_cast<uint64_t>(steps);
   static std::atomic<bool> ready[64];    // per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -799,6 +803,7 @@ cudaError_t launch_attention_bwd(const AttentionArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   if (d.Tk == 0) return cudaSuccess;
+  if (d.Tq > 0) prof_note_kernels(1);
   p.tmX0 = k;
   p.tmX1 = v;
   p.tmY0 = q;

@@ -26,6 +26,7 @@
 
 #include "attention.cuh"
 #include "attention_tc.cuh"
+#include "profile.h"
 #include "simple.cuh"
 
 namespace boost_gb300 {
@@ -642,6 +643,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream) {
   else if (f.tiles > 0)
     e = d.dim <= 64 ? launch_fwd<64, false>(p, stream) : launch_fwd<128, false>(p, stream);
   if (e != cudaSuccess || f.parts == 1) return e;
+  prof_note_kernels(1);
   return launch_k(attention_join_kernel, rows, stream, p);
 }
 
