@@ -190,7 +190,7 @@ boost_status boost_fp8_matmul(const boost_fp8_matmul_desc* desc, const void* a, 
  *   dim       values per head, a multiple of 8, <= 128
  *   sequences >= 1
  *   causal    0 or 1
- *   scale     > 0, finite
+ *   scale     > 0, at most 2^127
  *   q_ts, q_hs, ...  token and head strides in elements, multiples of 8, positive where there is
  *             more than one token or head. In an output no two elements may coincide.
  * The strides of dout, dq, dk and dv are the backward's alone.
@@ -260,17 +260,17 @@ boost_status boost_norm_quantize(int64_t T, int64_t d, int32_t fmt, float eps, c
 /* --------------------------------------------------------- gradient clipping
  *
  *     norm = sqrt(sum over all tensors of g^2),     out = g min(1, max_norm / (norm + 1e-6))
- * Squares in fp32, their sums in fp64 in a fixed order: two calls give the same bits. A norm
- * that is not finite gives what the formula gives (NaN where it is NaN; 0, or NaN from an
- * infinity, where it is infinite).
+ * Squares in fp32, where that holds them, their sums in fp64 in a fixed order: two calls give the
+ * same bits, and gradients of any size count. Gradients that hold an infinity or NaN give what the
+ * formula gives, with any max_norm (all NaN where there is a NaN; 0, and NaN from an infinity).
  *   count      tensors, >= 0
  *   g          16-byte aligned
  *   out        may be g (then nothing is written where nothing is to be scaled); NULL: the tensor
  *              only counts in the norm. Otherwise it shares no byte with any tensor of the call.
  *   n          elements, >= 0
  *   wide       0: bf16, 1: fp32
- *   max_norm   >= 0; infinity: no scaling
- *   norm       out, fp32 [1]
+ *   max_norm   >= 0; infinity: no scaling of finite gradients
+ *   norm       out, fp32 [1] (infinity beyond fp32's range; what scales is its fp64 value)
  *   ws         workspace of boost_grad_clip_workspace_bytes() bytes, 256-byte aligned
  */
 typedef struct {

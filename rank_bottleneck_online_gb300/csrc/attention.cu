@@ -1,8 +1,6 @@
 // attention.cu -- C ABI of attention and its gradients: argument checks.
 #include "attention.cuh"
 
-#include <cmath>
-
 #include "boost_ops.h"
 #include "heads.h"
 #include "internal.h"
@@ -20,7 +18,7 @@ boost_status validate(const boost_attention_desc* desc) {
   if (desc == nullptr) return BOOST_ERR_INVALID_ARG;
   const boost_attention_desc& D = *desc;
   if (D.Tq < 0 || D.Tk < 0 || D.hq < 1 || D.hk < 1 || D.dim < 1 || D.sequences < 1 ||
-      (D.causal & ~1) || D.hq % D.hk || !(D.scale > 0.0f) || !std::isfinite(D.scale))
+      (D.causal & ~1) || D.hq % D.hk || !(D.scale > 0.0f) || D.scale > 0x1p127f)
     return BOOST_ERR_INVALID_ARG;
   if (D.dim % 8 || D.dim > BOOST_ATTENTION_MAX_DIM) return BOOST_ERR_UNSUPPORTED_SHAPE;
   // token and tile numbers, and tiles times heads, stay within 31 bits

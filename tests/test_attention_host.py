@@ -106,6 +106,7 @@ DESCS = [
     (dict(hq=3), INVALID), (dict(dim=0), INVALID), (dict(sequences=0), INVALID),
     (dict(causal=2), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(scale=2.0 ** 127 * 1.5), INVALID),
     (dict(dim=60), SHAPE), (dict(dim=136), SHAPE), (dict(Tq=1 << 31), SHAPE),
     (dict(Tk=1 << 31), SHAPE), (dict(hq=1 << 17, hk=1), SHAPE), (dict(sequences=1 << 21), SHAPE),
     (dict(Tq=1 << 30, hq=256), SHAPE),                 # too many tiles

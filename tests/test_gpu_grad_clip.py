@@ -175,3 +175,23 @@ def test_refuses_what_the_binding_sees(ws):
         B.grad_clip([g[0][1:]], 1.0, ws)                # not 16-byte aligned
     with pytest.raises(B.BoostError):
         B.grad_clip(g, 1.0, B.Workspace(256))
+
+
+@pytest.mark.parametrize("big", [1e-44, 1e-30, 1e-20, 1e19, 1e25, 3e36])
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_gradients_whose_squares_leave_fp32(dtype, big, ws):
+    """Their squares in fp64, every rounding below NORM; beside zeros, and in ragged tensors. (The
+    norm of 17269 values of 3e36 is 131 times that, 3.9e38, which rounds to fp32's infinity; what
+    scales is the fp64 norm.)"""
+    g = make([8192, 9000, 77], [dtype] * 3, seed=8, std=1.0)
+    g = [(t.double() * big).to(dtype) for t in g] + [torch.zeros(20000, dtype=dtype, device="cuda")]
+    before = [t.clone() for t in g]
+    norm = B.grad_clip(g, None, ws)
+    want, _ = ops.grad_clip([f64(t) for t in before], float("inf"))
+    if want > torch.finfo(torch.float32).max:
+        assert norm.item() == float("inf")
+    else:
+        assert abs(norm.item() - want) <= (NORM + 2.0 ** -24) * want + 2.0 ** -149
+    if big >= 1e19:
+        assert torch.equal(B.grad_clip(g, 0.5 * want, ws), norm)
+        compare(g, torch.tensor(want, dtype=torch.float64), before, 0.5 * want)
