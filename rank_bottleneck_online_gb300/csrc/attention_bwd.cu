@@ -23,8 +23,8 @@
 // shared memory while both operands lie there, which is all that there is: the loads' writes cost
 // time. So with heads of more than 64 values a pair of CTAs works on 256 rows: each has half of
 // the other side's tile, once split along its rows (for S and dP) and once along its values (for
-// the sums), and half the reads. Short sequences, whose rows would leave a CTA of the pair idle,
-// take single CTAs.
+// the sums), and half the reads. Shorter sequences, whose last rows leave a CTA of the pair idle
+// and which wait for their pair at each end of a work, take single CTAs.
 //
 // Warp 0 loads the tiles, each through two buffers, warp 1 issues the products, warp 2 fetches lse
 // and delta (the first pass's a work ahead, the second's a step), warp 3 the next work, sixteen
@@ -759,8 +759,11 @@ cudaError_t launch_pass(BwdParams p, int64_t T, cudaStream_t stream) {
 template <int PASS>
 cudaError_t launch(const BwdParams& p, int64_t T, cudaStream_t stream) {
   if (p.dim <= 64) return launch_pass<64, 1, PASS>(p, T, stream);
-  // pairs where a sequence has a few tiles' rows
-  if (T / p.sequences >= 512) return launch_pass<128, 2, PASS>(p, T, stream);
+  // Pairs where sequences are long. (16384 tokens, 16 heads, us of both passes, singles and pairs: 32 x
+  // 512 334 and 349 causal, 370 and 386 without; 24 x 640 310 and 356, 369 and 407; 16 x 1024 382 and
+  // 387, 468 and 469; 10 x 1664 462 and 481, 658 and 676; 8 x 2048 505 and 504, 780 and 760; 4 x 4096
+  // 820 and 800, 1450 and 1405.)
+  if (T / p.sequences >= 2048) return launch_pass<128, 2, PASS>(p, T, stream);
   return launch_pass<128, 1, PASS>(p, T, stream);
 }
 

@@ -96,6 +96,34 @@ def test_sequences_of_several_tiles_with_shared_key_heads(hq, hk, layout):
     Case([(700, 700), (1, 900), (850, 610)], hq, hk, 128, layout=layout, tail=3, seed=hq).check()
 
 
+def behind(lengths):
+    """Rows behind the last sequence that make a sequence's share of all rows 2100: the size that
+    the gradients' tiles are chosen by, where the sequences themselves are smaller."""
+    return max(2100 * len(lengths) - min(map(sum, zip(*lengths))), 70)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim", [72, 96, 104, 128])
+@pytest.mark.parametrize("lengths", [[(1, 1)], [(129, 257)], [(512, 512)], [(1025, 1153)],
+                                     [(900, 1300), (700, 515)], [(1300, 600)], [(2305, 2177)],
+                                     [(1000, 1090), (130, 0), (0, 7), (511, 513)]])
+def test_sequences_of_pairs_of_tiles(lengths, dim, causal):
+    Case(lengths, 2, 2, dim, causal=causal, seed=dim, tail=behind(lengths)).check()
+
+
+@pytest.mark.parametrize("hq,hk", [(6, 2), (5, 1)])
+@pytest.mark.parametrize("layout", ["packed", "heads"])
+def test_sequences_of_pairs_of_tiles_with_shared_key_heads(hq, hk, layout):
+    lengths = [(700, 700), (1, 900), (850, 610)]
+    Case(lengths, hq, hk, 128, layout=layout, tail=behind(lengths), seed=hq).check()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_pairs_of_tiles_do_not_leak(bad):
+    lengths = [(600, 790), (530, 570), (660, 660), (629, 840)]
+    _leak(lengths, 128, bad, behind(lengths))
+
+
 @pytest.mark.parametrize("nq", [1, 3])
 def test_one_token_over_a_long_context(nq):
     Case([(nq, 30000), (nq, 1), (nq, 129), (nq, 9999)], 5, 1, 128, seed=9).check()
@@ -129,8 +157,8 @@ def test_long_sequences_do_not_leak(bad):
     _leak([(600, 790), (530, 570), (660, 660), (629, 840)], 128, bad)
 
 
-def _leak(lengths, dim, bad):
-    c = Case(lengths, 4, 2, dim, tail=150, seed=10)
+def _leak(lengths, dim, bad, tail=150):
+    c = Case(lengths, 4, 2, dim, tail=tail, seed=10)
     want = c.want()
     (q0, k0), (nq, nk) = lengths[0], lengths[1]
     for t, at, n in ((c.q, q0, nq), (c.dout, q0, nq), (c.k, k0, nk), (c.v, k0, nk)):
