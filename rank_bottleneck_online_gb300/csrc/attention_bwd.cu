@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
       if (lane == 0) mbar_arrive(&stat_full[n & 1]);
     }
   } else if (warp == 2) {
-    // ----------------------------------------------- lse and delta of the queries
+    // ----------------------------------- lse and delta of the queries, less than zero
     // (loaded a step ahead, all at once: the threads wait for these as for the scores)
     int32_t u = 0;
     bool ok = true;
@@ -539,8 +539,8 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
         for (int k = 0; k < 4; ++k) {
           // (a query that is none, or sees no key, has no probabilities)
           const bool none = l[k] == -CUDART_INF_F;
-          stat[b * 2 * kTile + k * 32 + lane] = none ? CUDART_INF_F : l[k] * kLog2e;
-          stat[b * 2 * kTile + kTile + k * 32 + lane] = none ? 0.0f : d[k];
+          stat[b * 2 * kTile + k * 32 + lane] = none ? -CUDART_INF_F : l[k] * -kLog2e;
+          stat[b * 2 * kTile + kTile + k * 32 + lane] = none ? 0.0f : -d[k];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&stat_full[b]);
@@ -557,6 +557,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_at = tS + lane_base + kCols * part, d_at = tD + lane_base + kCols * part;
     uint8_t* stage = smem + Cfg::kStageOffset + (warp - 4) * 1024;
+    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
     int32_t u = 0;
     uint32_t tiles = 0, stats = 0;                        // works with steps; works
     bool ok = true;
@@ -596,12 +597,14 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
           constexpr int kHalf = kCols / 2;
 #pragma unroll
           for (int c = half * kHalf; c < (half + 1) * kHalf; c += 4) {
-            float4 l = make_float4(lse, lse, lse, lse);
+            float4 l = make_float4(-lse, -lse, -lse, -lse);
             if (PASS == kDkv) l = *reinterpret_cast<const float4*>(st + c);
-            s[c] = exp2_fast(fmaf(s[c], p.scale_log2, -l.x));
-            s[c + 1] = exp2_fast(fmaf(s[c + 1], p.scale_log2, -l.y));
-            s[c + 2] = exp2_fast(fmaf(s[c + 2], p.scale_log2, -l.z));
-            s[c + 3] = exp2_fast(fmaf(s[c + 3], p.scale_log2, -l.w));
+            const float2 x = fma2(make_float2(s[c], s[c + 1]), scale2, make_float2(l.x, l.y));
+            const float2 y = fma2(make_float2(s[c + 2], s[c + 3]), scale2, make_float2(l.z, l.w));
+            s[c] = exp2_fast(x.x);
+            s[c + 1] = exp2_fast(x.y);
+            s[c + 2] = exp2_fast(y.x);
+            s[c + 3] = exp2_fast(y.y);
           }
           if (cut) {
 #pragma unroll
@@ -627,24 +630,17 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
         float d[kCols];
         tmem_ld_32x32b_x32(d_at, d);
         tmem_ld_wait();
-        if (PASS == kDq) {
-          float sum[4] = {};
+        float2 sum[2] = {};
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) {
-            d[c] = s[c] * (d[c] - delta);
-            sum[c & 3] += d[c];
-          }
-          e += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < kCols; c += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(st + kTile + c);
-            d[c] = s[c] * (d[c] - l.x);
-            d[c + 1] = s[c + 1] * (d[c + 1] - l.y);
-            d[c + 2] = s[c + 2] * (d[c + 2] - l.z);
-            d[c + 3] = s[c + 3] * (d[c + 3] - l.w);
-          }
+        for (int c = 0; c < kCols; c += 2) {
+          float2 l = make_float2(-delta, -delta);
+          if (PASS == kDkv) l = *reinterpret_cast<const float2*>(st + kTile + c);
+          const float2 x = mul2(make_float2(s[c], s[c + 1]), add2(make_float2(d[c], d[c + 1]), l));
+          if (PASS == kDq) sum[c / 2 & 1] = add2(sum[c / 2 & 1], x);
+          d[c] = x.x;
+          d[c + 1] = x.y;
         }
+        if (PASS == kDq) e += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 #pragma unroll
         for (int c = 0; c < kCols / 2; ++c) pk[c] = pack_bf16x2(d[2 * c], d[2 * c + 1]);
         tmem_st_32x32b_x16(d_at, pk);

@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     const int32_t sees =
         (p.causal ? min(at.nk, tq + off + 1) : at.nk) - (first + (own ? x : 0)) * kTile;
     const int32_t step = own ? 2 * kTile : kTile;
+    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
     float m = -CUDART_INF_F, l = 0.0f;                    // reference in S's units, sum of P
     bool ok = true;
     for (int32_t j = 0; j < n[x]; ++j) {
@@ -368,7 +369,8 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
       }
       // (a row that sees nothing yet: all its scores are -inf, and so are their exponents)
       const float shift = m == -CUDART_INF_F ? 0.0f : -m * p.scale_log2;
-      float sum[4] = {};
+      const float2 shift2 = make_float2(shift, shift);
+      float2 sum[2] = {};
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t w[32];
@@ -376,9 +378,11 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
         for (int k = 0; k < 64; k += 4) {
           const int c = 64 * half + k;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[c + i] = exp2_fast(fmaf(s[c + i], p.scale_log2, shift));
-            sum[i] += s[c + i];
+          for (int i = 0; i < 4; i += 2) {
+            const float2 x = fma2(make_float2(s[c + i], s[c + i + 1]), scale2, shift2);
+            s[c + i] = exp2_fast(x.x);
+            s[c + i + 1] = exp2_fast(x.y);
+            sum[i / 2] = add2(sum[i / 2], make_float2(s[c + i], s[c + i + 1]));
           }
           w[k / 2] = pack_bf16x2(s[c], s[c + 1]);
           w[k / 2 + 1] = pack_bf16x2(s[c + 2], s[c + 3]);
@@ -389,7 +393,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_bar[2 * x + half]);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     }
     // O / l, and the logarithm of the sum
     if (ok && n[x] > 0) ok = warp_wait_all(&o_bar[x], 0, p.err, 50, p.wait_limit_ns);
