@@ -151,7 +151,25 @@ __device__ __forceinline__ void store_rows(const HeadsOut& out, int32_t head, in
   }
 }
 
-template <int HD, int CG, int PASS>
+// Rounds s to bf16 as an operand in TMEM, pairs of columns a word: N / 2 words from `to` on; with
+// FINE what that rounds off as another operand, `apart` words behind it.
+template <int N, bool FINE>
+__device__ __forceinline__ void store_operand(uint32_t to, uint32_t apart, const float* s) {
+  static_assert(N == 16 || (N == 32 && !FINE), "");
+  uint32_t hi[N / 2];
+#pragma unroll
+  for (int c = 0; c < N; c += 2) hi[c / 2] = pack_bf16x2(s[c], s[c + 1]);
+  if constexpr (N == 16) tmem_st_32x32b_x8(to, hi); else tmem_st_32x32b_x16(to, hi);
+  if constexpr (FINE) {
+    uint32_t lo[N / 2];
+#pragma unroll
+    for (int c = 0; c < N; c += 2)
+      lo[c / 2] = pack_bf16x2(s[c] - bf16_lo(hi[c / 2]), s[c + 1] - bf16_hi(hi[c / 2]));
+    tmem_st_32x32b_x8(to + apart, lo);
+  }
+}
+
+template <int HD, int CG, int PASS, bool FINE>
 __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
     attention_bwd_kernel(const __grid_constant__ BwdParams p) {
   using Cfg = BwdCfg<HD, CG>;
@@ -415,13 +433,17 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
           ok = (CG == 1 || take(kB1, u)) && written(&p_bar[0], u, 64);
           if (!ok) break;
           tc_fence_after();
-          if (elect_one()) issue_sums<CG, Cfg::kCols, 0, 2>(tAcc1, tS, b1, id_acc, i > 0);
+          if (elect_one()) {
+            issue_sums<CG, Cfg::kCols, 0, 2>(tAcc1, tS, b1, id_acc, i > 0);
+            if (FINE) issue_sums<CG, Cfg::kCols, 0, 2>(tAcc1, tS + Cfg::kCols / 2, b1, id_acc, true);
+          }
           __syncwarp();
           ok = written(&p_bar[1], u, 64);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
             issue_sums<CG, Cfg::kCols, 1, 2>(tAcc1, tS, b1, id_acc, true);
+            if (FINE) issue_sums<CG, Cfg::kCols, 1, 2>(tAcc1, tS + Cfg::kCols / 2, b1, id_acc, true);
             if (PASS == kDkv) free_slot(k1m, u);
           }
           __syncwarp();
@@ -441,6 +463,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
           tc_fence_after();
           if (elect_one()) {
             issue_sums<CG, Cfg::kCols>(tAcc2, tD, b2, id_acc, i > 0);
+            if (FINE) issue_sums<CG, Cfg::kCols>(tAcc2, tD + Cfg::kCols / 2, b2, id_acc, true);
             free_slot(k0m, u);
             if (!more) commit(acc_bar);
           }
@@ -591,7 +614,6 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
         tmem_ld_wait();
         const int32_t lim = bound - tile * kTile - kCols * part;   // of this part's columns
         const bool cut = __any_sync(0xffffffffu, PASS == kDq ? lim < kCols : lim > 0);
-        uint32_t pk[kCols / 2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           constexpr int kHalf = kCols / 2;
@@ -611,10 +633,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
             for (int c = half * kHalf; c < (half + 1) * kHalf; ++c)
               s[c] = (PASS == kDq ? c < lim : c >= lim) ? s[c] : 0.0f;
           }
-#pragma unroll
-          for (int c = half * kHalf / 2; c < (half + 1) * kHalf / 2; ++c)
-            pk[c] = pack_bf16x2(s[2 * c], s[2 * c + 1]);
-          tmem_st_32x32b_x8(s_at + half * (kHalf / 2), pk + half * (kHalf / 2));
+          store_operand<kHalf, FINE>(s_at + half * (kHalf / 2), kCols / 2, s + half * kHalf);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -641,9 +660,12 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
           d[c + 1] = x.y;
         }
         if (PASS == kDq) e += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-#pragma unroll
-        for (int c = 0; c < kCols / 2; ++c) pk[c] = pack_bf16x2(d[2 * c], d[2 * c + 1]);
-        tmem_st_32x32b_x16(d_at, pk);
+        if constexpr (FINE) {
+          store_operand<kCols / 2, true>(d_at, kCols / 2, d);
+          store_operand<kCols / 2, true>(d_at + kCols / 4, kCols / 2, d + kCols / 2);
+        } else {
+          store_operand<kCols, false>(d_at, 0, d);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -665,6 +687,8 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
         if (ok && valid && part == 0) p.delta[w.head * p.Tq + t.x_row + row] = delta + e;
         ++stats;
       }
+      // (the softmax of a single key is constant: the gradients of its score are 0, to the bit)
+      const float scale = (PASS == kDq ? bound : w.at.nk) == 1 ? 0.0f : p.scale;
       const Tile<CG, PASS> done = t;
       const int32_t head = w.head;
       have = ok && next_work(sched, works, w, p.err, p.wait_limit_ns);
@@ -692,7 +716,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
             a2[k] = fmaf(-e, a1[k], a2[k]);
             a2[k + 1] = fmaf(-e, a1[k + 1], a2[k + 1]);
           }
-          g2[(c + k) / 2] = pack_bf16x2(p.scale * a2[k], p.scale * a2[k + 1]);
+          g2[(c + k) / 2] = pack_bf16x2(scale * a2[k], scale * a2[k + 1]);
           if (PASS == kDkv) g1[(c + k) / 2] = pack_bf16x2(a1[k], a1[k + 1]);
         }
       }
@@ -715,10 +739,10 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
   }
 }
 
-template <int HD, int CG, int PASS>
+template <int HD, int CG, int PASS, bool FINE>
 cudaError_t launch_pass(BwdParams p, int64_t T, cudaStream_t stream) {
   using Cfg = BwdCfg<HD, CG>;
-  const auto kern = attention_bwd_kernel<HD, CG, PASS>;
+  const auto kern = attention_bwd_kernel<HD, CG, PASS, FINE>;
   // the other side: k and v of a key head, or q and dout of its query heads
   const double bytes = 4.0 * p.dim * (PASS == kDq ? static_cast<double>(p.Tk) / p.group
                                                   : static_cast<double>(p.Tq) * p.group);
@@ -753,14 +777,17 @@ cudaError_t launch_pass(BwdParams p, int64_t T, cudaStream_t stream) {
 }
 
 template <int PASS>
-cudaError_t launch(const BwdParams& p, int64_t T, cudaStream_t stream) {
-  if (p.dim <= 64) return launch_pass<64, 1, PASS>(p, T, stream);
+cudaError_t launch(const BwdParams& p, int64_t T, bool fine, cudaStream_t stream) {
+  if (fine)
+    return p.dim <= 64 ? launch_pass<64, 1, PASS, true>(p, T, stream)
+                       : launch_pass<128, 1, PASS, true>(p, T, stream);
+  if (p.dim <= 64) return launch_pass<64, 1, PASS, false>(p, T, stream);
   // Pairs where sequences are long. (16384 tokens, 16 heads, us of both passes, singles and pairs: 32 x
   // 512 334 and 349 causal, 370 and 386 without; 24 x 640 310 and 356, 369 and 407; 16 x 1024 382 and
   // 387, 468 and 469; 10 x 1664 462 and 481, 658 and 676; 8 x 2048 505 and 504, 780 and 760; 4 x 4096
   // 820 and 800, 1450 and 1405.)
-  if (T / p.sequences >= 2048) return launch_pass<128, 2, PASS>(p, T, stream);
-  return launch_pass<128, 1, PASS>(p, T, stream);
+  if (T / p.sequences >= 2048) return launch_pass<128, 2, PASS, false>(p, T, stream);
+  return launch_pass<128, 1, PASS, false>(p, T, stream);
 }
 
 }  // namespace
@@ -789,6 +816,12 @@ cudaError_t launch_attention_bwd(const AttentionArgs& a, cudaStream_t stream) {
   p.scale_log2 = d.scale * kLog2e;
   p.err = static_cast<DeviceError*>(a.ws);
   p.wait_limit_ns = wait_limit_ns();
+  // Few scores (of sequences of one length): P and dS as two operands each. The roundings of few
+  // values do not average out (gradients of 6 tokens of one head were off by 0.0033, relative to
+  // all, where a bf16 result alone is by 0.0016, and those of long sequences by 0.0024), and the
+  // tensor cores have little else to do (77 tokens, 16 heads, forward and backward: 33 us, 32
+  // without).
+  const bool fine = static_cast<double>(d.Tq) * d.Tk / d.sequences * d.hq <= 262144.0;
   if (d.Tq > 0) {
     p.tmX0 = q;
     p.tmX1 = dout;
@@ -798,7 +831,7 @@ cudaError_t launch_attention_bwd(const AttentionArgs& a, cudaStream_t stream) {
     p.dout = a.dout;
     p.g2 = a.dq;
     p.order.heads = d.hq;
-    const cudaError_t e = launch<kDq>(p, d.Tq, stream);
+    const cudaError_t e = launch<kDq>(p, d.Tq, fine, stream);
     if (e != cudaSuccess) return e;
   }
   if (d.Tk == 0) return cudaSuccess;
@@ -810,7 +843,7 @@ cudaError_t launch_attention_bwd(const AttentionArgs& a, cudaStream_t stream) {
   p.g1 = a.dv;
   p.g2 = a.dk;
   p.order.heads = d.hk;
-  return launch<kDkv>(p, d.Tk, stream);
+  return launch<kDkv>(p, d.Tk, fine, stream);
 }
 
 }  // namespace boost_gb300

@@ -6,6 +6,9 @@ exponentials and sums is below 2^-10 of the same magnitudes for the scores met h
 sums of at most 128 products, is off by less than 2^-12, and so is exp(s) relative to itself. So an
 output is off by at most SLACK times the magnitudes that these roundings scale with (the oracle's
 *_size), and by half a bf16 step of its own. lse: 2^-12 from the scores and as much from the sum.
+The gradients of a call of few scores take both operands in two parts (2^-16 of each): what is left
+of SLACK is the fp32 part, exp(s - lse) off by 2^-12 from s and 2^-11 from lse, and what is below
+2^-13 together.
 """
 
 import itertools
@@ -19,6 +22,7 @@ from rank_bottleneck_online_gb300 import binding as B
 from ops_parity import BF, close, f64, guarded
 
 SLACK = 2.0 ** -8 + 2.0 ** -10
+FINE = 2.0 ** -10
 LSE = 2.0 ** -11
 SENTINEL = -7.25                       # a bf16 value that no output takes by chance
 
@@ -106,16 +110,16 @@ class Case:
         assert np.abs(got[~empty] - exact[~empty]).max(initial=0.0) <= LSE
         assert (out[behind] == SENTINEL).all() and (lse[:, behind] == SENTINEL).all()
 
-    def check_backward(self, grads, want):
+    def check_backward(self, grads, want, slack=SLACK):
         for name, got, which in zip(("dq", "dk", "dv"), grads, (0, 1, 1)):
             i, behind = self.rows(which)
-            close(got[i], want[name][i], SLACK * want[f"{name}_size"][i])
+            close(got[i], want[name][i], slack * want[f"{name}_size"][i])
             assert (got[behind] == SENTINEL).all(), name
 
-    def check(self):
+    def check(self, slack=SLACK):
         want = self.want()
         out, lse = self.forward()
         self.check_forward(out, lse, want)
         grads = self.backward(out, lse)
-        self.check_backward(grads, want)
+        self.check_backward(grads, want, slack)
         return out, lse, grads

@@ -9,7 +9,7 @@ from oracle import ops
 from rank_bottleneck_online_gb300 import binding as B
 from rank_bottleneck_online_gb300 import build as build_mod
 
-from attention_parity import SENTINEL, Case
+from attention_parity import FINE, SENTINEL, Case
 from ops_parity import BF, f64, normal
 
 pytestmark = pytest.mark.gpu
@@ -122,6 +122,47 @@ def test_sequences_of_pairs_of_tiles_with_shared_key_heads(hq, hk, layout):
 def test_pairs_of_tiles_do_not_leak(bad):
     lengths = [(600, 790), (530, 570), (660, 660), (629, 840)]
     _leak(lengths, 128, bad, behind(lengths))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim", [8, 40, 64, 72, 128])
+@pytest.mark.parametrize("n", [(1, 1), (2, 3), (7, 128), (63, 1), (127, 129), (256, 255), (400, 400)])
+def test_one_sequence_of_many_rows(n, dim, causal):
+    """Rows behind the sequence count as scores of the call, whose number decides how the gradients'
+    operands are rounded."""
+    Case([n], 3, 1, dim, causal=causal, tail=600, seed=n[0] + dim).check()
+
+
+@pytest.mark.parametrize("layout", ["planes", "packed", "heads"])
+@pytest.mark.parametrize("dim", [56, 96])
+def test_packed_sequences_of_many_rows(dim, layout):
+    lengths = [(1, 1), (0, 5), (130, 130), (7, 300), (5, 0), (0, 0), (256, 256), (64, 65), (3, 2)]
+    Case(lengths, 4, 2, dim, tail=2000, layout=layout, seed=dim).check()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim", [16, 64, 80, 128])
+@pytest.mark.parametrize("lengths,hq,hk", [([(1, 2)], 1, 1), ([(4, 4), (4, 4)], 2, 1), ([(6, 6)], 1, 1),
+                                           ([(33, 65), (5, 1), (0, 3)], 4, 2), ([(130, 257)], 6, 2),
+                                           ([(200, 140), (3, 200)], 6, 6)])
+def test_few_scores(lengths, hq, hk, dim, causal):
+    """Gradients that are off by little more than their own rounding."""
+    for seed in range(4):
+        Case(lengths, hq, hk, dim, causal=causal, seed=seed).check(FINE)
+
+
+@pytest.mark.parametrize("tail", [0, 700, 4500])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_single_key_has_no_gradient(dim, tail):
+    """Its probability is 1 whatever its score: dq of a row that sees one key and dk of a sequence
+    of one key are 0, to the bit."""
+    c = Case([(150, 1), (70, 70)], 4, 2, dim, tail=tail, seed=dim, causal=False)
+    _, _, (dq, dk, _) = c.check()
+    assert (dq[:150] == 0).all() and (dk[:1] == 0).all()
+    c = Case([(150, 1), (70, 70), (1, 1)], 4, 2, dim, tail=tail, seed=dim)
+    _, _, (dq, dk, _) = c.check()
+    assert (dq[:151] == 0).all() and (dk[:1] == 0).all() and (dq[220] == 0).all()
+    assert (dk[71] == 0).all()
 
 
 @pytest.mark.parametrize("nq", [1, 3])
