@@ -449,16 +449,23 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
   }
 }
 
-// Joins the parts of a row's keys: a block a row of one head, its warps take parts in turn, and
-// the warps' sums are added in their order. (A warp alone a row took 22 us for the 100 parts of the
-// longest of eight rows of 40 heads, one load after another; a block 4.)
+// Joins the parts of a row's keys: WARPS of a block take a row of one head, each parts in turn, and
+// the warps' sums are added in their order. (Many parts, a block a row: a warp alone took 22 us for
+// the 100 parts of the longest of eight rows of 40 heads, one load after another, a block 4. Few
+// parts of many rows, a warp a row: 2048 tokens of 4 heads in four parts take 25 us in all, with a
+// block a row 47.)
+template <int WARPS>
 __global__ void __launch_bounds__(kThreads) attention_join_kernel(const FwdParams p) {
   pdl_enter();
   constexpr int kWarps = kThreads / 32;
-  __shared__ float4 sums[kWarps][32];
-  __shared__ float tops[kWarps], totals[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t item = blockIdx.x, rows = p.Tq * p.hq;
+  static_assert(WARPS == 1 || WARPS == kWarps, "a warp or a block");
+  __shared__ float4 sums[WARPS][32];
+  __shared__ float tops[WARPS], totals[WARPS];
+  const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
+  const int64_t rows = p.Tq * p.hq;
+  const int64_t item = WARPS == 1 ? static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)
+                                  : static_cast<int64_t>(blockIdx.x);
+  if (item >= rows) return;
   const int32_t token = static_cast<int32_t>(item / p.hq), h = static_cast<int32_t>(item % p.hq);
   int32_t keys = -1;                                     // rows of no sequence stay
   for (int s = lane; s < p.sequences; s += 32) {
@@ -468,17 +475,17 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const FwdParam
     if (token >= q0 && token < q0 + nq) keys = nk;
   }
   keys = __reduce_max_sync(0xffffffffu, keys);
-  if (keys < 0) return;                                  // (the whole block)
+  if (keys < 0) return;                                  // (all of the row's warps)
   // (a sequence has two parts for each `chunk` tiles of its keys)
   const int32_t step = p.chunk * kTile, parts = step > 0 ? 2 * ((keys + step - 1) / step) : p.splits;
   float top = -CUDART_INF_F, sum = 0.0f, o[4] = {};
   const int c = lane * 4;
-  for (int i0 = warp; i0 < parts; i0 += 4 * kWarps) {
+  for (int i0 = warp; i0 < parts; i0 += 4 * WARPS) {
     float l[4];
     float4 v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int i = i0 + k * kWarps;
+      const int i = i0 + k * WARPS;
       l[k] = -CUDART_INF_F;
       v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (i < parts) {
@@ -504,25 +511,27 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const FwdParam
       }
     }
   }
-  sums[warp][lane] = make_float4(o[0], o[1], o[2], o[3]);
-  if (lane == 0) {
-    tops[warp] = top;
-    totals[warp] = sum;
-  }
-  __syncthreads();
-  if (warp != 0) return;
+  if constexpr (WARPS > 1) {
+    sums[warp][lane] = make_float4(o[0], o[1], o[2], o[3]);
+    if (lane == 0) {
+      tops[warp] = top;
+      totals[warp] = sum;
+    }
+    __syncthreads();
+    if (warp != 0) return;
 #pragma unroll
-  for (int i = 1; i < kWarps; ++i) top = fmaxf(top, tops[i]);
-  const float base = top == -CUDART_INF_F ? 0.0f : top;
-  sum = o[0] = o[1] = o[2] = o[3] = 0.0f;
+    for (int i = 1; i < WARPS; ++i) top = fmaxf(top, tops[i]);
+    const float base = top == -CUDART_INF_F ? 0.0f : top;
+    sum = o[0] = o[1] = o[2] = o[3] = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    const float w = exp2_fast(tops[i] - base);
-    const float4 v = sums[i][lane];
-    sum = fmaf(w, totals[i], sum);
-    if (w != 0.0f) {
-      o[0] = fmaf(w, v.x, o[0]); o[1] = fmaf(w, v.y, o[1]);
-      o[2] = fmaf(w, v.z, o[2]); o[3] = fmaf(w, v.w, o[3]);
+    for (int i = 0; i < WARPS; ++i) {
+      const float w = exp2_fast(tops[i] - base);
+      const float4 v = sums[i][lane];
+      sum = fmaf(w, totals[i], sum);
+      if (w != 0.0f) {
+        o[0] = fmaf(w, v.x, o[0]); o[1] = fmaf(w, v.y, o[1]);
+        o[2] = fmaf(w, v.z, o[2]); o[3] = fmaf(w, v.w, o[3]);
+      }
     }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -550,11 +559,13 @@ FwdPlan plan(const boost_attention_desc& d) {
   f.tok = kTile / f.pack;
   f.splits = f.parts = 1;
   const int64_t heads = d.hq / f.pack, keys = (d.Tk + kTile - 1) / kTile;
-  // All queries are a tile's: parts of the keys of a fixed length, three for each SM, but long
-  // enough that the parts' own traffic stays below half of the keys' and values'.
+  // All queries are a tile's: parts of the keys of a fixed length, two for each SM, but long
+  // enough that the parts' own traffic stays below half of the keys' and values'. (A token of eight
+  // sequences of 1 to 16384 keys, 40 heads, 8 of keys: 54 us, in equal parts 68; with three parts an
+  // SM 55, with one 62. 32 x 2048 keys, 8 heads: 60, three 62, one 55.)
   if (d.Tq <= f.tok) {
     const int64_t rows = d.Tq / d.sequences * f.pack;
-    const int64_t chunk = std::max<int64_t>({4, rows / 16, (keys * heads + 455) / 456});
+    const int64_t chunk = std::max<int64_t>({4, rows / 16, (keys * heads + 303) / 304});
     if (keys > chunk) {
       f.chunk = static_cast<int>(std::min<int64_t>(chunk, 1 << 20));
       f.parts = static_cast<int>(2 * ((keys + f.chunk - 1) / f.chunk));
@@ -562,12 +573,16 @@ FwdPlan plan(const boost_attention_desc& d) {
       return f;
     }
   }
-  // Else as many equal parts as fill the SMs, each with four tiles of an average sequence's keys.
+  // Else as many equal parts as an SM each takes at once, with four tiles of an average sequence's
+  // keys or more. (512 queries over 8192 keys, 8 heads: 30 us, in one part 100; 300 over 6000, 2
+  // heads: 23, one 76, parts of two tiles 21; 512 over 512, 8 heads: 14.5 in one part, 18.6 in parts
+  // of two tiles.)
   f.tiles = most_tiles(d.Tq, 2 * f.tok, d.sequences);
-  const int64_t ctas = f.tiles * heads;
+  const int64_t each = (d.Tq + d.sequences - 1) / d.sequences;
+  const int64_t ctas = (each + 2 * f.tok - 1) / (2 * f.tok) * d.sequences * heads;
   if (ctas > 0)
     f.splits = static_cast<int>(
-        std::max<int64_t>(1, std::min<int64_t>({304 / ctas, d.Tk / d.sequences / kTile / 4, 64})));
+        std::max<int64_t>(1, std::min<int64_t>({152 / ctas, d.Tk / d.sequences / kTile / 4, 64})));
   f.parts = f.splits;
   return f;
 }
@@ -648,7 +663,9 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream) {
     e = d.dim <= 64 ? launch_fwd<64, false>(p, stream) : launch_fwd<128, false>(p, stream);
   if (e != cudaSuccess || f.parts == 1) return e;
   prof_note_kernels(1);
-  return launch_k(attention_join_kernel, rows, stream, p);
+  constexpr int kWarps = kThreads / 32;
+  if (f.parts > 2 * kWarps) return launch_k(attention_join_kernel<kWarps>, rows, stream, p);
+  return launch_k(attention_join_kernel<1>, (rows + kWarps - 1) / kWarps, stream, p);
 }
 
 }  // namespace boost_gb300
