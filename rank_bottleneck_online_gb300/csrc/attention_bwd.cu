@@ -31,6 +31,15 @@
 // warps are the rows of a tile, four threads a row. The products of one kind run while the threads
 // work on the other's scores: acc1 += P B and the next S during dS, acc2 += dS Y0 and the next dP
 // during P.
+//
+// Measured, both passes: 16384 tokens in four sequences, 16 heads of 128, 1265 us (1.09 PFLOP/s by the
+// formula's 5 products, 1.74 by the 8 done), causal 754. A step of four products takes the tensor
+// core 2048 cycles and lasts about 2800 in the first pass and 2600 in the second (tensor pipe 66%
+// and 72% busy): the chain from a product over the threads' work to the next one. Between works pass
+// about 9000 cycles. Not faster: P handed over whole (826 us causal, 797 then in halves), dS in halves
+// (769, 753 then), a half's exponents begun before the one before is handed over (784), two sets of 64
+// columns in turns (995, 961 then), two buffers of S for heads of 64 (416 us for 426, and 685 for
+// 678).
 #include <math_constants.h>
 
 #include <atomic>

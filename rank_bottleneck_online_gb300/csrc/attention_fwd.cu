@@ -18,6 +18,15 @@
 // single tile's (a decoding step), into parts of a fixed number of key tiles, so that long and
 // short sequences fill the SMs alike. There A and B are the same queries, A with the even and B
 // with the odd tiles of a part: two steps of a chain of load, product, softmax, product at a time.
+//
+// Measured: 16384 tokens in four sequences, 16 heads of 128, 375 us (1.47 PFLOP/s), causal 222 (1.24).
+// A step of both tiles takes the tensor core 2048 cycles and lasts about 3000: what bounds it is each
+// tile's chain (scores, softmax of a row in one thread, product) and the issuing warp's waits for
+// both (tensor pipe 53-60% busy, issue slots 35%). Not faster: CTAs that go from tile to tile (290-320
+// us causal), CTA pairs, two threads a row (spills), an issuing warp for each tile (567 us), the next
+// K and V awaited behind queued products (409), P handed over whole (405) or its second half's
+// exponents begun before the first is handed over (377). Decoding: a token of eight sequences of 1 to
+// 16384 keys, 40 heads over 8: 53 us, 4.6 TB/s of their keys and values.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -630,10 +639,17 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream) {
   p.pack = f.pack;
   p.tok = f.tok;
   p.group = d.hq / p.pack / d.hk;
-  // (With a causal mask all heads are one set: the tiles with most work, of every head, go out
-  // first. 16384 tokens in four sequences, 16 heads: 225 us, in sets of three heads 254; without the
-  // mask, where all have as much, 418 and 402.)
-  p.order = grid_order(d.hq / p.pack, f.tiles, d.causal ? 0.0 : 4.0 * d.dim * d.Tk / p.group);
+  // With a causal mask a set of heads ends with its shortest tiles, and the next begins with long ones:
+  // few and equal sets, of about 96 MB. (16384 tokens in four sequences, causal: 16 heads 222 us in one
+  // set, 254 in sets of three heads; 32 heads 437 in three sets, 457 in one. Without the mask, where
+  // all tiles have as much, 16 heads 418 in one set and 402 in sets of 32 MB.)
+  const int heads = d.hq / p.pack;
+  const double bytes = 4.0 * d.dim * d.Tk / p.group;      // of a head's keys and values
+  p.order = grid_order(heads, f.tiles, bytes);
+  if (d.causal) {
+    const int sets = std::max(1, static_cast<int>(std::min(bytes * heads / 96e6 + 0.5, 1.0 * heads)));
+    p.order.set = (heads + sets - 1) / sets;
+  }
   if (!heads_map(&p.tmQ, a.q.at, a.ws, d.Tq, d.hq, d.dim, d.q_ts, d.q_hs, p.pack, p.tok) ||
       !heads_map(&p.tmK, a.k.at, a.ws, d.Tk, d.hk, d.dim, d.k_ts, d.k_hs, 1, kTile) ||
       !heads_map(&p.tmV, a.v.at, a.ws, d.Tk, d.hk, d.dim, d.v_ts, d.v_hs, 1, kTile))

@@ -255,7 +255,9 @@ __device__ __forceinline__ Place find_tile(const int32_t* q_starts, const int32_
       const uint32_t has = __ballot_sync(kAll, index < sum);
       if (has != 0) {
         src = __ffs(has) - 1;
-        f.tile = index - __shfl_sync(kAll, sum - mine.tiles, src);
+        // (inside the sequence whatever the starts hold: sums over ones that overlap may wrap)
+        f.tile = min(max(index - __shfl_sync(kAll, sum - mine.tiles, src), 0),
+                     max(__shfl_sync(kAll, mine.tiles, src) - 1, 0));
       } else {
         index -= __shfl_sync(kAll, sum, 31);
       }

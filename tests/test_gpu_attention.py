@@ -9,8 +9,8 @@ from oracle import ops
 from rank_bottleneck_online_gb300 import binding as B
 from rank_bottleneck_online_gb300 import build as build_mod
 
-from attention_parity import FINE, SENTINEL, Case
-from ops_parity import BF, f64, normal
+from attention_parity import FINE, SENTINEL, SLACK, Case
+from ops_parity import BF, close, f64, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -324,6 +324,39 @@ def test_offsets_beyond_32_bits():
     torch.testing.assert_close(lse, near[1], atol=2.0 ** -10, rtol=0)
     want = ops.attention(f64(q), f64(k[-200:]), f64(v[-200:]), [(3, 200)])
     assert np.abs(f64(out) - want["out"]).max() < 0.02
+
+
+def test_gradients_beyond_32_bits():
+    """The last tokens of long tensors, whose other rows lie in no sequence and stay as they are."""
+    T, heads, dim, n = (1 << 20) + 300, 32, 128, 200
+    big = [torch.full((T, heads, dim), SENTINEL, dtype=BF, device="cuda") for _ in range(4)]
+    near = [normal(seed, n, heads, dim) for seed in (21, 22, 23, 24)]     # q, dout, k, v
+    k, v, dk, dv = big
+    k[-n:], v[-n:] = near[2], near[3]
+    starts = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    far = torch.tensor([T - n, T], dtype=torch.int32, device="cuda")
+    ws = B.Workspace(B.attention_workspace_bytes(n, T, heads, heads, dim))
+    out, lse = B.attention(near[0], k, v, ws, q_starts=starts, k_starts=far)
+    dq, _, _ = B.attention_bwd(near[0], k, v, out, lse, near[1], ws, q_starts=starts, k_starts=far,
+                               dk=dk, dv=dv)
+    B.check(ws)
+    want = ops.attention(*map(f64, (near[0], near[2], near[3])), [(n, n)], True, None, f64(near[1]))
+    for got, name in ((dq, "dq"), (dk[-n:], "dk"), (dv[-n:], "dv")):
+        close(got, want[name], SLACK * want[f"{name}_size"])
+    for t in (dk, dv):
+        assert (t[:-n] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("n", [2, 40])
+def test_starts_beyond_the_rows_count_as_their_bounds(n):
+    c = Case([(60, 90)] * n, 4, 2, 64, seed=25)
+    want = c.forward()
+    grads = c.backward(*want)
+    for s in (c.q_starts, c.k_starts):
+        s[0], s[-1] = -7, 1 << 30
+    got = c.forward()
+    for a, b in zip((*want, *grads), (*got, *c.backward(*got))):
+        assert torch.equal(a, b)
 
 
 def test_refuses_what_the_binding_sees():
