@@ -14,10 +14,13 @@
 //
 // delta: sum_d dout out is its value but for the rounding of out, which is of the size of dS
 // where a row's probability lies on few keys (a row of one key: dS = 0). The first pass takes
-// delta from out and sums what is missing, e = sum_j P (dP - delta), beside sum_j P k in TMEM;
-// dq = scale (sum dS k - e sum P k), and the second pass reads delta + e. (Without that the
-// gradients of 77 tokens were off by 0.0030, relative to all, with it by the 0.002 of a bf16
-// result and bf16 dS.)
+// delta from out and sums what is missing, e = sum_j P (dP - delta), beside sum_j P k in TMEM, and
+// the second pass reads delta + e. (Without that the gradients of 77 tokens were off by 0.0030,
+// relative to all, with it by the 0.002 of a bf16 result and bf16 dS.) A row's dS sum to 0, so what
+// its keys have in common has no part in dq, but has in the sum's error by dS's rounding: dq = scale
+// (sum dS k - r sum P k) with r, e's sum over dS as rounded, in place of e. (Heads of 40
+// values, scores spread by up to 4, 6641 tokens: dq off by 1.50 times a bf16 result's rounding with
+// e, 1.32 with r; it costs 1%.)
 //
 // A tile of 128 x 128 products takes 512 cycles of the tensor core, and reads 128 bytes a cycle of
 // shared memory while both operands lie there, which is all that there is: the loads' writes cost
@@ -32,8 +35,8 @@
 // work on the other's scores: acc1 += P B and the next S during dS, acc2 += dS Y0 and the next dP
 // during P.
 //
-// Measured, both passes: 16384 tokens in four sequences, 16 heads of 128, 1265 us (1.09 PFLOP/s by the
-// formula's 5 products, 1.74 by the 8 done), causal 754. A step of four products takes the tensor
+// Measured, both passes: 16384 tokens in four sequences, 16 heads of 128, 1275 us (1.08 PFLOP/s by the
+// formula's 5 products, 1.73 by the 8 done), causal 735. A step of four products takes the tensor
 // core 2048 cycles and lasts about 2800 in the first pass and 2600 in the second (tensor pipe 66%
 // and 72% busy): the chain from a product over the threads' work to the next one. Between works pass
 // about 9000 cycles. Not faster: P handed over whole (826 us causal, 797 then in halves), dS in halves
@@ -86,8 +89,8 @@ struct BwdCfg {
   static constexpr int kStatOffset = 2 * kTileBytes + 2 * kSlotKinds * kSlotBytes;
   static constexpr int kParts = 4;                       // threads of a row
   static constexpr int kCols = kTile / kParts;           // of its scores, each
-  // two buffers of lse and delta; kDq: and two of the parts of e
-  static constexpr int kStatBytes = (4 + 2 * kParts) * 4 * kTile;
+  // two buffers of lse and delta; kDq: and two of the parts of e and r
+  static constexpr int kStatBytes = (4 + 4 * kParts) * 4 * kTile;
   static constexpr int kWarps = 4 * kParts;              // that work on the scores
   static constexpr int kStageOffset = kStatOffset + kStatBytes;   // 16 rows of 64 bytes a warp
   static constexpr int kSchedOffset = kStageOffset + kWarps * 1024;
@@ -160,14 +163,30 @@ __device__ __forceinline__ void store_rows(const HeadsOut& out, int32_t head, in
   }
 }
 
+// Adds a pair of bf16 values to two sums, an instruction each.
+__device__ __forceinline__ void add_bf16x2(float2& sum, uint32_t pair) {
+  asm("{\n\t.reg .b16 x, y;\n\t"
+      "mov.b32 {x, y}, %2;\n\t"
+      "add.f32.bf16 %0, x, %0;\n\t"
+      "add.f32.bf16 %1, y, %1;\n\t}"
+      : "+f"(sum.x), "+f"(sum.y)
+      : "r"(pair));
+}
+
 // Rounds s to bf16 as an operand in TMEM, pairs of columns a word: N / 2 words from `to` on; with
-// FINE what that rounds off as another operand, `apart` words behind it.
+// FINE what that rounds off as another operand, `apart` words behind it. The rounded values are
+// added to `kept`, if it is given.
 template <int N, bool FINE>
-__device__ __forceinline__ void store_operand(uint32_t to, uint32_t apart, const float* s) {
+__device__ __forceinline__ void store_operand(uint32_t to, uint32_t apart, const float* s,
+                                              float2* kept = nullptr) {
   static_assert(N == 16 || (N == 32 && !FINE), "");
   uint32_t hi[N / 2];
 #pragma unroll
   for (int c = 0; c < N; c += 2) hi[c / 2] = pack_bf16x2(s[c], s[c + 1]);
+  if (kept != nullptr) {
+#pragma unroll
+    for (int c = 0; c < N / 2; ++c) add_bf16x2(kept[c & 1], hi[c]);
+  }
   if constexpr (N == 16) tmem_st_32x32b_x8(to, hi); else tmem_st_32x32b_x16(to, hi);
   if constexpr (FINE) {
     uint32_t lo[N / 2];
@@ -598,7 +617,8 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
     while (have) {
       const int32_t x = t.x0 + row;                       // in the sequence
       const bool valid = x < t.nx;
-      float lse = 0.0f, delta = 0.0f, e = 0.0f;           // kDq: of this row; what delta lacks
+      // kDq: of this row; what delta lacks, and the same sum over dS as rounded
+      float lse = 0.0f, delta = 0.0f, e = 0.0f, rounded = 0.0f;
       if (PASS == kDq) {
         const float* st = stat + (stats & 1) * 2 * kTile;
         ok = warp_wait_all(&stat_full[stats & 1], stats >> 1 & 1, p.err, 69, p.wait_limit_ns);
@@ -673,7 +693,9 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
           store_operand<kCols / 2, true>(d_at, kCols / 2, d);
           store_operand<kCols / 2, true>(d_at + kCols / 4, kCols / 2, d + kCols / 2);
         } else {
-          store_operand<kCols, false>(d_at, 0, d);
+          float2 kept[2] = {};
+          store_operand<kCols, false>(d_at, 0, d, PASS == kDq ? kept : nullptr);
+          if (PASS == kDq) rounded += (kept[0].x + kept[0].y) + (kept[1].x + kept[1].y);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -684,15 +706,22 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
         }
         if (++tile == t.first + t.count) tile = t.first;
       }
-      if (PASS == kDq) {                                  // e over the row's parts, in order
-        float* parts = stat + 4 * kTile + (stats & 1) * Cfg::kParts * kTile;
+      if (PASS == kDq) {                                  // over the row's parts, in order
+        float* parts = stat + 4 * kTile + (stats & 1) * 2 * Cfg::kParts * kTile;
+        float* others = parts + Cfg::kParts * kTile;
         parts[part * kTile + row] = e;
+        if (!FINE) others[part * kTile + row] = rounded;
         __syncwarp();
         if (lane == 0) mbar_arrive(sync_bar);
         ok = ok && warp_wait_all(sync_bar, stats & 1, p.err, 73, p.wait_limit_ns);
         e = parts[row];
+        if (!FINE) rounded = others[row];
 #pragma unroll
-        for (int i = 1; i < Cfg::kParts; ++i) e += parts[i * kTile + row];
+        for (int i = 1; i < Cfg::kParts; ++i) {
+          e += parts[i * kTile + row];
+          if (!FINE) rounded += others[i * kTile + row];
+        }
+        if (FINE) rounded = e;
         if (ok && valid && part == 0) p.delta[w.head * p.Tq + t.x_row + row] = delta + e;
         ++stats;
       }
@@ -722,8 +751,8 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
           if (PASS == kDq) {
-            a2[k] = fmaf(-e, a1[k], a2[k]);
-            a2[k + 1] = fmaf(-e, a1[k + 1], a2[k + 1]);
+            a2[k] = fmaf(-rounded, a1[k], a2[k]);
+            a2[k + 1] = fmaf(-rounded, a1[k + 1], a2[k + 1]);
           }
           g2[(c + k) / 2] = pack_bf16x2(scale * a2[k], scale * a2[k + 1]);
           if (PASS == kDkv) g1[(c + k) / 2] = pack_bf16x2(a1[k], a1[k + 1]);
@@ -755,7 +784,9 @@ cudaError_t launch_pass(BwdParams p, int64_t T, cudaStream_t stream) {
   // the other side: k and v of a key head, or q and dout of its query heads
   const double bytes = 4.0 * p.dim * (PASS == kDq ? static_cast<double>(p.Tk) / p.group
                                                   : static_cast<double>(p.Tq) * p.group);
-  p.order = grid_order(p.order.heads, most_tiles(T, CG * kTile, p.sequences), bytes);
+  // (16 x 1024 tokens, 16 heads, causal: four sets of four heads 354 us, five of three and one of one
+  // 371; sets of 96 MB 381)
+  p.order = grid_order(p.order.heads, most_tiles(T, CG * kTile, p.sequences), bytes, 32e6);
   // (some waits last as long as a tile's work: 4 us a step at most, on top of the limit)
   const int64_t steps = PASS == kDq ? p.Tk / kTile + 1 : (p.Tq / kTile + 1) * p.group;
   p.wait_limit_ns += 4000 * static_cast<uint64_t>(steps);

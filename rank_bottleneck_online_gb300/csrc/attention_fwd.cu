@@ -643,13 +643,7 @@ cudaError_t launch_attention(const AttentionArgs& a, cudaStream_t stream) {
   // few and equal sets, of about 96 MB. (16384 tokens in four sequences, causal: 16 heads 222 us in one
   // set, 254 in sets of three heads; 32 heads 437 in three sets, 457 in one. Without the mask, where
   // all tiles have as much, 16 heads 418 in one set and 402 in sets of 32 MB.)
-  const int heads = d.hq / p.pack;
-  const double bytes = 4.0 * d.dim * d.Tk / p.group;      // of a head's keys and values
-  p.order = grid_order(heads, f.tiles, bytes);
-  if (d.causal) {
-    const int sets = std::max(1, static_cast<int>(std::min(bytes * heads / 96e6 + 0.5, 1.0 * heads)));
-    p.order.set = (heads + sets - 1) / sets;
-  }
+  p.order = grid_order(d.hq / p.pack, f.tiles, 4.0 * d.dim * d.Tk / p.group, d.causal ? 96e6 : 32e6);
   if (!heads_map(&p.tmQ, a.q.at, a.ws, d.Tq, d.hq, d.dim, d.q_ts, d.q_hs, p.pack, p.tok) ||
       !heads_map(&p.tmK, a.k.at, a.ws, d.Tk, d.hk, d.dim, d.k_ts, d.k_hs, 1, kTile) ||
       !heads_map(&p.tmV, a.v.at, a.ws, d.Tk, d.hk, d.dim, d.v_ts, d.v_hs, 1, kTile))

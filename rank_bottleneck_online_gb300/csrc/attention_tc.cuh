@@ -315,17 +315,17 @@ __device__ __forceinline__ int32_t clc_answer(const void* response) {
   return canceled != 0u ? static_cast<int32_t>(x) : -1;
 }
 
-// The grid's order: heads in sets of `set` whose other side (what the tiles stream through) stays
-// in L2, within a set tile by tile, the set's heads side by side.
+// The grid's order: heads in equal sets of about `bytes` of the other side (what the tiles stream
+// through, which stays in L2), within a set tile by tile, the set's heads side by side.
 struct Order {
   int32_t heads, set, tiles;             // tiles: the most that there can be
 };
 
-inline Order grid_order(int64_t heads, int64_t tiles, double bytes_per_head) {
-  constexpr double kSet = 32e6;          // of 129 MB of L2
-  const double fit = kSet / std::max(bytes_per_head, 1.0);
-  const int64_t set = std::max<int64_t>(1, std::min<int64_t>(heads, static_cast<int64_t>(fit)));
-  return {static_cast<int32_t>(heads), static_cast<int32_t>(set), static_cast<int32_t>(tiles)};
+inline Order grid_order(int64_t heads, int64_t tiles, double bytes_per_head, double bytes) {
+  const double sets = std::min(std::floor(bytes_per_head * heads / bytes + 0.5), 1.0 * heads);
+  const int64_t n = std::max<int64_t>(1, static_cast<int64_t>(sets));
+  return {static_cast<int32_t>(heads), static_cast<int32_t>((heads + n - 1) / n),
+          static_cast<int32_t>(tiles)};
 }
 
 struct Work {

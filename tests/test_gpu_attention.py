@@ -285,6 +285,30 @@ def test_outputs_between_the_heads_of_a_packed_buffer():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dim", [40, 64, 128])
+def test_what_the_keys_have_in_common_adds_nothing_to_dq(dim):
+    """A row's dS sum to 0, so rounding them may cost dq 2^-8 of the sum of |dS| |k - k'| alone, k' the
+    row's mean key, and of |k| only what fp32 loses (2^-11: SLACK's fp32 part twice)."""
+    n, heads = 700, 2
+    common = 4 * normal(31, 1, heads, dim).float()
+    q, k, v, do = (normal(32 + i, n, heads, dim) for i in range(4))
+    k = (k.float() + common).to(BF)
+    scale = dim ** -0.5
+    ws = B.Workspace(B.attention_workspace_bytes(n, n, heads, heads, dim))
+    out, lse = B.attention(q, k, v, ws, causal=False)
+    dq, _, _ = B.attention_bwd(q, k, v, out, lse, do, ws, causal=False)
+    B.check(ws)
+    for h in range(heads):
+        x, y, z, g = (f64(t[:, h]) for t in (q, k, v, do))
+        s = x @ y.T * scale
+        p = np.exp(s - s.max(1, keepdims=True))
+        p /= p.sum(1, keepdims=True)
+        ds = p * (g @ z.T - (g * (p @ z)).sum(1, keepdims=True)) * scale
+        mean = p @ y
+        apart = np.stack([np.abs(ds[i]) @ np.abs(y - mean[i]) for i in range(n)])
+        close(dq[:, h], ds @ y, 2.0 ** -8 * apart + 2.0 ** -11 * (np.abs(ds) @ np.abs(y)))
+
+
 def test_gradients_by_differences():
     """(f(x + e d) - f(x - e d)) / 2e of f = sum dout out in direction d, on the fp64 definition
     with the kernel's gradients: they point where the definition's values go."""
