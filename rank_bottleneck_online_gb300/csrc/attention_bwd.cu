@@ -173,28 +173,48 @@ __device__ __forceinline__ void add_bf16x2(float2& sum, uint32_t pair) {
       : "r"(pair));
 }
 
-// Rounds s to bf16 as an operand in TMEM, pairs of columns a word: N / 2 words from `to` on; with
-// FINE what that rounds off as another operand, `apart` words behind it. The rounded values are
-// added to `kept`, if it is given.
-template <int N, bool FINE>
-__device__ __forceinline__ void store_operand(uint32_t to, uint32_t apart, const float* s,
+// Rounds s to bf16 as an operand in TMEM, pairs of columns a word: N / 2 words from `to` on; what that
+// rounds off, where `fine`, as another operand `apart` words behind it. The rounded values are added
+// to `kept`, if it is given.
+template <int N>
+__device__ __forceinline__ void store_operand(uint32_t to, uint32_t apart, const float* s, bool fine,
                                               float2* kept = nullptr) {
-  static_assert(N == 16 || (N == 32 && !FINE), "");
-  uint32_t hi[N / 2];
+  static_assert(N == 16 || N == 32, "");
+  uint32_t w[N / 2];
 #pragma unroll
-  for (int c = 0; c < N; c += 2) hi[c / 2] = pack_bf16x2(s[c], s[c + 1]);
+  for (int c = 0; c < N; c += 2) w[c / 2] = pack_bf16x2(s[c], s[c + 1]);
   if (kept != nullptr) {
 #pragma unroll
-    for (int c = 0; c < N / 2; ++c) add_bf16x2(kept[c & 1], hi[c]);
+    for (int c = 0; c < N / 2; ++c) add_bf16x2(kept[c & 1], w[c]);
   }
-  if constexpr (N == 16) tmem_st_32x32b_x8(to, hi); else tmem_st_32x32b_x16(to, hi);
-  if constexpr (FINE) {
-    uint32_t lo[N / 2];
+  if constexpr (N == 16) tmem_st_32x32b_x8(to, w); else tmem_st_32x32b_x16(to, w);
+  if (fine) {
 #pragma unroll
     for (int c = 0; c < N; c += 2)
-      lo[c / 2] = pack_bf16x2(s[c] - bf16_lo(hi[c / 2]), s[c + 1] - bf16_hi(hi[c / 2]));
-    tmem_st_32x32b_x8(to + apart, lo);
+      w[c / 2] = pack_bf16x2(s[c] - bf16_lo(w[c / 2]), s[c + 1] - bf16_hi(w[c / 2]));
+    if constexpr (N == 16) tmem_st_32x32b_x8(to + apart, w); else tmem_st_32x32b_x16(to + apart, w);
   }
+}
+
+// Whether a call has few scores, of all heads and of up to 32 sequences: P and dS are two operands each
+// then. The roundings of few values do not average out (gradients of 6 tokens of one head were off
+// by 0.0033, relative to all, where a bf16 result alone is by 0.0016, and those of long sequences by
+// 0.0024), and the tensor cores have little else to do (77 tokens, 16 heads, forward and backward: 35
+// us, 32 without). By a whole warp.
+__device__ __forceinline__ bool few_scores(const BwdParams& p, int32_t heads) {
+  if (p.sequences > 32) return false;
+  constexpr int64_t kMost = 1 << 18;
+  const int lane = threadIdx.x & 31;
+  int64_t pairs = 0;
+  if (lane < p.sequences) {
+    int32_t q0, nq, k0, nk;
+    sequence_bounds(p.q_starts, p.Tq, lane, q0, nq);
+    sequence_bounds(p.k_starts, p.Tk, lane, k0, nk);
+    const int64_t m = min(nq, nk);
+    pairs = p.causal ? m * nk - m * (m - 1) / 2 : static_cast<int64_t>(nq) * nk;
+  }
+  const uint32_t all = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(min(pairs, kMost + 1)));
+  return static_cast<int64_t>(all) * heads <= kMost;
 }
 
 template <int HD, int CG, int PASS, bool FINE>
@@ -279,6 +299,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
 
+  const bool fine = FINE && few_scores(p, PASS == kDq ? p.order.heads : p.order.heads * p.group);
   const int ksteps = (p.dim + 15) / 16;
   const int32_t width = CG == 2 ? (p.dim + 31) / 32 * 32 : 16 * ksteps;   // columns of the sums
   uint32_t works = 0;                                    // of this warp so far
@@ -463,7 +484,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
           tc_fence_after();
           if (elect_one()) {
             issue_sums<CG, Cfg::kCols, 0, 2>(tAcc1, tS, b1, id_acc, i > 0);
-            if (FINE) issue_sums<CG, Cfg::kCols, 0, 2>(tAcc1, tS + Cfg::kCols / 2, b1, id_acc, true);
+            if (fine) issue_sums<CG, Cfg::kCols, 0, 2>(tAcc1, tS + Cfg::kCols / 2, b1, id_acc, true);
           }
           __syncwarp();
           ok = written(&p_bar[1], u, 64);
@@ -471,7 +492,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
           tc_fence_after();
           if (elect_one()) {
             issue_sums<CG, Cfg::kCols, 1, 2>(tAcc1, tS, b1, id_acc, true);
-            if (FINE) issue_sums<CG, Cfg::kCols, 1, 2>(tAcc1, tS + Cfg::kCols / 2, b1, id_acc, true);
+            if (fine) issue_sums<CG, Cfg::kCols, 1, 2>(tAcc1, tS + Cfg::kCols / 2, b1, id_acc, true);
             if (PASS == kDkv) free_slot(k1m, u);
           }
           __syncwarp();
@@ -491,7 +512,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
           tc_fence_after();
           if (elect_one()) {
             issue_sums<CG, Cfg::kCols>(tAcc2, tD, b2, id_acc, i > 0);
-            if (FINE) issue_sums<CG, Cfg::kCols>(tAcc2, tD + Cfg::kCols / 2, b2, id_acc, true);
+            if (fine) issue_sums<CG, Cfg::kCols>(tAcc2, tD + Cfg::kCols / 2, b2, id_acc, true);
             free_slot(k0m, u);
             if (!more) commit(acc_bar);
           }
@@ -662,7 +683,7 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
             for (int c = half * kHalf; c < (half + 1) * kHalf; ++c)
               s[c] = (PASS == kDq ? c < lim : c >= lim) ? s[c] : 0.0f;
           }
-          store_operand<kHalf, FINE>(s_at + half * (kHalf / 2), kCols / 2, s + half * kHalf);
+          store_operand<kHalf>(s_at + half * (kHalf / 2), kCols / 2, s + half * kHalf, fine);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -689,14 +710,9 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
           d[c + 1] = x.y;
         }
         if (PASS == kDq) e += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        if constexpr (FINE) {
-          store_operand<kCols / 2, true>(d_at, kCols / 2, d);
-          store_operand<kCols / 2, true>(d_at + kCols / 4, kCols / 2, d + kCols / 2);
-        } else {
-          float2 kept[2] = {};
-          store_operand<kCols, false>(d_at, 0, d, PASS == kDq ? kept : nullptr);
-          if (PASS == kDq) rounded += (kept[0].x + kept[0].y) + (kept[1].x + kept[1].y);
-        }
+        float2 kept[2] = {};
+        store_operand<kCols>(d_at, kCols / 2, d, fine, PASS == kDq ? kept : nullptr);
+        if (PASS == kDq) rounded += (kept[0].x + kept[0].y) + (kept[1].x + kept[1].y);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -710,18 +726,18 @@ __global__ void __launch_bounds__(BwdCfg<HD, CG>::kThreads, 1)
         float* parts = stat + 4 * kTile + (stats & 1) * 2 * Cfg::kParts * kTile;
         float* others = parts + Cfg::kParts * kTile;
         parts[part * kTile + row] = e;
-        if (!FINE) others[part * kTile + row] = rounded;
+        others[part * kTile + row] = rounded;
         __syncwarp();
         if (lane == 0) mbar_arrive(sync_bar);
         ok = ok && warp_wait_all(sync_bar, stats & 1, p.err, 73, p.wait_limit_ns);
         e = parts[row];
-        if (!FINE) rounded = others[row];
+        rounded = others[row];
 #pragma unroll
         for (int i = 1; i < Cfg::kParts; ++i) {
           e += parts[i * kTile + row];
-          if (!FINE) rounded += others[i * kTile + row];
+          rounded += others[i * kTile + row];
         }
-        if (FINE) rounded = e;
+        if (fine) rounded = e;
         if (ok && valid && part == 0) p.delta[w.head * p.Tq + t.x_row + row] = delta + e;
         ++stats;
       }
@@ -817,8 +833,11 @@ cudaError_t launch_pass(BwdParams p, int64_t T, cudaStream_t stream) {
 }
 
 template <int PASS>
-cudaError_t launch(const BwdParams& p, int64_t T, bool fine, cudaStream_t stream) {
-  if (fine)
+cudaError_t launch(const BwdParams& p, int64_t T, cudaStream_t stream) {
+  // Where the rows bound the scores by 2^24 (sequences of one length), the kernels that look how many
+  // there are: in the others that would cost 3% (16384 tokens: 735 us, 757).
+  const double heads = static_cast<double>(p.order.heads) * (PASS == kDq ? 1 : p.group);
+  if (static_cast<double>(p.Tq) * p.Tk / p.sequences * heads <= 0x1p24)
     return p.dim <= 64 ? launch_pass<64, 1, PASS, true>(p, T, stream)
                        : launch_pass<128, 1, PASS, true>(p, T, stream);
   if (p.dim <= 64) return launch_pass<64, 1, PASS, false>(p, T, stream);
@@ -856,12 +875,6 @@ cudaError_t launch_attention_bwd(const AttentionArgs& a, cudaStream_t stream) {
   p.scale_log2 = d.scale * kLog2e;
   p.err = static_cast<DeviceError*>(a.ws);
   p.wait_limit_ns = wait_limit_ns();
-  // Few scores (of sequences of one length): P and dS as two operands each. The roundings of few
-  // values do not average out (gradients of 6 tokens of one head were off by 0.0033, relative to
-  // all, where a bf16 result alone is by 0.0016, and those of long sequences by 0.0024), and the
-  // tensor cores have little else to do (77 tokens, 16 heads, forward and backward: 33 us, 32
-  // without).
-  const bool fine = static_cast<double>(d.Tq) * d.Tk / d.sequences * d.hq <= 262144.0;
   if (d.Tq > 0) {
     p.tmX0 = q;
     p.tmX1 = dout;
@@ -871,7 +884,7 @@ cudaError_t launch_attention_bwd(const AttentionArgs& a, cudaStream_t stream) {
     p.dout = a.dout;
     p.g2 = a.dq;
     p.order.heads = d.hq;
-    const cudaError_t e = launch<kDq>(p, d.Tq, fine, stream);
+    const cudaError_t e = launch<kDq>(p, d.Tq, stream);
     if (e != cudaSuccess) return e;
   }
   if (d.Tk == 0) return cudaSuccess;
@@ -883,7 +896,7 @@ cudaError_t launch_attention_bwd(const AttentionArgs& a, cudaStream_t stream) {
   p.g1 = a.dv;
   p.g2 = a.dk;
   p.order.heads = d.hk;
-  return launch<kDkv>(p, d.Tk, fine, stream);
+  return launch<kDkv>(p, d.Tk, stream);
 }
 
 }  // namespace boost_gb300

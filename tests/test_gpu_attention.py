@@ -96,10 +96,11 @@ def test_sequences_of_several_tiles_with_shared_key_heads(hq, hk, layout):
     Case([(700, 700), (1, 900), (850, 610)], hq, hk, 128, layout=layout, tail=3, seed=hq).check()
 
 
-def behind(lengths):
-    """Rows behind the last sequence that make a sequence's share of all rows 2100: the size that
-    the gradients' tiles are chosen by, where the sequences themselves are smaller."""
-    return max(2100 * len(lengths) - min(map(sum, zip(*lengths))), 70)
+def behind(lengths, heads=2):
+    """Rows behind the last sequence that make a sequence's share of all rows 2100, and that of scores
+    2^24: the sizes that the gradients' kernels are chosen by, where the sequences are smaller."""
+    n = len(lengths)
+    return max(2100 * n, int((2.0 ** 24 * n / heads) ** 0.5) + 1) - min(map(sum, zip(*lengths))) + 70
 
 
 @pytest.mark.parametrize("causal", [True, False])
@@ -128,9 +129,15 @@ def test_pairs_of_tiles_do_not_leak(bad):
 @pytest.mark.parametrize("dim", [8, 40, 64, 72, 128])
 @pytest.mark.parametrize("n", [(1, 1), (2, 3), (7, 128), (63, 1), (127, 129), (256, 255), (400, 400)])
 def test_one_sequence_of_many_rows(n, dim, causal):
-    """Rows behind the sequence count as scores of the call, whose number decides how the gradients'
-    operands are rounded."""
+    """Most rows lie behind the sequence."""
     Case([n], 3, 1, dim, causal=causal, tail=600, seed=n[0] + dim).check()
+
+
+@pytest.mark.parametrize("n", [(1, 1), (7, 128), (127, 129), (400, 380)])
+@pytest.mark.parametrize("dim", [64, 72, 128])
+def test_two_sequences_of_many_rows(dim, n):
+    """As many rows as hide how few scores there are."""
+    Case([n, n[::-1]], 12, 6, dim, tail=1900, seed=n[0] + dim).check()
 
 
 @pytest.mark.parametrize("layout", ["planes", "packed", "heads"])
@@ -138,13 +145,15 @@ def test_one_sequence_of_many_rows(n, dim, causal):
 def test_packed_sequences_of_many_rows(dim, layout):
     lengths = [(1, 1), (0, 5), (130, 130), (7, 300), (5, 0), (0, 0), (256, 256), (64, 65), (3, 2)]
     Case(lengths, 4, 2, dim, tail=2000, layout=layout, seed=dim).check()
+    Case(lengths, 4, 2, dim, tail=6000, layout=layout, seed=dim).check()
 
 
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("dim", [16, 64, 80, 128])
 @pytest.mark.parametrize("lengths,hq,hk", [([(1, 2)], 1, 1), ([(4, 4), (4, 4)], 2, 1), ([(6, 6)], 1, 1),
                                            ([(33, 65), (5, 1), (0, 3)], 4, 2), ([(130, 257)], 6, 2),
-                                           ([(200, 140), (3, 200)], 6, 6)])
+                                           ([(200, 140), (3, 200)], 6, 6),
+                                           ([(867, 3), (3, 1350)], 2, 1)])
 def test_few_scores(lengths, hq, hk, dim, causal):
     """Gradients that are off by little more than their own rounding."""
     for seed in range(4):
