@@ -28,34 +28,37 @@ struct Slice {
   }
 };
 
-// Whether |x + i step| >= apart for every i from -times to times.
-inline bool stays_away(int64_t x, int64_t step, int64_t times, int64_t apart) {
-  if (step == 0) times = 0;
-  const int64_t n = times == 0 ? 0 : -x / step;        // the nearest is one of n - 1 .. n + 1
+// Whether |x + i step| >= apart for every i from lo to hi.
+inline bool stays_away(int64_t x, int64_t step, int64_t lo, int64_t hi, int64_t apart) {
+  if (step == 0) lo = hi = 0;
+  const int64_t n = step == 0 ? 0 : -x / step;         // the nearest is one of n - 1 .. n + 1
   for (int64_t i = n - 1; i <= n + 1; ++i)
-    if (std::abs(x + std::clamp(i, -times, times) * step) < apart) return false;
+    if (std::abs(x + std::clamp(i, lo, hi) * step) < apart) return false;
   return true;
 }
 
-// Whether two operands share no element: disjoint ranges; heads side by side in the rows of one
-// packed buffer (the same token stride, and spans that do not meet modulo it); or heads that lie
-// between each other's (the same strides, and no pair of heads and tokens that meet).
+// Whether two operands, of as many tokens and heads as each has, share no element: disjoint ranges;
+// heads side by side in the rows of one packed buffer (the same token stride, and spans that do
+// not meet modulo it); or heads that lie between each other's (the same strides, and no pair of
+// heads and tokens that meet). The stride of a single token or head says nothing: the other's
+// counts.
 inline bool disjoint(const Slice& a, const Slice& b) {
   if (a.extent() == 0 || b.extent() == 0) return true;
   if (a.base + a.extent() <= b.base || b.base + b.extent() <= a.base) return true;
-  if (a.T > 1 && a.ts != b.ts) return false;
+  if (a.T > 1 && b.T > 1 && a.ts != b.ts) return false;
+  const int64_t ts = a.T > 1 ? a.ts : b.T > 1 ? b.ts : 0;
   const int64_t away = static_cast<int64_t>(b.base) - static_cast<int64_t>(a.base);   // bytes
-  if (a.T > 1 && a.ts > 0) {
+  if (ts > 0) {
     const int64_t sa = 2 * ((a.heads - 1) * a.hs + a.dim), sb = 2 * ((b.heads - 1) * b.hs + b.dim);
-    const int64_t row = 2 * a.ts;
+    const int64_t row = 2 * ts;
     // where b's span begins within a's rows
     const int64_t o = (away % row + row) % row;
     if (o >= sa && o + sb <= row) return true;
   }
   if (a.heads > 1 && b.heads > 1 && a.hs != b.hs) return false;
-  const int64_t hs = a.heads > 1 ? a.hs : b.hs;
+  const int64_t hs = a.heads > 1 ? a.hs : b.hs, dim = std::max(a.dim, b.dim);
   for (int64_t h = 1 - a.heads; h < b.heads; ++h)      // b's head less a's
-    if (!stays_away(away / 2 + h * hs, a.ts, a.T - 1, a.dim)) return false;
+    if (!stays_away(away / 2 + h * hs, ts, 1 - a.T, b.T - 1, dim)) return false;
   return true;
 }
 
