@@ -159,16 +159,23 @@ class Rotary:
 
 class Attention:
     """The layer's attention core: ``heads`` heads of ``dim`` values, causal unless told otherwise,
-    over packed sequences (``binding.attention``), with what its backward keeps."""
+    over packed sequences (``binding.attention``), with what its backward keeps: a core serves
+    one layer, and a second ``Layer`` that is given it makes one of its own (``like``)."""
 
     def __init__(self, T, heads, dim, *, causal=True, scale=None, sequences=1, device="cuda"):
         """sequences: the most that a call has."""
         self.T, self.heads, self.dim, self.causal, self.scale = T, heads, dim, causal, scale
+        self.sequences, self.taken = sequences, False      # taken: by a layer
         self.out = torch.empty(T, heads * dim, dtype=torch.bfloat16, device=device)
         self.lse = torch.empty(heads, T, dtype=torch.float32, device=device)
         # (of fewer sequences, too: they may be cut in more parts)
         self.workspace_bytes = max(B.attention_workspace_bytes(T, T, heads, heads, dim, s)
                                    for s in range(1, sequences + 1))
+
+    def like(self):
+        """Another core of this form, with buffers of its own."""
+        return Attention(self.T, self.heads, self.dim, causal=self.causal, scale=self.scale,
+                         sequences=self.sequences, device=self.out.device)
 
     def _split(self, t):
         return t.view(self.T, self.heads, self.dim)
@@ -289,7 +296,8 @@ class Layer:
     """QKV (normed, k=3) -> O (k=1) on V -> residual -> MLP -> residual.
 
     attention (an ``Attention``): O works on the attention of q, k and v, and the backward forms
-    their gradients; without it O works on V, and the gradients of q and k are given.
+    their gradients; without it O works on V, and the gradients of q and k are given. The
+    layer's own is its ``attention``: the one given, or one like it where that is another layer's.
 
     Both residual adds run in GEMM epilogues: x1 = x + O(v) in the O block's
     up-projection, out = x1 + MLP(x1) in the MLP's down up-projection; in the backward,
@@ -308,12 +316,16 @@ class Layer:
         p = weights or {}
         self.T, self.d = T, d
         self.rotary, self.dropout, self.seed = rotary, dropout, seed
-        self.attention, self.fused_norm = attention, fused_norm
         if attention is not None and (attention.T, attention.heads * attention.dim) != (T, d):
             raise ValueError(f"the attention core is of {attention.T} tokens and {attention.heads} "
                              f"heads of {attention.dim}, the layer of {T} x {d}")
         if fused_norm and not fp8:
             raise ValueError("the fused norm gives 8-bit values")
+        if attention is not None:
+            if attention.taken:
+                attention = attention.like()
+            attention.taken = True
+        self.attention, self.fused_norm = attention, fused_norm
         block = Fp8Block if fp8 else Block
         self.qkv = block(T, d, r, 3, d, S=S, eps=eps, act=act, has_norm=True,
                          weights={"gamma": p.get("gamma1"), "A": p.get("A_qkv"),
