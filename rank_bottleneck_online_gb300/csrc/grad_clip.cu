@@ -280,13 +280,17 @@ cudaError_t launch(int64_t count, const boost_grad* grads, double max_norm, floa
                static_cast<uint32_t>((grads[i].n + kChunk - 1) / kChunk);
     if (grads[i].wide) p.wide[t >> 5] |= 1u << (t & 31);
   }
-  if (launches.empty()) return cudaMemsetAsync(norm, 0, 4, s);
+  if (launches.empty()) {
+    prof_note_kernels(-1);
+    return cudaMemsetAsync(norm, 0, 4, s);
+  }
   // (every launch of the first pass has all blocks: each leaves its sum)
   for (const ClipParams<N>& p : launches) {
     const cudaError_t e = launch_k(grad_norm_kernel<N>, kBlocks, s, p);
     if (e != cudaSuccess) return e;
   }
   launches.front().norm = norm;            // the last of the second pass
+  int kernels = static_cast<int>(launches.size());
   for (size_t i = launches.size(); i-- > 0;) {
     ClipParams<N>& p = launches[i];
     const bool writes = std::any_of(p.out, p.out + p.tensors, [](void* q) { return q != nullptr; });
@@ -295,8 +299,9 @@ cudaError_t launch(int64_t count, const boost_grad* grads, double max_norm, floa
     const int64_t grid = p.tensors == 0 ? 1 : std::min<int64_t>(p.end[p.tensors - 1], kBlocks);
     const cudaError_t e = launch_k(grad_scale_kernel<N>, grid, s, p);
     if (e != cudaSuccess) return e;
+    ++kernels;
   }
-  prof_note_kernels(static_cast<int>(2 * launches.size()) - 1);
+  prof_note_kernels(kernels - 1);
   return cudaSuccess;
 }
 
