@@ -808,6 +808,11 @@ def _of(t):
     return t.shape, t.stride()
 
 
+def _number(scale):
+    """A plan is kept by its arguments' values: a tensor's would be kept by the tensor."""
+    return None if scale is None else float(scale)
+
+
 def _starts(t, name, device):
     return None if t is None else _take(t, name, torch.int32, t.shape, device)
 
@@ -826,7 +831,7 @@ def attention(q, k, v, ws: Workspace, *, causal=True, scale=None, q_starts=None,
     bf, device = torch.bfloat16, _device()
     if out is None:
         out = torch.empty(q.shape, dtype=bf, device=q.device)
-    D = _attention_plan(_of(q), _of(k), _of(v), _of(out), None, bool(causal), scale,
+    D = _attention_plan(_of(q), _of(k), _of(v), _of(out), None, bool(causal), _number(scale),
                         (None if q_starts is None else q_starts.shape,
                          None if k_starts is None else k_starts.shape))
     if lse is None:
@@ -852,7 +857,7 @@ def attention_bwd(q, k, v, out, lse, dout, ws: Workspace, *, causal=True, scale=
     if dv is None:
         dv = torch.empty(v.shape, dtype=bf, device=q.device)
     D = _attention_plan(_of(q), _of(k), _of(v), _of(out), (_of(dout), _of(dq), _of(dk), _of(dv)),
-                        bool(causal), scale,
+                        bool(causal), _number(scale),
                         (None if q_starts is None else q_starts.shape,
                          None if k_starts is None else k_starts.shape))
     _check(lib().boost_attention_bwd(
