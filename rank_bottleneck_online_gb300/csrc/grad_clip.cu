@@ -171,6 +171,28 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
   if (threadIdx.x == 0) p.sums[blockIdx.x] = (p.first ? 0.0 : p.sums[blockIdx.x]) + sum;
 }
 
+// What scales. A factor below fp32's normal numbers would have few bits, or none: then the values go
+// down first, by a power of two, which is exact for all that do not become 0, and the factor goes
+// up. (By its exponent's bits: fp64 instructions are what small calls wait for.)
+struct Factor {
+  float down, f;
+  __device__ __forceinline__ explicit Factor(double by) {
+    const int hi = __double2hiint(by), exponent = (hi >> 20 & 0x7ff) - 1023;
+    const int up = exponent < -180 ? 149 : exponent < -100 ? 64 : 0;
+    down = up == 149 ? 0x1p-149f : up == 64 ? 0x1p-64f : 1.0f;
+    f = static_cast<float>(__hiloint2double(hi + (up << 20), __double2loint(by)));
+  }
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&x)[N]) const {
+    if (down != 1.0f) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[e] *= down;
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] *= f;
+  }
+};
+
 template <int N>
 __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ ClipParams<N> p) {
   pdl_enter();
@@ -181,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.norm != nullptr) *p.norm = static_cast<float>(norm);
   const double by = p.max_norm / (norm + 1e-6);
   const bool whole = by >= 1.0;            // (a NaN scales)
-  const float f = whole ? 1.0f : static_cast<float>(by);
+  const Factor scale(whole ? 1.0 : by);
   const uint32_t chunks = p.tensors > 0 ? p.end[p.tensors - 1] : 0;
   for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     int64_t at;
@@ -197,11 +219,18 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
         for (int i = 0; i < kChunk / 4 / kThreads; ++i)
           v[i] = *(reinterpret_cast<const float4*>(g) + i * kThreads + threadIdx.x);
 #pragma unroll
-        for (int i = 0; i < kChunk / 4 / kThreads; ++i)
+        for (int i = 0; i < kChunk / 4 / kThreads; ++i) {
+          float x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          scale(x);
           __stcs(reinterpret_cast<float4*>(out) + i * kThreads + threadIdx.x,
-                 make_float4(v[i].x * f, v[i].y * f, v[i].z * f, v[i].w * f));
+                 make_float4(x[0], x[1], x[2], x[3]));
+        }
       } else {
-        for (int i = threadIdx.x; i < n; i += kThreads) out[i] = g[i] * f;
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+          float x[1] = {g[i]};
+          scale(x);
+          out[i] = x[0];
+        }
       }
     } else {
       const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(p.g[t]) + at;
@@ -215,13 +244,15 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
         for (int i = 0; i < kChunk / 8 / kThreads; ++i) {
           float x[8];
           unpack8(v[i], x);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= f;
+          scale(x);
           __stcs(reinterpret_cast<uint4*>(out) + i * kThreads + threadIdx.x, pack8(x));
         }
       } else {
-        for (int i = threadIdx.x; i < n; i += kThreads)
-          out[i] = __float2bfloat16_rn(__bfloat162float(g[i]) * f);
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+          float x[1] = {__bfloat162float(g[i])};
+          scale(x);
+          out[i] = __float2bfloat16_rn(x[0]);
+        }
       }
     }
   }
