@@ -183,7 +183,11 @@ boost_status boost_fp8_matmul(const boost_fp8_matmul_desc* desc, const void* a, 
  * keys, the first ones, see none: their out and gradients are 0, their lse is -infinity. Query
  * head h reads key head h / (hq / hk). Products of bf16 values, sums and the softmax's
  * statistics in fp32; the probabilities and their gradients are rounded to bf16 as the operands
- * of the second products.
+ * of the second products. The backward of a call of few scores (at most 2^18 of all heads, in up to
+ * 32 sequences whose rows bound them by 2^24) takes both as two bf16 operands, 2^-16 off in place
+ * of 2^-8; so the last bits of a sequence's gradients depend on what else is in the call, as those
+ * of its out do on how its keys are cut into parts. Scores and their magnitudes' sums stay within
+ * fp32's range (below 2^127): beyond it out, lse and the gradients are not defined.
  *
  *   Tq, Tk    rows of q and of k and v, >= 0
  *   hq, hk    query and key heads, hq a multiple of hk
@@ -243,7 +247,7 @@ boost_status boost_attention_bwd(const boost_attention_desc* desc, const void* q
  * sum quantised for the 8-bit product that follows:
  *     h = x + residual (bf16)          rstd[t] = (mean_j h[t][j]^2 + eps)^-1/2
  *     q, sf = 8-bit operand of h, or of bf16(gamma[j] h[t][j]), rows alone (block_rows 1)
- * as boost_fp8_quantize gives it. The norm's value is q's times rstd of its row, which the product
+ * as boost_fp8_quantize gives it; squares and their sums in fp32. The norm's value is q's times rstd of its row, which the product
  * applies (row_scale). Its gradient is the normed block's (boost_block_bwd).
  *   T, d       d a multiple of 8
  *   fmt        boost_fp8
@@ -271,7 +275,8 @@ boost_status boost_norm_quantize(int64_t T, int64_t d, int32_t fmt, float eps, c
  *   wide       0: bf16, 1: fp32
  *   max_norm   >= 0; infinity: no scaling of finite gradients
  *   norm       out, fp32 [1] (infinity beyond fp32's range; what scales is its fp64 value)
- *   ws         workspace of boost_grad_clip_workspace_bytes() bytes, 256-byte aligned
+ *   ws         workspace of boost_grad_clip_workspace_bytes() bytes, 256-byte aligned. Calls that
+ *              may run at the same time need one each.
  */
 typedef struct {
     const void* g;

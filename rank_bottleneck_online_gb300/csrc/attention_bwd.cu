@@ -35,8 +35,9 @@
 // work on the other's scores: acc1 += P B and the next S during dS, acc2 += dS Y0 and the next dP
 // during P.
 //
-// Measured, both passes: 16384 tokens in four sequences, 16 heads of 128, 1275 us (1.08 PFLOP/s by the
-// formula's 5 products, 1.73 by the 8 done), causal 735. A step of four products takes the tensor
+// Measured, both passes: 16384 tokens in four sequences, 16 heads of 128, 1280 us (1.07 PFLOP/s by the
+// formula's 5 products, 1.72 by the 8 done), causal 736, in bursts at 2070 MHz, as all times here;
+// one after another the power cap leaves 1700 to 1850 MHz, and they take 1390 and 790. A step of four products takes the tensor
 // core 2048 cycles and lasts about 2800 in the first pass and 2600 in the second (tensor pipe 66%
 // and 72% busy): the chain from a product over the threads' work to the next one. Between works pass
 // about 9000 cycles. Not faster: P handed over whole (826 us causal, 797 then in halves), dS in halves
@@ -197,10 +198,11 @@ __device__ __forceinline__ void store_operand(uint32_t to, uint32_t apart, const
 }
 
 // Whether a call has few scores, of all heads and of up to 32 sequences: P and dS are two operands each
-// then. The roundings of few values do not average out (gradients of 6 tokens of one head were off
-// by 0.0033, relative to all, where a bf16 result alone is by 0.0016, and those of long sequences by
-// 0.0024), and the tensor cores have little else to do (77 tokens, 16 heads, forward and backward: 35
-// us, 32 without). By a whole warp.
+// then. Rounded once they put the gradients off by 1.3 to 1.4 times what a bf16 result alone is, at
+// any size; but over few values that scatters (6 tokens of one head of 16: 1.14 to 1.61 times in nine
+// draws of ten, up to 2; 200 tokens: 1.36 to 1.42), and the tensor cores have little else to do (77
+// tokens, 16 heads, forward and backward: 35 us, 32 without). A short sequence among many is rounded
+// once, as a long one: what is bounded here is a whole call's error. By a whole warp.
 __device__ __forceinline__ bool few_scores(const BwdParams& p, int32_t heads) {
   if (p.sequences > 32) return false;
   constexpr int64_t kMost = 1 << 18;
@@ -842,9 +844,9 @@ cudaError_t launch(const BwdParams& p, int64_t T, cudaStream_t stream) {
                        : launch_pass<128, 1, PASS, true>(p, T, stream);
   if (p.dim <= 64) return launch_pass<64, 1, PASS, false>(p, T, stream);
   // Pairs where sequences are long. (16384 tokens, 16 heads, us of both passes, singles and pairs: 32 x
-  // 512 334 and 349 causal, 370 and 386 without; 24 x 640 310 and 356, 369 and 407; 16 x 1024 382 and
-  // 387, 468 and 469; 10 x 1664 462 and 481, 658 and 676; 8 x 2048 505 and 504, 780 and 760; 4 x 4096
-  // 820 and 800, 1450 and 1405.)
+  // 512 321 and 344 causal, 357 and 366 without; 24 x 640 306 and 353, 363 and 400; 16 x 1024 355 and
+  // 367, 452 and 444; 10 x 1664 428 and 451, 636 and 651; 8 x 2048 471 and 483, 752 and 723; 6 x 2816
+  // 604 and 615, 1015 and 965; 4 x 4096 788 and 778, 1411 and 1336.)
   if (T / p.sequences >= 2048) return launch_pass<128, 2, PASS, false>(p, T, stream);
   return launch_pass<128, 1, PASS, false>(p, T, stream);
 }

@@ -19,8 +19,9 @@
 // short sequences fill the SMs alike. There A and B are the same queries, A with the even and B
 // with the odd tiles of a part: two steps of a chain of load, product, softmax, product at a time.
 //
-// Measured: 16384 tokens in four sequences, 16 heads of 128, 375 us (1.47 PFLOP/s), causal 222 (1.24).
-// A step of both tiles takes the tensor core 2048 cycles and lasts about 3000: what bounds it is each
+// Measured: 16384 tokens in four sequences, 16 heads of 128, 379 us (1.45 PFLOP/s), causal 225 (1.22),
+// in bursts at 2070 MHz, as all times here (one after another, at the 1920 MHz that the power cap
+// leaves, 397 and 233). A step of both tiles takes the tensor core 2048 cycles and lasts about 3000: what bounds it is each
 // tile's chain (scores, softmax of a row in one thread, product) and the issuing warp's waits for
 // both (tensor pipe 53-60% busy, issue slots 35%). Not faster: CTAs that go from tile to tile (290-320
 // us causal), CTA pairs, two threads a row (spills), an issuing warp for each tile (567 us), the next
@@ -553,7 +554,9 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const FwdParam
 // Heads that share a tile's rows.
 int packed_heads(const boost_attention_desc& d) {
   const int group = d.hq / d.hk;
-  return group <= 32 ? group : 1;        // (128 / 33 tokens would leave a fifth of the rows idle)
+  // (128 / 33 tokens would leave a fifth of the rows idle. A token of 32 sequences of 4096 keys, heads
+  // over one: 32 heads 19 us; 48 heads, each with a tile of its own, 367.)
+  return group <= 32 ? group : 1;
 }
 
 // How a call's work is cut.
@@ -571,7 +574,9 @@ FwdPlan plan(const boost_attention_desc& d) {
   // All queries are a tile's: parts of the keys of a fixed length, two for each SM, but long
   // enough that the parts' own traffic stays below half of the keys' and values'. (A token of eight
   // sequences of 1 to 16384 keys, 40 heads, 8 of keys: 54 us, in equal parts 68; with three parts an
-  // SM 55, with one 62. 32 x 2048 keys, 8 heads: 60, three 62, one 55.)
+  // SM 55, with one 62. 32 x 2048 keys, 8 heads: 60, three 62, one 55.) Queries of more than a tile
+  // go on below, where a sequence's keys are one CTA's: 25 tokens of 40 heads over 8, contexts of up to
+  // 16384 keys of any length, 87 us (4.9 TB/s), 26 such tokens 168 (2.4); of 4096 keys each 79 and 95.
   if (d.Tq <= f.tok) {
     const int64_t rows = d.Tq / d.sequences * f.pack;
     const int64_t chunk = std::max<int64_t>({4, rows / 16, (keys * heads + 303) / 304});
