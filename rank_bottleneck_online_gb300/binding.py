@@ -913,7 +913,7 @@ def grad_clip(grads, max_norm, ws: Workspace, *, outs=None, norm=None, stream=No
     """The norm over all gradients (float32 [1], on the device), and each scaled in place by
     min(1, max_norm / (norm + 1e-6)), or into ``outs``, each of its gradient's type and number of
     values. max_norm None: the norm alone. Gradients are contiguous, bfloat16 or float32, of any
-    number, sizes and shapes."""
+    number, sizes and shapes, at addresses that are multiples of 16 bytes."""
     device = _device()
     grads = list(grads)
     outs = grads if outs is None else list(outs)
